@@ -10,7 +10,9 @@ Entry points (same names as the C ABI): ``gdn_conv``, ``gdn_seq``,
 ``gdn_chunk_prefill``, ``gdn_chunk_prefill_noalloc``, ``gdn_page_to_slots``, ``gdn_slots_to_page``,
 ``gdn_chunk_prefill_workspace_bytes``, ``gdn_page_layout``,
 ``gdn_slot_layout``, ``gdn_check_bounded_wait``, ``gdn_strerror``,
-``gdn_abi_version``.
+``gdn_abi_version``; for the attention layers between GDN layers ``gdn_rope``,
+``gdn_kv_append``, ``gdn_attn_plan``, ``gdn_attn``, ``gdn_attn_plan_bytes``,
+``gdn_attn_workspace_bytes``.
 """
 from __future__ import annotations
 
@@ -23,6 +25,7 @@ LIB_PATH = os.path.join(PKG_DIR, "libgdn.so")
 
 GDN_F32 = 0
 GDN_BF16 = 1
+GDN_F16 = 2
 GDN_REQ_FRESH = 0x1
 GDN_REQ_SPEC = 0x2
 GDN_REQ_PARITY = 0x4
@@ -81,6 +84,28 @@ class SlotLayout(ctypes.Structure):
                 ("state_offset", ctypes.c_size_t), ("window_offset", ctypes.c_size_t)]
 
 
+class AttnDims(ctypes.Structure):
+    _fields_ = [("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class RopeParams(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("num_axes", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("inv_freq", ctypes.c_void_p),
+                ("axis", ctypes.c_void_p), ("positions", ctypes.c_void_p)]
+
+
+class KvBatch(ctypes.Structure):
+    _fields_ = [("num_requests", ctypes.c_int32), ("num_rows", ctypes.c_int32),
+                ("max_rows", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("num_groups", ctypes.c_int32),
+                ("row_start", ctypes.c_void_p), ("row_len", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("group_start", ctypes.c_void_p), ("group_len", ctypes.c_void_p),
+                ("group_pages", ctypes.c_void_p)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -97,6 +122,9 @@ def load_library(path: str = LIB_PATH):
         lib = ctypes.CDLL(path)
         P, I, S = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
         D, B, PR = ctypes.POINTER(Dims), ctypes.POINTER(Batch), ctypes.POINTER(Params)
+        AD, KB, RP = (ctypes.POINTER(AttnDims), ctypes.POINTER(KvBatch),
+                      ctypes.POINTER(RopeParams))
+        L = ctypes.c_int64
         sig = {
             "gdn_page_layout": ([D, ctypes.POINTER(PageLayout)], I),
             "gdn_slot_layout": ([D, ctypes.POINTER(SlotLayout)], I),
@@ -113,6 +141,12 @@ def load_library(path: str = LIB_PATH):
             "gdn_chunk_prefill": ([D, B, PR, P, P, P, P, P, P, S, P, P], I),
             "gdn_chunk_prefill_noalloc": ([D, B, PR, P, P, P, P, P, P, P], I),
             "gdn_check_bounded_wait": ([ctypes.c_int64, P, P], I),
+            "gdn_rope": ([AD, RP, I, P, L, P, L, P, L, P, L, I, P], I),
+            "gdn_kv_append": ([AD, KB, RP, P, L, P, L, P, L, P, L, P, P, P, P], I),
+            "gdn_attn_plan_bytes": ([AD, KB], S),
+            "gdn_attn_workspace_bytes": ([AD, KB], S),
+            "gdn_attn_plan": ([AD, KB, P, S, P, P], I),
+            "gdn_attn": ([AD, KB, P, P, L, P, P, P, P, P, S, P, P], I),
             "gdn_strerror": ([I], ctypes.c_char_p),
             "gdn_abi_version": ([], I),
         }
@@ -261,6 +295,76 @@ def gdn_chunk_prefill_noalloc(dims, batch, params, qkv, a, b, o, pages, status, 
                                                     _ptr(b), _ptr(o), _ptr(pages), _ptr(status),
                                                     _stream(stream)),
            "gdn_chunk_prefill_noalloc")
+
+
+def make_attn_dims(Hq, Hkv, D, page_size, io=GDN_BF16, scale=0.0) -> AttnDims:
+    return AttnDims(Hq, Hkv, D, page_size, io, float(scale))
+
+
+def make_rope(rotary_dim, inv_freq, positions, axis=None, interleaved=False) -> RopeParams:
+    """positions: device int32 [rows] or [axes][rows]; axis: device int32 [rotary_dim / 2]."""
+    axes = 1 if positions is None or positions.dim() == 1 else positions.shape[0]
+    return RopeParams(int(rotary_dim), int(axes), int(interleaved), _ptr(inv_freq), _ptr(axis),
+                      _ptr(positions))
+
+
+def make_kv_batch(num_requests, num_rows, max_rows, num_pages, row_start, row_len, kv_len,
+                  page_table, group_start=None, group_len=None, group_pages=None) -> KvBatch:
+    """Row map over a paged cache from device int32 tensors; page_table [requests][pages]."""
+    return KvBatch(int(num_requests), int(num_rows), int(max_rows), int(num_pages),
+                   0 if page_table is None else int(page_table.shape[1]),
+                   0 if group_start is None else int(group_start.numel()), _ptr(row_start),
+                   _ptr(row_len), _ptr(kv_len), _ptr(page_table), _ptr(group_start),
+                   _ptr(group_len), _ptr(group_pages))
+
+
+def _rows(t):
+    """(address, elements between rows) of a [rows][heads][dim] tensor whose heads are
+    contiguous within a row, e.g. a slice of a projection's output."""
+    if t is None:
+        return None, 0
+    heads, dim = t.shape[1], t.shape[2]
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise GdnError(CODES["GDN_ERR_INVALID_ARG"], "row tensor: heads not contiguous")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else heads * dim)
+
+
+def gdn_rope(dims, rope, q, q_out, k=None, k_out=None, inverse=False, stream=None):
+    rows = (q if q is not None else k).shape[0]
+    _check(load_library().gdn_rope(ctypes.byref(dims), ctypes.byref(rope), rows, *_rows(q),
+                                   *_rows(q_out), *_rows(k), *_rows(k_out), int(inverse),
+                                   _stream(stream)), "gdn_rope")
+
+
+def gdn_kv_append(dims, batch, rope, q, k, v, q_out, k_cache, v_cache, status, stream=None):
+    _check(load_library().gdn_kv_append(ctypes.byref(dims), ctypes.byref(batch),
+                                        None if rope is None else ctypes.byref(rope), *_rows(q),
+                                        *_rows(k), *_rows(v), *_rows(q_out), _ptr(k_cache),
+                                        _ptr(v_cache), _ptr(status), _stream(stream)),
+           "gdn_kv_append")
+
+
+def gdn_attn_plan_bytes(dims, batch) -> int:
+    return int(load_library().gdn_attn_plan_bytes(ctypes.byref(dims), ctypes.byref(batch)))
+
+
+def gdn_attn_workspace_bytes(dims, batch) -> int:
+    return int(load_library().gdn_attn_workspace_bytes(ctypes.byref(dims), ctypes.byref(batch)))
+
+
+def gdn_attn_plan(dims, batch, plan, plan_bytes, status, stream=None):
+    _check(load_library().gdn_attn_plan(ctypes.byref(dims), ctypes.byref(batch), _ptr(plan),
+                                        int(plan_bytes), _ptr(status), _stream(stream)),
+           "gdn_attn_plan")
+
+
+def gdn_attn(dims, batch, plan, q, k_cache, v_cache, o, lse, workspace, workspace_bytes, status,
+             stream=None):
+    q_ptr, q_stride = _rows(q)
+    _check(load_library().gdn_attn(ctypes.byref(dims), ctypes.byref(batch), _ptr(plan), q_ptr,
+                                   q_stride, _ptr(k_cache), _ptr(v_cache), _ptr(o), _ptr(lse),
+                                   _ptr(workspace), int(workspace_bytes), _ptr(status),
+                                   _stream(stream)), "gdn_attn")
 
 
 def gdn_check_bounded_wait(limit_ns, status, stream=None):

@@ -98,7 +98,9 @@ typedef enum {
                                  results are not written)                    */
 } gdn_status;
 
-typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
+/* GDN_F16 is a type of the attention-layer calls only (gdn_rope, gdn_kv_append,
+ * gdn_attn); the GDN calls take GDN_F32 and GDN_BF16. */
+typedef enum { GDN_F32 = 0, GDN_BF16 = 1, GDN_F16 = 2 } gdn_dtype;
 
 /* Shapes and dtypes of one GDN layer. Supported: Dk = Dv in {32, 64, 128},
  * Hv a multiple of Hk, W = 4, 0 <= max_candidates <= 8. */
@@ -457,6 +459,134 @@ gdn_status gdn_prefill(const gdn_dims* dims, const gdn_batch* batch,
  * Returns GDN_ERR_INVALID_ARG for a NULL status or a limit out of range. */
 gdn_status gdn_check_bounded_wait(int64_t limit_ns, int32_t* status,
                                   gdn_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Softmax-attention layers beside the GDN layers (a hybrid stack puts one
+ * after every few GDN layers): rotary positions, a paged key/value cache and
+ * the attention that reads it. Same conventions as above; rows are packed and
+ * addressed through a row map, so the rows of one step serve both kinds of
+ * layer.
+ *
+ *   rows:   q [num_rows][Hq][D], k, v [num_rows][Hkv][D]; consecutive rows lie
+ *           `stride` elements apart (>= heads * D: q, k and v may be slices of
+ *           one projection's output), the heads of a row are contiguous;
+ *   cache:  k_cache, v_cache [num_pages][Hkv][page_size][D], io dtype; token j
+ *           of request r is slot j % page_size of page page_table[r][j / page_size];
+ *   heads:  query head h reads key/value head floor(h * Hkv / Hq).
+ * ------------------------------------------------------------------------- */
+
+typedef struct {
+  int32_t num_q_heads;     /* Hq, a multiple of Hkv                          */
+  int32_t num_kv_heads;    /* Hkv                                            */
+  int32_t head_dim;        /* D                                              */
+  int32_t page_size;       /* tokens per cache page (gdn_rope ignores it)    */
+  int32_t io_dtype;        /* gdn_dtype of q, k, v, the cache and o          */
+  float scale;             /* score scale; <= 0 selects D^-1/2               */
+} gdn_attn_dims;
+
+/* Rotary positions: pair j of a head's first rotary_dim elements turns by the
+ * angle positions[axis[j]][row] * inv_freq[j]. The angle is formed and reduced
+ * to a turn with 48 bits, so far positions lose nothing against near ones. */
+typedef struct {
+  int32_t rotary_dim;        /* even, <= head_dim; the other elements pass through */
+  int32_t num_axes;          /* position axes: 1 for text, 3 for (time, height, width) */
+  int32_t interleaved;       /* pair j is elements (j, j + rotary_dim/2) if 0,
+                                (2j, 2j + 1) if 1                              */
+  const float* inv_freq;     /* device [rotary_dim / 2]                        */
+  const int32_t* axis;       /* device [rotary_dim / 2], values in [0, num_axes)
+                                (others count as 0), or NULL: every pair on axis 0 */
+  const int32_t* positions;  /* device [num_axes][num_rows]                    */
+} gdn_rope_params;
+
+/* The row map of one step over a paged cache. Groups declare which requests
+ * share leading pages: the first group_pages[g] entries of page_table are the
+ * same for the requests group_start[g] .. + group_len[g] - 1. Results do not
+ * depend on the groups (up to the order of additions); keys that are declared
+ * shared are read once for the group instead of once per request. Groups do
+ * not overlap. */
+typedef struct {
+  int32_t num_requests;        /* R                                            */
+  int32_t num_rows;            /* rows in the packed q/k/v/o buffers           */
+  int32_t max_rows;            /* upper bound on any row_len (host-known)      */
+  int32_t num_pages;           /* pages in the cache                           */
+  int32_t max_pages;           /* entries per request in page_table            */
+  int32_t num_groups;          /* 0: nothing is declared shared                */
+  const int32_t* row_start;    /* device [R]: first packed row of request r    */
+  const int32_t* row_len;      /* device [R]: new rows of request r this step  */
+  const int32_t* kv_len;       /* device [R]: tokens of request r in the cache,
+                                  this step's rows included (row t is token
+                                  kv_len - row_len + t)                        */
+  const int32_t* page_table;   /* device [R][max_pages]                        */
+  const int32_t* group_start;  /* device [num_groups]: first request           */
+  const int32_t* group_len;    /* device [num_groups]: requests                */
+  const int32_t* group_pages;  /* device [num_groups]: shared leading pages    */
+} gdn_kv_batch;
+
+/* Rotate query and key rows: for each pair (x, y) with angle t,
+ *   x' = x cos t - y sin t,   y' = y cos t + x sin t   (t -> -t if inverse != 0),
+ * in fp32 (any io dtype), rounded once. The inverse is the transpose, so it
+ * is also the gradient: it takes dL/dx' to dL/dx. q or k may be NULL (then so
+ * is its output). An output may be its input (same stride) or must not
+ * overlap it. Strides are in elements. One launch on `stream`; rope->positions
+ * has num_rows entries per axis. D and rotary_dim even, D <= 1024; any
+ * alignment (16-byte aligned rows run fastest). */
+gdn_status gdn_rope(const gdn_attn_dims* dims, const gdn_rope_params* rope, int32_t num_rows,
+                    const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                    const void* k, int64_t k_stride, void* k_out, int64_t k_out_stride,
+                    int32_t inverse, gdn_stream_t stream);
+
+/* Append a step's rows to the paged cache: row t of request r becomes token
+ * kv_len[r] - row_len[r] + t; k is rotated as by gdn_rope and v copied. With q
+ * (else NULL, as q_out) the query rows are rotated to q_out in the same
+ * launch. rope NULL: nothing is rotated (q must be NULL). The groups of the
+ * batch are not read: no page that is written may be shared.
+ * D in {64, 128, 256}, page_size a power of two in [16, 256], io dtype bf16 or
+ * fp16. Device errors, request skipped: GDN_DEV_BAD_ROWS (row range, kv_len <
+ * row_len or kv_len > max_pages * page_size); GDN_DEV_BAD_PAGE: a row whose
+ * page index is out of range is not written (its q_out is). */
+gdn_status gdn_kv_append(const gdn_attn_dims* dims, const gdn_kv_batch* batch,
+                         const gdn_rope_params* rope, const void* q, int64_t q_stride,
+                         const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                         void* q_out, int64_t q_out_stride, void* k_cache, void* v_cache,
+                         int32_t* status, gdn_stream_t stream);
+
+/* Bytes of the plan and of the workspace of gdn_attn for this batch (host
+ * only, from the host-known bounds). 0 when the shape is not supported. */
+size_t gdn_attn_plan_bytes(const gdn_attn_dims* dims, const gdn_kv_batch* batch);
+size_t gdn_attn_workspace_bytes(const gdn_attn_dims* dims, const gdn_kv_batch* batch);
+
+/* Plan a step's attention: reads row_start, row_len, kv_len and the groups on
+ * the device and writes the work of every CTA to `plan` (device, 16-byte
+ * aligned, at least gdn_attn_plan_bytes). The plan holds for every gdn_attn
+ * call with these dims, counts and lengths, e.g. for all attention layers of
+ * the step; it does not hold page indexes, rows or cache contents. One launch
+ * on `stream`. Device error, request skipped: GDN_DEV_BAD_ROWS. */
+gdn_status gdn_attn_plan(const gdn_attn_dims* dims, const gdn_kv_batch* batch, void* plan,
+                         size_t plan_bytes, int32_t* status, gdn_stream_t stream);
+
+/* Causal attention of the step's query rows over the paged cache: with s_j =
+ * scale q.k_j over the tokens j <= kv_len[r] - row_len[r] + t that row t of
+ * request r sees,
+ *   o = sum_j e^{s_j} v_j / sum_j e^{s_j},   lse = log sum_j e^{s_j}.
+ * (kv_len >= row_len, so every row sees at least its own token.) Scores,
+ * softmax statistics and sums are fp32; the probabilities are rounded to the
+ * io dtype for the tensor-core product with v.
+ *   plan       as written by gdn_attn_plan for this step
+ *   q          device rows, 16-byte aligned, q_stride a multiple of 8 (else
+ *              GDN_ERR_UNSUPPORTED)
+ *   o          device [num_rows][Hq][D] io dtype, 16-byte aligned
+ *   lse        device [num_rows][Hq] fp32 (natural logarithm) or NULL
+ *   workspace  device, 16-byte aligned, at least gdn_attn_workspace_bytes;
+ *              overwritten, in use until the launches complete
+ * Cache slots past a request's kv_len are never used, whatever they hold.
+ * D in {64, 128, 256}, page_size a power of two in [16, 256], bf16 or fp16,
+ * Hq / Hkv <= 128. Rows of no request are not written. Device error:
+ * GDN_DEV_BAD_PAGE (a page index out of range: the outputs of that request are
+ * undefined, the others complete), GDN_DEV_TIMEOUT. */
+gdn_status gdn_attn(const gdn_attn_dims* dims, const gdn_kv_batch* batch, const void* plan,
+                    const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                    void* o, float* lse, void* workspace, size_t workspace_bytes,
+                    int32_t* status, gdn_stream_t stream);
 
 /* Text for a status code (host, static storage). */
 const char* gdn_strerror(int32_t status);
