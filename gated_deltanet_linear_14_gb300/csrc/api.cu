@@ -281,6 +281,25 @@ gdn_status encode_rows_tmap(CUtensorMap* tm, const void* rows, int num_rows, con
   return r == CUDA_SUCCESS ? GDN_OK : GDN_ERR_UNSUPPORTED;
 }
 
+}  // namespace
+
+gdn_status gdn::encode_cache_tmap(void* tmap, const void* cache, int D, int tokens, int pages,
+                                  int box_tokens) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tmap_encoder();
+  if (!enc) return GDN_ERR_NO_DEVICE;
+  cuuint64_t gdim[3] = {(cuuint64_t)D, (cuuint64_t)tokens, (cuuint64_t)pages};
+  cuuint64_t gstride[2] = {(cuuint64_t)D * 2, (cuuint64_t)tokens * D * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_tokens, 1};
+  cuuint32_t estride[3] = {1, 1, 1};
+  const CUresult r = enc((CUtensorMap*)tmap, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3,
+                         const_cast<void*>(cache), gdim, gstride, box, estride,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? GDN_OK : GDN_ERR_UNSUPPORTED;
+}
+
+namespace {
+
 gdn_status handover_entry(int dir, const gdn_dims* dims, int32_t n, const int32_t* page,
                           const int32_t* pool, const int32_t* slot, int32_t num_pages,
                           int32_t num_pools, void* pages, void* slots, int32_t* status,

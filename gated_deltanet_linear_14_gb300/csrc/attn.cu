@@ -1,83 +1,575 @@
-// Causal attention of a step's rows over a paged cache (sm_103a), the plain
-// form: one block per (request, row, query head), each of its four warps
-// walks every fourth key with its own running maximum m and sum l,
-//   m' = max(m, s),  l' = l e^{m-m'} + e^{s-m'},  o' = o e^{m-m'} + e^{s-m'} v,
-// and the four are joined at the end. A lane holds D / 32 elements of q and o.
-#include "attn.cuh"
+// Causal attention of a step's rows over a paged cache, on the tcgen05 tensor
+// cores (sm_103a).
+//
+// An item (attn_plan.cuh) is a tile Q of 128 (row, query head) pairs of one
+// key/value head and a range of keys. One pass over the keys, 128 at a time:
+//   S = Q K^T                               (tensor cores, fp32 in TMEM)
+//   m' = max(m, max_j s_j),  p_j = 2^{c (s_j - m')},  c = scale log2 e
+//   l = l 2^{c (m - m')} + sum_j p_j,   O = O 2^{c (m - m')} + P V
+// P goes back to TMEM in the io type, where the second product reads it as
+// its A operand; O stays in TMEM. o = O / l at the end, or (m, l, O) to the
+// workspace where the item goes on in another CTA or is joined with another.
+//
+// Roles: warps 0-3 softmax, one (row, head) pair a thread (its TMEM lane, so
+// that no statistic crosses lanes); warp 4 fetches keys and values by TMA, a
+// box per page; warp 5 issues the MMAs. The ring between them holds units of
+// 128 keys x 64 elements (16 KB), K and V alike, in the order in which the
+// MMAs use them: nothing is resident but Q.
+//
+// D <= 128 runs two CTAs per SM (256 TMEM columns each): one's softmax covers
+// the other's products, so one score buffer each is enough. D = 256 has one
+// CTA per SM with two score buffers, the next tile's scores being formed while
+// this tile's softmax runs.
+#include <cuda.h>
+
+#include <type_traits>
+
+#include "attn_plan.cuh"
 #include "kernels.h"
+#include "umma.cuh"
 
 namespace gdn {
 
-template <class T, int D>
-__global__ void __launch_bounds__(128)
-attn_kernel(AttnDims A, KvBatch B, const T* q, long long qs, const T* kc, const T* vc, T* o,
-            float* lse, int32_t* status) {
-  constexpr int E = D / 32;
-  pdl_begin();
-  const int r = blockIdx.y, t = blockIdx.x / A.Hq, h = blockIdx.x % A.Hq;
-  const int start = B.row_start[r], len = B.row_len[r], kv = B.kv_len[r];
-  if (!kv_request_ok(B, A.ps, start, len, kv)) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) report(status, GDN_DEV_BAD_ROWS);
-    return;
+using namespace umma;
+
+namespace {
+
+constexpr int kSoftmaxWarps = 4;
+constexpr int kAttnThreads = 32 * (kSoftmaxWarps + 2);
+constexpr uint32_t kUnit = kAttnKeys * 128;  // bytes of a ring unit
+// The running maximum is raised only when a score exceeds it by more than
+// this (in powers of two): until then p grows up to 2^8, harmless in fp32 sums
+// and in a bf16 or fp16 P, and O need not be rescaled.
+constexpr float kRaise = 8.0f;
+
+template <int D>
+struct Cfg {
+  static constexpr int NC = D / 64;                    // 64-element chunks of a head
+  static constexpr int NSB = D == 256 ? 2 : 1;         // score buffers
+  static constexpr int NS = D == 64 ? 6 : D == 128 ? 5 : 10;  // ring units
+  static constexpr int CTAS = D == 256 ? 1 : 2;
+  static constexpr uint32_t TM_COLS = D == 256 ? 512 : 256;
+  static constexpr uint32_t TM_O = NSB * 128;
+  static constexpr uint32_t RING = NC * kUnit;
+  static constexpr uint32_t BARS = RING + NS * kUnit;
+  static constexpr uint32_t BYTES = BARS + 8 * (2 * NS + 7) + 16;
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"((uint64_t)tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// D += A B with A (128 x 16, 16-bit, two elements a column) in TMEM.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 32 columns of this thread's lane, in flight until tm_wait32 returns them.
+struct Cols {
+  uint32_t r[32];
+};
+__device__ __forceinline__ void tm_load32(uint32_t taddr, Cols& c) {
+  uint32_t* r = c.r;
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tm_wait32(Cols& c) {
+  uint32_t* r = c.r;
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])::"memory");
+}
+__device__ __forceinline__ void tm_store16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Instruction descriptor: io type x io type -> fp32, 128 x N.
+template <class T>
+__device__ __forceinline__ constexpr uint32_t idesc(int N, int b_mn_major) {
+  return (1u << 4) | (std::is_same<T, bf16>::value ? (1u << 7) | (1u << 10) : 0u) |
+         ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+// Whether any of four words holds an infinite or NaN 16-bit value.
+template <class T>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  constexpr uint32_t E = std::is_same<T, bf16>::value ? 0x7F80u : 0x7C00u;
+  return (((w & E) == E) ? 0xFFFFu : 0u) | (((w >> 16 & E) == E) ? 0xFFFF0000u : 0u);
+}
+
+// The items of one CTA, walked alike by every role.
+struct Walk {
+  const AttnPlan& P;
+  int Hkv, G, c, q, Q, item, head;
+  unsigned long long share, off;
+  AttnItem it;
+  int t0, t1;
+
+  __device__ __forceinline__ Walk(const AttnPlan& P_, const AttnDims& A)
+      : P(P_), Hkv(A.Hkv), G(A.G), c(blockIdx.x) {
+    share = P.head->share;
+    Q = P.head->items * Hkv;
+    q = P.qfirst[c];
+    // the item that holds the start of the share; if an item starts right
+    // there or the previous one ended before it, q is already that one
+    item = q / Hkv;
+    head = q - item * Hkv;
+    --head;
+    --q;
   }
-  if (t >= len) return;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, hk = h / A.G;
-  float qv[E], acc[E], m = -INFINITY, l = 0.0f;
-  for (int e = 0; e < E; ++e) {
-    qv[e] = elem_to_f(q[(long long)(start + t) * qs + h * D + lane * E + e]);
-    acc[e] = 0.0f;
-  }
-  for (int j = w; j < kv - len + t + 1; j += 4) {
-    const int page = B.table[(size_t)r * B.max_pages + (j >> A.ps_log2)];
-    if (page < 0 || page >= B.num_pages) {
-      if (lane == 0) report(status, GDN_DEV_BAD_PAGE);
-      continue;
+  __device__ __forceinline__ bool next() {
+    while (true) {
+      ++q;
+      if (++head == Hkv) head = 0, ++item;
+      if (q >= Q) return false;
+      it = P.items[item];
+      off = it.off + (unsigned long long)head * it.cost;
+      if (off >= (unsigned long long)(c + 1) * share) return false;
+      piece_tiles(it, off, share, c, t0, t1);
+      if (t0 < t1) return true;
     }
-    const size_t off = (((size_t)page * A.Hkv + hk) * A.ps + (j & (A.ps - 1))) * D + lane * E;
-    float s = 0.0f;
-    for (int e = 0; e < E; ++e) s += qv[e] * elem_to_f(kc[off + e]);
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
-    s *= A.scale;
-    const float mn = fmaxf(m, s), c = m == mn ? 1.0f : expf(m - mn);
-    const float p = s == -INFINITY ? 0.0f : expf(s - mn);
-    l = l * c + p;
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * c + p * elem_to_f(vc[off + e]);
-    m = mn;
   }
-  __shared__ float sm[4], sl[4], so[4][D];
-  if (lane == 0) sm[w] = m, sl[w] = l;
-  for (int e = 0; e < E; ++e) so[w][lane * E + e] = acc[e];
+  __device__ __forceinline__ bool split() const {
+    return off / share != (off + it.cost - 1) / share;
+  }
+};
+
+}  // namespace
+
+template <class T, int D>
+__global__ void __launch_bounds__(kAttnThreads, Cfg<D>::CTAS)
+attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+            AttnDims A, KvBatch B, AttnPlan P, const T* q, long long qs, const T* vc, T* o,
+            float* lse, float* po, float2* pml, int32_t* status) {
+  using C = Cfg<D>;
+  constexpr int NC = C::NC, NS = C::NS, NSB = C::NSB;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sb = smem_u32(smem), ring = sb + C::RING;
+  const uint32_t full = sb + C::BARS, empty = full + 8 * NS, q_full = empty + 8 * NS;
+  const uint32_t s_full = q_full + 8, p_ready = s_full + 16, o_full = p_ready + 16;
+  volatile uint32_t* words = reinterpret_cast<uint32_t*>(smem + C::BARS + 8 * (2 * NS + 7));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
+    mbar_init(q_full, kSoftmaxWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(p_ready + 8 * i, kSoftmaxWarps);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(o_full + 8 * i, 1);
+    words[1] = words[2] = words[3] = 0;
+    mbar_fence_init();
+  }
+  if (warp == 5) tmem_alloc(smem_u32((const void*)words), C::TM_COLS);
+  tc_fence_before();
   __syncthreads();
-  const float mm = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  float ll = 0.0f, c[4];
-  for (int i = 0; i < 4; ++i) {
-    c[i] = sm[i] == -INFINITY ? 0.0f : expf(sm[i] - mm);
-    ll += c[i] * sl[i];
+  tc_fence_after();
+  const uint32_t tmem = words[0];
+  pdl_begin();
+
+  // A wait that gives up ends its role; words[1] then ends the others.
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    if (words[1]) return false;
+    if (mbar_wait(bar, parity)) return true;
+    words[1] = 1;
+    report(status, GDN_DEV_TIMEOUT);
+    return false;
+  };
+
+  Walk W(P, A);
+  if (warp == 4) {
+    // ------------------------------------------------------------ producer
+    const int br = min(A.ps, kAttnKeys), boxes = kAttnKeys / br;
+    int slot = 0, used = 0;  // used: units issued so far, up to NS
+    uint32_t phase = 0;
+    bool ok = true;
+    while (ok && W.next()) {
+      const int32_t* table = B.table + (size_t)W.it.req * B.max_pages;
+      // this lane's page of tile t (-1: past the keys, or no such box)
+      auto page_of = [&](int t) {
+        const int key = W.it.k0 + t * kAttnKeys + lane * br;
+        if (lane >= boxes || t >= W.t1 || key >= W.it.kend) return -1;
+        const int p = table[key >> A.ps_log2];
+        if (p >= 0 && p < B.num_pages) return p;
+        report(status, GDN_DEV_BAD_PAGE);
+        return 0;
+      };
+      auto emit = [&](const CUtensorMap& tm, int t, int page) {
+        const int key = W.it.k0 + t * kAttnKeys + lane * br;
+        const int n = __popc(__ballot_sync(~0u, page >= 0));
+        for (int c = 0; c < NC && ok; ++c) {
+          ok = wait(empty + 8 * slot, phase ^ 1);
+          ok = __all_sync(~0u, ok);
+          if (!ok) return;
+          if (lane == 0) mbar_expect_tx(full + 8 * slot, n * br * 128);
+          __syncwarp();
+          if (page >= 0)
+            tma_load_3d(ring + slot * kUnit + lane * br * 128, &tm, c * 64,
+                        W.head * A.ps + (key & (A.ps - 1)), page, full + 8 * slot);
+          if (++slot == NS) slot = 0, phase ^= 1;
+          used = min(used + 1, NS);
+        }
+      };
+      int cur = page_of(W.t0), nxt = page_of(W.t0 + 1);
+      emit(tk, W.t0, cur);
+      for (int t = W.t0; ok && t < W.t1; ++t) {
+        const int after = page_of(t + 2);
+        if (NSB == 2 && t + 1 < W.t1) emit(tk, t + 1, nxt);
+        emit(tv, t, cur);
+        if (NSB == 1 && t + 1 < W.t1) emit(tk, t + 1, nxt);
+        cur = nxt, nxt = after;
+      }
+    }
+    if (!ok) {  // gave up: let the copies in flight land
+      for (int i = 0; i < used; ++i) {
+        if (--slot < 0) slot = NS - 1, phase ^= 1;
+        mbar_wait(full + 8 * slot, phase);
+      }
+    }
+  } else if (warp == 5) {
+    // ----------------------------------------------------------------- MMA
+    if (lane == 0) {
+      int slot = 0, g = 0;  // g: tiles so far
+      uint32_t phase = 0, items = 0;
+      bool ok = true;
+      const uint32_t id_s = idesc<T>(128, 0), id_o = idesc<T>(64, 1);
+      auto advance = [&]() {
+        mma_commit(empty + 8 * slot);
+        if (++slot == NS) slot = 0, phase ^= 1;
+      };
+      auto scores = [&](int b) {
+        for (int c = 0; c < NC; ++c) {
+          if (!(ok = wait(full + 8 * slot, phase))) return;
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_bf16(tmem + 128 * b, sdesc(sb + c * kUnit + ks * 32, 16, 1024),
+                     sdesc(ring + slot * kUnit + ks * 32, 16, 1024), id_s, (c | ks) != 0);
+          advance();
+        }
+        mma_commit(s_full + 8 * b);
+      };
+      auto values = [&](int b, bool first) {
+        for (int c = 0; c < NC; ++c) {
+          if (!(ok = wait(full + 8 * slot, phase))) return;
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            mma_ts(tmem + C::TM_O + 64 * c, tmem + 128 * b + 8 * ks,
+                   sdesc(ring + slot * kUnit + ks * 2048, 16, 1024), id_o, !(first && ks == 0));
+          advance();
+        }
+        mma_commit(o_full + 8 * b);
+      };
+      while (ok && W.next()) {
+        if (!(ok = wait(q_full, items++ & 1))) break;
+        tc_fence_after();
+        if (NSB == 2) scores(g & 1);
+        for (int t = W.t0; ok && t < W.t1; ++t, ++g) {
+          if (NSB == 1) scores(0);
+          else if (t + 1 < W.t1) scores((g + 1) & 1);
+          if (!ok) break;
+          const int b = NSB == 2 ? g & 1 : 0;
+          if (!(ok = wait(p_ready + 8 * b, (NSB == 2 ? g >> 1 : g) & 1))) break;
+          tc_fence_after();
+          values(b, t == W.t0);
+        }
+      }
+      if (!ok) {  // gave up: give the issued MMAs a millisecond to finish
+        const uint64_t t = global_ns();
+        for (int i = 0; i < 1000 && global_ns() - t < 1000000; ++i) __nanosleep(1000);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- softmax
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    const float c2 = A.scale * 1.44269504088896341f;
+    int g = 0;
+    uint32_t units = 0, items = 0;  // ring units and items before this one
+    bool ok = true;
+    // all lanes wait, and go on together
+    auto wait_all = [&](uint32_t bar, uint32_t parity) {
+      return __all_sync(~0u, wait(bar, parity)) != 0;
+    };
+    for (; ok && W.next(); ++items) {
+      const AttnItem& it = W.it;
+      const bool rows_here = it.m_cnt > warp * 32;
+      // this thread's (row, head) pair
+      const int mi = it.m0 + min(tid, it.m_cnt - 1), i = mi / A.G, hq = W.head * A.G + mi - i * A.G;
+      const bool group = it.kind == ITEM_GROUP;
+      const long long row = group ? P.list[it.row_base + i].row : it.row_base + i;
+      const int seen = group ? it.kend : it.vis0 + i;  // keys below this
+      const int first_seen = group ? it.kend : it.vis0 + it.m0 / A.G;
+      const bool mixed = !group && it.m0 / A.G != (it.m0 + it.m_cnt - 1) / A.G;
+
+      if (rows_here) {
+        constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte pieces of a row, rows at once
+        const unsigned long long src = (unsigned long long)(q + row * qs + (long long)hq * D);
+        const int n = min(32, it.m_cnt - warp * 32), ch = lane % CH;
+#pragma unroll 4
+        for (int r0 = 0; r0 < 32; r0 += RPI) {
+          const int r = r0 + lane / CH;
+          const unsigned long long from = __shfl_sync(~0u, src, r);
+          if (r < n) {
+            const uint4 v = *reinterpret_cast<const uint4*>(from + ch * 16);
+            *reinterpret_cast<uint4*>(smem + (ch >> 3) * kUnit +
+                                      sw128_chunk(warp * 32 + r, ch & 7)) = v;
+          }
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+
+      float m = -INFINITY, l = 0.0f;
+      const int tiles = W.t1 - W.t0;
+      for (int t = W.t0; t < W.t1; ++t, ++g) {
+        const int b = NSB == 2 ? g & 1 : 0;
+        const uint32_t ts = tmem + 128 * b + lane_base;
+        const int base = it.k0 + t * kAttnKeys, nv = min(kAttnKeys, it.kend - base);
+        const bool cut = mixed && base + kAttnKeys > first_seen;  // rows see different keys
+        if (!(ok = wait_all(s_full + 8 * b, (NSB == 2 ? g >> 1 : g) & 1))) break;
+        tc_fence_after();
+        // every warp is past the previous item: its flag is the next item's
+        if (t == W.t0 && tid == 0) words[2 + ((items + 1) & 1)] = 0;
+        if (rows_here) {
+          const bool masked = cut || nv < kAttnKeys;
+          const int lim = min(seen, it.kend) - base;
+          Cols x;
+          float mx = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            tm_load32(ts + 32 * j, x);
+            tm_wait32(x);
+            if (masked) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                mx = fmaxf(mx, 32 * j + e < lim ? __uint_as_float(x.r[e]) : -INFINITY);
+            } else {
+              float m4[4] = {mx, mx, mx, mx};
+#pragma unroll
+              for (int e = 0; e < 32; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(x.r[e]));
+              mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            }
+          }
+          if (t == W.t0) {
+            m = mx;
+          } else if (__any_sync(~0u, (mx - m) * c2 > kRaise || (m == -INFINITY && mx > m))) {
+            const float nm = fmaxf(m, mx);
+            const float f = nm == -INFINITY ? 1.0f : ex2((m - nm) * c2);
+            l *= f;
+            m = nm;
+            // O is complete up to the previous tile: with one score buffer these
+            // scores came after its product, with two they did not
+            if (NSB == 2 && !(ok = wait_all(o_full + 8 * (b ^ 1), ((g - 1) >> 1) & 1))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int j = 0; j < D / 32; ++j) {
+              float v[32];
+              tmem_ld32(tmem + C::TM_O + lane_base + 32 * j, v);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] *= f;
+              tmem_st32(tmem + C::TM_O + lane_base + 32 * j, v);
+            }
+          }
+          const float mc = m == -INFINITY ? 0.0f : m * c2;
+          float2 sum = make_float2(0.0f, 0.0f), sum2 = sum;
+          const float2 cc = make_float2(c2, c2), nm2 = make_float2(-mc, -mc);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            tm_load32(ts + 32 * j, x);
+            tm_wait32(x);
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float2 s = make_float2(__uint_as_float(x.r[2 * e]), __uint_as_float(x.r[2 * e + 1]));
+              s = __ffma2_rn(s, cc, nm2);
+              s.x = ex2(s.x);
+              s.y = ex2(s.y);
+              if (masked) {
+                if (32 * j + 2 * e >= lim) s.x = 0.0f;
+                if (32 * j + 2 * e + 1 >= lim) s.y = 0.0f;
+              }
+              if (e & 1) sum2 = __fadd2_rn(sum2, s);
+              else sum = __fadd2_rn(sum, s);
+              p[e] = pack2<T>(s.x, s.y);
+            }
+            tm_store16(ts + 16 * j, p);
+          }
+          l += (sum.x + sum.y) + (sum2.x + sum2.y);
+          tmem_st_wait();
+        }
+        // Value rows past the last key hold whatever was there, and p = 0 does
+        // not silence a NaN: they are zeroed. Where rows see different keys,
+        // infinite and NaN values are zeroed too and added at the end to the
+        // rows that see them.
+        if (cut || nv < kAttnKeys) {
+          // (two score buffers: the ring slots may still belong to the previous
+          // tile's values until its product is complete)
+          if (NSB == 2 && t > W.t0 &&
+              !(ok = wait_all(o_full + 8 * (b ^ 1), ((g - 1) >> 1) & 1)))
+            break;
+          const int j = t - W.t0;
+          const uint32_t at = units + NC * (NSB == 1 ? 2 * j + 1 : min(2 * j + 2, 2 * tiles - 1));
+          for (int c = 0; c < NC && ok; ++c) {
+            const uint32_t u = at + c, s = u % NS;
+            if (!(ok = wait_all(full + 8 * s, (u / NS) & 1))) break;
+            uint4* vrow = reinterpret_cast<uint4*>(smem + C::RING + s * kUnit + tid * 128);
+            for (int k = 0; k < 8; ++k) {
+              uint4& w = vrow[(k + lane) & 7];  // all banks at once
+              if (tid >= nv) {
+                w = make_uint4(0, 0, 0, 0);
+              } else if (cut) {
+                uint4 v = w;
+                const uint4 bad = make_uint4(not_finite<T>(v.x), not_finite<T>(v.y),
+                                             not_finite<T>(v.z), not_finite<T>(v.w));
+                if (bad.x | bad.y | bad.z | bad.w) {
+                  words[2 + (items & 1)] = 1;
+                  w = make_uint4(v.x & ~bad.x, v.y & ~bad.y, v.z & ~bad.z, v.w & ~bad.w);
+                }
+              }
+            }
+          }
+          fence_async_smem();
+          if (!ok) break;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_ready + 8 * b);
+      }
+      if (!ok) break;
+      units += 2 * NC * tiles;
+      const int last = g - 1;
+      if (!(ok = wait_all(o_full + 8 * (NSB == 2 ? last & 1 : 0),
+                          (NSB == 2 ? last >> 1 : last) & 1)))
+        break;
+      tc_fence_after();
+      // whether an infinite or NaN value was taken out of a tile of this item
+      const bool strange = words[2 + (items & 1)] != 0;
+      if (rows_here) {
+        const bool direct = it.kind == ITEM_OWN && !W.split();
+        const bool mine = tid < it.m_cnt;
+        const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+        const long long part =
+            direct || !mine ? 0 : partial_row(P, it, W.head, A.Hq, A.G, W.off, W.share, W.c, tid);
+        T* dst = o + (row * A.Hq + hq) * D;
+        float* pdst = po + part * D;
+#pragma unroll 1
+        for (int j = 0; j < D / 32; ++j) {
+          float v[32];
+          tmem_ld32(tmem + C::TM_O + lane_base + 32 * j, v);
+          if (strange && mine) {
+            // the values that were taken out, of this CTA's tiles in which rows
+            // see different keys
+            int key = it.k0 + W.t0 * kAttnKeys;
+            while (key + kAttnKeys <= first_seen) key += kAttnKeys;
+            for (; key < min(seen, it.k0 + W.t1 * kAttnKeys); ++key) {
+              int page = B.table[(size_t)it.req * B.max_pages + (key >> A.ps_log2)];
+              if (page < 0 || page >= B.num_pages) page = 0;
+              const uint32_t* src = reinterpret_cast<const uint32_t*>(
+                  vc + (((size_t)page * A.Hkv + W.head) * A.ps + (key & (A.ps - 1))) * D + 32 * j);
+              for (int e = 0; e < 16; ++e) {
+                const uint32_t w = src[e], bad = not_finite<T>(w);
+                const uint16_t lo = w & 0xFFFF, hi = w >> 16;
+                if (bad & 0xFFFF) v[2 * e] += elem_to_f(*reinterpret_cast<const T*>(&lo));
+                if (bad >> 16) v[2 * e + 1] += elem_to_f(*reinterpret_cast<const T*>(&hi));
+              }
+            }
+          }
+          if (mine && direct) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = pack2<T>(v[2 * e] * inv, v[2 * e + 1] * inv);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              reinterpret_cast<uint4*>(dst + 32 * j)[e] =
+                  make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+          } else if (mine) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<float4*>(pdst + 32 * j)[e] =
+                  make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          }
+          __syncwarp();
+        }
+        if (mine && direct && lse) lse[row * A.Hq + hq] = m * A.scale + logf(l);
+        if (mine && !direct) pml[part] = make_float2(m * c2, l);
+      }
+      tc_fence_before();
+    }
   }
-  for (int d = threadIdx.x; d < D; d += 128) {
-    float v = 0.0f;
-    for (int i = 0; i < 4; ++i) v += c[i] * so[i][d];
-    elem_from_f(ll == 0.0f ? 0.0f : v / ll, o[((size_t)(start + t) * A.Hq + h) * D + d]);
-  }
-  if (lse && threadIdx.x == 0) lse[(size_t)(start + t) * A.Hq + h] = mm + logf(ll);
+  __syncthreads();
+  if (warp == 5) tmem_dealloc(tmem, C::TM_COLS);
 }
 
 namespace {
-template <class T>
-cudaError_t go(const AttnDims& A, const KvBatch& B, const void* q, long long qs, const void* kc,
-               const void* vc, void* o, float* lse, int32_t* status, cudaStream_t s) {
-  const dim3 grid(B.max_rows * A.Hq, B.R);
-  auto f = A.D == 64 ? attn_kernel<T, 64> : A.D == 128 ? attn_kernel<T, 128> : attn_kernel<T, 256>;
-  return launch_pdl(f, grid, dim3(128), 0, s, A, B, (const T*)q, qs, (const T*)kc, (const T*)vc,
-                    (T*)o, lse, status);
+
+template <class T, int D>
+cudaError_t go(const void* tk, const void* tv, const AttnDims& A, const KvBatch& B, int io,
+               const void* plan, const void* q, long long qs, const void* vc, void* o, float* lse,
+               void* ws, int32_t* status, cudaStream_t s) {
+  constexpr int bytes = Cfg<D>::BYTES;
+  const AttnLayout L = attn_layout(A, B);
+  const AttnPlan P = attn_plan_view(L, B, plan);
+  cudaError_t e = ensure_smem_limit<attn_kernel<T, D>>(bytes);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(attn_kernel<T, D>, dim3(L.ctas), dim3(kAttnThreads), bytes, s,
+                 *(const CUtensorMap*)tk, *(const CUtensorMap*)tv, A, B, P, (const T*)q, qs,
+                 (const T*)vc, (T*)o, lse, (float*)ws, (float2*)((char*)ws + L.ws_ml), status);
+  if (e != cudaSuccess) return e;
+  return launch_attn_join(A, B, io, plan, ws, o, lse, s);
 }
+
 }  // namespace
 
-cudaError_t launch_attn(const AttnDims& A, const KvBatch& B, int io, const void* q, long long qs,
-                        const void* kc, const void* vc, void* o, float* lse, int32_t* status,
-                        cudaStream_t s) {
-  return io == GDN_BF16 ? go<bf16>(A, B, q, qs, kc, vc, o, lse, status, s)
-                        : go<__half>(A, B, q, qs, kc, vc, o, lse, status, s);
+cudaError_t launch_attn(const void* tk, const void* tv, const AttnDims& A, const KvBatch& B,
+                        int io, const void* plan, const void* q, long long qs, const void* vc,
+                        void* o, float* lse, void* ws, int32_t* status, cudaStream_t s) {
+  auto by_type = [&](auto t) {
+    using T = decltype(t);
+    if (A.D == 64) return go<T, 64>(tk, tv, A, B, io, plan, q, qs, vc, o, lse, ws, status, s);
+    if (A.D == 128) return go<T, 128>(tk, tv, A, B, io, plan, q, qs, vc, o, lse, ws, status, s);
+    return go<T, 256>(tk, tv, A, B, io, plan, q, qs, vc, o, lse, ws, status, s);
+  };
+  return io == GDN_BF16 ? by_type(bf16()) : by_type(__half());
 }
 
 }  // namespace gdn

@@ -1,5 +1,5 @@
 // Shapes, types and row helpers of the attention-layer kernels (rope.cu,
-// attn.cu, attn_plan.cu).
+// attn_plan.cu, attn.cu).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -97,9 +97,5 @@ struct RopeCall {
 cudaError_t launch_rope(const RopeCall& C, const Rope& P, cudaStream_t s);
 cudaError_t launch_kv_append(const RopeCall& C, const Rope& P, const AttnDims& A, const KvBatch& B,
                              int32_t* status, cudaStream_t s);
-
-cudaError_t launch_attn(const AttnDims& A, const KvBatch& B, int io, const void* q, long long qs,
-                        const void* kc, const void* vc, void* o, float* lse, int32_t* status,
-                        cudaStream_t s);
 
 }  // namespace gdn

@@ -1,8 +1,10 @@
 // C ABI of the attention-layer calls: host-side validation and launches. As
 // in api.cu, a negative return means nothing was launched and nothing written.
+#include <cuda.h>
+
 #include <cmath>
 
-#include "attn.cuh"
+#include "attn_plan.cuh"
 #include "gdn.h"
 #include "kernels.h"
 
@@ -209,12 +211,12 @@ gdn_status gdn_kv_append(const gdn_attn_dims* dims, const gdn_kv_batch* batch,
 
 size_t gdn_attn_plan_bytes(const gdn_attn_dims* dims, const gdn_kv_batch* batch) {
   if (check_attn(dims) != GDN_OK || check_kv_batch(batch, true) != GDN_OK) return 0;
-  return 16;
+  return attn_layout(attn_dims(dims), kv_batch(batch)).bytes;
 }
 
 size_t gdn_attn_workspace_bytes(const gdn_attn_dims* dims, const gdn_kv_batch* batch) {
   if (check_attn(dims) != GDN_OK || check_kv_batch(batch, true) != GDN_OK) return 0;
-  return 16;
+  return attn_layout(attn_dims(dims), kv_batch(batch)).ws_bytes;
 }
 
 gdn_status gdn_attn_plan(const gdn_attn_dims* dims, const gdn_kv_batch* batch, void* plan,
@@ -224,8 +226,10 @@ gdn_status gdn_attn_plan(const gdn_attn_dims* dims, const gdn_kv_batch* batch, v
   if ((e = check_kv_batch(batch, true)) != GDN_OK) return e;
   if (!plan || !status || ((uintptr_t)plan & 15) != 0) return GDN_ERR_INVALID_ARG;
   if (plan_bytes < gdn_attn_plan_bytes(dims, batch)) return GDN_ERR_WORKSPACE;
-  (void)stream;
-  return GDN_OK;
+  return launch_attn_plan(attn_dims(dims), kv_batch(batch), plan, status, (cudaStream_t)stream) ==
+                 cudaSuccess
+             ? GDN_OK
+             : GDN_ERR_LAUNCH;
 }
 
 gdn_status gdn_attn(const gdn_attn_dims* dims, const gdn_kv_batch* batch, const void* plan,
@@ -244,8 +248,15 @@ gdn_status gdn_attn(const gdn_attn_dims* dims, const gdn_kv_batch* batch, const 
       q_stride % 8 != 0)
     return GDN_ERR_UNSUPPORTED;
   if (workspace_bytes < gdn_attn_workspace_bytes(dims, batch)) return GDN_ERR_WORKSPACE;
-  return launch_attn(attn_dims(dims), kv_batch(batch), dims->io_dtype, q, q_stride, k_cache,
-                     v_cache, o, lse, status, (cudaStream_t)stream) == cudaSuccess
+  if (batch->num_pages == 0) return GDN_ERR_INVALID_ARG;
+  const AttnDims A = attn_dims(dims);
+  const int box = A.ps < kAttnKeys ? A.ps : kAttnKeys;
+  CUtensorMap tk, tv;
+  if ((e = encode_cache_tmap(&tk, k_cache, A.D, A.Hkv * A.ps, batch->num_pages, box)) != GDN_OK ||
+      (e = encode_cache_tmap(&tv, v_cache, A.D, A.Hkv * A.ps, batch->num_pages, box)) != GDN_OK)
+    return e;
+  return launch_attn(&tk, &tv, A, kv_batch(batch), dims->io_dtype, plan, q, q_stride, v_cache, o,
+                     lse, workspace, status, (cudaStream_t)stream) == cudaSuccess
              ? GDN_OK
              : GDN_ERR_LAUNCH;
 }

@@ -1,0 +1,397 @@
+// The plan of a step's attention, and the join of split items (sm_103a). See
+// attn_plan.cuh for what the plan holds.
+#include "attn_plan.cuh"
+#include "kernels.h"
+
+namespace gdn {
+
+constexpr int kPlanThreads = 1024;
+
+int attn_ctas_per_sm(int D) { return D == 256 ? 1 : 2; }
+
+AttnLayout attn_layout(const AttnDims& A, const KvBatch& B) {
+  AttnLayout L{};
+  auto up = [](size_t x) { return (x + 63) & ~(size_t)63; };
+  L.ctas = device_sms() * attn_ctas_per_sm(A.D);
+  L.ents = B.num_groups + B.R;
+  // rows that may join: at most kJoinRows / G per request
+  const long long join = B.num_groups ? (long long)B.R * (kJoinRows / A.G) : 0;
+  L.max_list = (int)(join < B.num_rows ? join : B.num_rows);
+  const long long pairs = (long long)B.num_rows * A.G + (long long)L.max_list * A.G;
+  L.max_items = (int)(pairs / kAttnM + L.ents + 2);
+  size_t at = up(sizeof(AttnHead));
+  L.qfirst = at, at = up(at + 4 * ((size_t)L.ctas + 1));
+  L.items = at, at = up(at + sizeof(AttnItem) * (size_t)L.max_items);
+  L.list = at, at = up(at + sizeof(AttnRow) * (size_t)L.max_list);
+  L.first_item = at, at = up(at + 4 * ((size_t)L.ents + 1));
+  L.k0 = at, at = up(at + 4 * (size_t)B.R);
+  L.req_list = at, at = up(at + 4 * (size_t)B.R);
+  L.g_shared = at, at = up(at + 4 * (size_t)B.num_groups);
+  L.g_rows = at, at = up(at + 4 * (size_t)B.num_groups);
+  L.g_off = at, at = up(at + 4 * (size_t)B.num_groups);
+  L.bytes = at;
+  L.ws_rows = (long long)2 * L.ctas * kAttnM + 2 * (long long)L.max_list * A.Hq;
+  L.ws_ml = (size_t)L.ws_rows * A.D * 4;
+  L.ws_bytes = L.ws_ml + (size_t)L.ws_rows * 8;
+  return L;
+}
+
+// Exclusive prefix sum over the block's threads; `total` is the block's sum.
+template <class T>
+__device__ __forceinline__ T block_scan(T v, T& total, T* sm) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  T x = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const T y = __shfl_up_sync(~0u, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) sm[w] = x;
+  __syncthreads();
+  if (w == 0) {
+    T s = sm[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const T y = __shfl_up_sync(~0u, s, d);
+      if (lane >= d) s += y;
+    }
+    sm[lane] = s;
+  }
+  __syncthreads();
+  total = sm[31];
+  const T excl = x - v + (w ? sm[w - 1] : (T)0);
+  __syncthreads();
+  return excl;
+}
+
+__global__ void __launch_bounds__(kPlanThreads)
+attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* status) {
+  __shared__ unsigned long long scan64[32];
+  __shared__ int scan32[32];
+  pdl_begin();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, NG = B.num_groups;
+  AttnHead* head = (AttnHead*)plan;
+  int32_t* qfirst = (int32_t*)(plan + L.qfirst);
+  AttnItem* items = (AttnItem*)(plan + L.items);
+  AttnRow* list = (AttnRow*)(plan + L.list);
+  int32_t* first_item = (int32_t*)(plan + L.first_item);
+  int32_t* req_k0 = (int32_t*)(plan + L.k0);
+  int32_t* req_list = (int32_t*)(plan + L.req_list);
+  int32_t* g_shared = (int32_t*)(plan + L.g_shared);
+  int32_t* g_rows = (int32_t*)(plan + L.g_rows);
+  int32_t* g_off = (int32_t*)(plan + L.g_off);
+
+  auto valid = [&](int r, int& start, int& len, int& kv) {
+    start = B.row_start[r], len = B.row_len[r], kv = B.kv_len[r];
+    return kv_request_ok(B, A.ps, start, len, kv);
+  };
+  auto joins = [&](int r, int& start, int& len, int& kv) {
+    return valid(r, start, len, kv) && len > 0 && len * A.G <= kJoinRows;
+  };
+
+  for (int r = tid; r < B.R; r += kPlanThreads) {
+    int start, len, kv;
+    if (!valid(r, start, len, kv)) report(status, GDN_DEV_BAD_ROWS);
+    req_k0[r] = 0;
+    req_list[r] = -1;
+  }
+  for (int i = tid; i < L.max_list; i += kPlanThreads) list[i].req = -1;
+  // groups: the keys that every joining member's rows all see, in whole pages
+  for (int g = warp; g < NG; g += kPlanThreads / 32) {
+    const int a = B.group_start[g], n = B.group_len[g];
+    int pages = min(B.group_pages[g], B.max_pages), members = 0, rows = 0, seen = 0x7fffffff;
+    if (a < 0 || n < 0 || (long long)a + n > B.R) {
+      if (lane == 0) report(status, GDN_DEV_BAD_ROWS);
+    } else {
+      for (int i = lane; i < n; i += 32) {
+        int start, len, kv;
+        if (!joins(a + i, start, len, kv)) continue;
+        members += 1, rows += len, seen = min(seen, kv - len);
+      }
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+      members += __shfl_xor_sync(~0u, members, d);
+      rows += __shfl_xor_sync(~0u, rows, d);
+      seen = min(seen, __shfl_xor_sync(~0u, seen, d));
+    }
+    pages = min(pages, seen >> A.ps_log2);
+    if (lane == 0) {
+      const bool on = members >= 2 && pages > 0 && ((long long)pages << A.ps_log2) >= kMinShared;
+      g_shared[g] = on ? pages << A.ps_log2 : 0;
+      g_rows[g] = on ? rows : 0;
+    }
+  }
+  __syncthreads();
+  int list_rows = 0;
+  for (int b = 0; b < NG; b += kPlanThreads) {
+    const int g = b + tid;
+    const int n = g < NG ? g_rows[g] : 0;
+    int total;
+    const int off = list_rows + block_scan(n, total, scan32);
+    if (g < NG) {
+      g_off[g] = off;
+      if ((long long)off + n > L.max_list) g_rows[g] = g_shared[g] = 0;  // groups that overlap
+    }
+    list_rows += total;
+  }
+  __syncthreads();
+  for (int g = warp; g < NG; g += kPlanThreads / 32) {
+    if (g_rows[g] == 0) continue;
+    const int a = B.group_start[g], n = B.group_len[g], off = g_off[g], shared = g_shared[g];
+    int at = 0;
+    for (int b = 0; b < n; b += 32) {
+      int start = 0, len = 0, kv = 0;
+      const int r = a + b + lane;
+      if (b + lane >= n || !joins(r, start, len, kv)) len = 0;
+      int x = len;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(~0u, x, d);
+        if (lane >= d) x += y;
+      }
+      const int pos = at + x - len;
+      if (len > 0) {
+        req_k0[r] = shared;
+        req_list[r] = off + pos;
+        for (int i = 0; i < len; ++i)
+          list[off + pos + i] = AttnRow{start + i, r, g, i * A.G, (pos + i) * A.G, {0, 0, 0}};
+      }
+      at += __shfl_sync(~0u, x, 31);
+    }
+  }
+  __syncthreads();
+  // tiles of 128 pairs: groups first (the long ones), then requests
+  int n_items = 0;
+  for (int b = 0; b < L.ents; b += kPlanThreads) {
+    const int e = b + tid;
+    long long pairs = 0;
+    if (e < NG) {
+      pairs = (long long)g_rows[e] * A.G;
+    } else if (e < L.ents) {
+      int start, len, kv;
+      if (valid(e - NG, start, len, kv)) pairs = (long long)len * A.G;
+    }
+    const int n = (int)((pairs + kAttnM - 1) / kAttnM);
+    int total;
+    const int off = n_items + block_scan(n, total, scan32);
+    if (e < L.ents) first_item[e] = min(off, L.max_items);
+    n_items += total;
+  }
+  // more items than the row counts allow: rows that belong to several requests
+  if (n_items > L.max_items) {
+    if (tid == 0) report(status, GDN_DEV_BAD_ROWS);
+    n_items = L.max_items;
+  }
+  if (tid == 0) first_item[L.ents] = n_items;
+  __syncthreads();
+  unsigned long long at = 0;
+  for (int b = 0; b < n_items; b += kPlanThreads) {
+    const int i = b + tid;
+    AttnItem it{};
+    if (i < n_items) {
+      int lo = 0, hi = L.ents;  // the last entry that starts at or before i
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first_item[mid] <= i) lo = mid;
+        else hi = mid;
+      }
+      it.m0 = (i - first_item[lo]) * kAttnM;
+      if (lo < NG) {
+        it.kind = ITEM_GROUP;
+        it.row_base = g_off[lo];
+        it.m_cnt = min(kAttnM, g_rows[lo] * A.G - it.m0);
+        it.kend = g_shared[lo];
+        it.req = list[it.row_base].req;
+      } else {
+        int start, len, kv;
+        it.req = lo - NG;
+        valid(it.req, start, len, kv);
+        it.m_cnt = (int)min((long long)kAttnM, (long long)len * A.G - it.m0);
+        it.row_base = start;
+        it.vis0 = kv - len + 1;
+        it.list = req_list[it.req];
+        it.kind = it.list >= 0 ? ITEM_JOINED : ITEM_OWN;
+        it.k0 = req_k0[it.req];
+        it.kend = it.vis0 + (it.m0 + it.m_cnt - 1) / A.G;
+      }
+      it.tiles = (it.kend - it.k0 + kAttnKeys - 1) / kAttnKeys;
+      it.cost = it.tiles * kTileCost + kItemCost;
+    }
+    unsigned long long total;
+    it.off = at + block_scan((unsigned long long)it.cost * A.Hkv, total, scan64);
+    if (i < n_items) items[i] = it;
+    at += total;
+  }
+  // equal shares, none below one tile and its item's own cost
+  const unsigned long long share =
+      max((at + L.ctas - 1) / L.ctas, (unsigned long long)(kTileCost + kItemCost));
+  const int Q = n_items * A.Hkv;
+  for (int c = tid; c <= L.ctas; c += kPlanThreads) qfirst[c] = Q;
+  if (tid == 0) *head = AttnHead{share, at, n_items, min(list_rows, L.max_list)};
+  __syncthreads();
+  for (int q = tid; q < Q; q += kPlanThreads) {
+    const int i = q / A.Hkv;
+    const uint32_t cost = items[i].cost;
+    const unsigned long long off = items[i].off + (unsigned long long)(q - i * A.Hkv) * cost;
+    for (unsigned long long c = (off + share - 1) / share; c * share < off + cost; ++c)
+      qfirst[c] = q;
+  }
+}
+
+cudaError_t launch_attn_plan(const AttnDims& A, const KvBatch& B, void* plan, int32_t* status,
+                             cudaStream_t s) {
+  return launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, A, B, attn_layout(A, B),
+                    (char*)plan, status);
+}
+
+// ---------------------------------------------------------------- the join
+//
+// Pieces of a row hold m (the maximum, in base-2 exponent units), l = sum
+// 2^{s - m} and o = sum 2^{s - m} v, so with M = max m
+//   o = sum 2^{m_p - M} o_p / sum 2^{m_p - M} l_p.
+// One warp per (row, query head): the lanes fetch the pieces' m and l at
+// once, then the warp adds up the pieces' o in their order. Blocks
+// [0, 4 ctas) take the items that are cut by a share's end, the others the
+// rows of the list.
+
+constexpr int kJoinWarps = 4;
+
+struct JoinPart {
+  int n, c0;  // pieces, and the CTA of the first
+};
+
+template <class T, int D>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+attn_join_kernel(AttnDims A, AttnPlan P, const float* po, const float2* pml, T* o, float* lse) {
+  constexpr int E = D / 32;
+  pdl_begin();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, Q = P.head->items * A.Hkv;
+  const unsigned long long share = P.head->share;
+  int q1 = -1, q2 = -1, m1 = 0, m2 = 0, row = 0, hq = 0, step = 0, m_end = 0;
+  const int split_blocks = 4 * P.ctas;
+  if ((int)blockIdx.x < split_blocks) {
+    const int c = blockIdx.x >> 2;
+    q1 = P.qfirst[c + 1];  // holds the start of share c + 1
+    if (q1 >= Q) return;
+    const AttnItem& it = P.items[q1 / A.Hkv];
+    const unsigned long long off = it.off + (unsigned long long)(q1 % A.Hkv) * it.cost;
+    // cut there, begun in share c, and not joined with another item
+    if (it.kind != ITEM_OWN || off == (c + 1) * share || off / share != (unsigned long long)c)
+      return;
+    m1 = (blockIdx.x & 3) * kJoinWarps + warp;
+    m_end = it.m_cnt;
+    step = 4 * kJoinWarps;
+  } else {
+    const int idx = (blockIdx.x - split_blocks) * kJoinWarps + warp;
+    const int i = idx / A.Hq;
+    if (i >= P.head->list_rows) return;
+    const AttnRow lr = P.list[i];
+    if (lr.req < 0) return;
+    hq = idx - i * A.Hq;
+    row = lr.row;
+    const int head = hq / A.G, hg = hq - head * A.G;
+    q1 = P.first_item[P.num_groups + lr.req] * A.Hkv + head;
+    m1 = lr.own_m + hg;
+    const int gm = lr.group_m + hg;
+    q2 = (P.first_item[lr.group] + gm / kAttnM) * A.Hkv + head;
+    m2 = gm % kAttnM;
+    m_end = m1 + 1;
+    step = 1;
+  }
+  const AttnItem it1 = P.items[q1 / A.Hkv], it2 = P.items[(q2 < 0 ? q1 : q2) / A.Hkv];
+  const int h1 = q1 % A.Hkv, h2 = q2 < 0 ? 0 : q2 % A.Hkv;
+  const unsigned long long off1 = it1.off + (unsigned long long)h1 * it1.cost;
+  const unsigned long long off2 = it2.off + (unsigned long long)h2 * it2.cost;
+  const JoinPart p1{(int)((off1 + it1.cost - 1) / share - off1 / share) + 1, (int)(off1 / share)};
+  const JoinPart p2{q2 < 0 ? 0 : (int)((off2 + it2.cost - 1) / share - off2 / share) + 1,
+                    (int)(off2 / share)};
+  for (; m1 < m_end; m1 += step) {
+    if (q2 < 0) {
+      const int mi = it1.m0 + m1, i = mi / A.G;
+      row = it1.row_base + i;
+      hq = h1 * A.G + mi - i * A.G;
+    }
+    float top = -INFINITY, sum = 0.0f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    for (int b = 0; b < p1.n + p2.n; b += 32) {
+      const int p = b + lane;
+      long long at = -1;
+      if (p < p1.n + p2.n) {
+        const bool own = p < p1.n;
+        const int c = own ? p1.c0 + p : p2.c0 + p - p1.n;
+        int t0, t1;
+        piece_tiles(own ? it1 : it2, own ? off1 : off2, share, c, t0, t1);
+        if (t0 < t1)
+          at = own ? partial_row(P, it1, h1, A.Hq, A.G, off1, share, c, m1)
+                   : partial_row(P, it2, h2, A.Hq, A.G, off2, share, c, m2);
+      }
+      const float2 ml = at >= 0 ? pml[at] : make_float2(-INFINITY, 0.0f);
+      float mx = ml.x;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
+      const float nt = fmaxf(top, mx), ref = nt == -INFINITY ? 0.0f : nt;
+      const float back = exp2f(top - ref);
+      const float w = at >= 0 ? exp2f(ml.x - ref) : 0.0f;
+      float s = at >= 0 ? w * ml.y : 0.0f;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
+      sum = sum * back + s;
+      top = nt;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= back;
+      const int n = min(32, p1.n + p2.n - b);
+#pragma unroll 4
+      for (int k = 0; k < n; ++k) {
+        const long long from = __shfl_sync(~0u, at, k);
+        const float wk = __shfl_sync(~0u, w, k);
+        if (from < 0) continue;
+        float v[E];
+        const float* src = po + from * D + lane * E;
+        if constexpr (E == 2) {
+          *(float2*)v = *(const float2*)src;
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; e += 4) *(float4*)(v + e) = *(const float4*)(src + e);
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += wk * v[e];
+      }
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+    uint32_t out[E / 2];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) out[e / 2] = pack2<T>(acc[e] * inv, acc[e + 1] * inv);
+    T* dst = o + ((size_t)row * A.Hq + hq) * D + lane * E;
+    if constexpr (E == 2) *(uint32_t*)dst = out[0];
+    else if constexpr (E == 4) *(uint2*)dst = *(uint2*)out;
+    else *(uint4*)dst = *(uint4*)out;
+    if (lse && lane == 0)
+      lse[(size_t)row * A.Hq + hq] = (top + log2f(sum)) * 0.693147180559945309f;
+  }
+}
+
+cudaError_t launch_attn_join(const AttnDims& A, const KvBatch& B, int io, const void* plan,
+                             const void* ws, void* o, float* lse, cudaStream_t s) {
+  const AttnLayout L = attn_layout(A, B);
+  const AttnPlan P = attn_plan_view(L, B, plan);
+  const float* po = (const float*)ws;
+  const float2* pml = (const float2*)((const char*)ws + L.ws_ml);
+  const long long rows = (long long)L.max_list * A.Hq;
+  const dim3 grid((unsigned)(4 * L.ctas + (rows + kJoinWarps - 1) / kJoinWarps));
+  const dim3 block(32 * kJoinWarps);
+  auto go = [&](auto t, auto d) {
+    using T = decltype(t);
+    return launch_pdl(attn_join_kernel<T, decltype(d)::value>, grid, block, 0, s, A, P, po, pml,
+                      (T*)o, lse);
+  };
+  auto by_dim = [&](auto t) {
+    if (A.D == 64) return go(t, std::integral_constant<int, 64>());
+    if (A.D == 128) return go(t, std::integral_constant<int, 128>());
+    return go(t, std::integral_constant<int, 256>());
+  };
+  return io == GDN_BF16 ? by_dim(bf16()) : by_dim(__half());
+}
+
+}  // namespace gdn

@@ -1,0 +1,115 @@
+// The work of a gdn_attn call as gdn_attn_plan writes it: how a step's rows
+// and keys are cut into items, and the items' cost divided over the CTAs.
+//
+// An item is one tile of up to 128 (row, query head) pairs of one key/value
+// head, with the keys they read: of one request (its own keys), or of a group
+// (the keys that its requests share, the rows of all its requests side by
+// side). Items repeat for every key/value head; item q = item * Hkv + head.
+// The items lie end to end on a line of cost (kTileCost per tile of 128 keys,
+// kItemCost per item and head) that is cut into equal shares, one per CTA, so
+// every CTA has the same work whatever the lengths are. An item that crosses a
+// share's end is finished by the next CTA; the pieces are joined afterwards.
+#pragma once
+
+#include "attn.cuh"
+
+namespace gdn {
+
+constexpr int kAttnM = 128;      // (row, head) pairs of an item: the tensor core's M
+constexpr int kAttnKeys = 128;   // keys of a tile
+constexpr unsigned kTileCost = 4, kItemCost = 3;
+// A request joins its group's shared pass with up to this many (row, head)
+// pairs; above, its own tiles are full enough to read the shared keys alone.
+constexpr int kJoinRows = 64;
+// Shared keys below which reading them per request costs less than the join.
+constexpr int kMinShared = 256;
+
+enum { ITEM_OWN = 0, ITEM_JOINED = 1, ITEM_GROUP = 2 };
+
+struct AttnItem {
+  unsigned long long off;  // of head 0 on the cost line
+  uint32_t cost;           // of each head
+  int32_t tiles;           // of 128 keys, from k0 on
+  int32_t row_base;        // first packed row (own), first entry of the row list (group)
+  int32_t m0, m_cnt;       // the tile's place among the item's (row, head) pairs
+  int32_t req;             // whose page table is read
+  int32_t k0, kend;        // keys [k0, kend)
+  int32_t vis0;            // own: row i of the request sees keys below vis0 + i
+  int32_t kind;
+  int32_t list;            // joined: the request's first entry of the row list
+  int32_t pad[3];
+};
+static_assert(sizeof(AttnItem) == 64, "one item is 64 bytes");
+
+// A row of the list: rows of requests that join a group's pass.
+struct AttnRow {
+  int32_t row, req, group;
+  int32_t own_m, group_m;  // of its head 0 in the request's item and among the group's pairs
+  int32_t pad[3];
+};
+
+struct AttnHead {
+  unsigned long long share, total;
+  int32_t items, list_rows;
+};
+
+// Byte offsets inside the plan, and the bounds they come from.
+struct AttnLayout {
+  int ctas, max_items, max_list, ents;  // ents: groups, then requests
+  size_t qfirst, items, list, first_item, k0, req_list, g_shared, g_rows, g_off, bytes;
+  size_t ws_ml, ws_bytes;  // partial rows: fp32 o, then (m, l)
+  long long ws_rows;
+};
+
+struct AttnPlan {
+  const AttnHead* head;
+  const int32_t* qfirst;      // [ctas + 1]: the item that holds the start of a CTA's share
+  const AttnItem* items;
+  const AttnRow* list;
+  const int32_t* first_item;  // [ents + 1]
+  int ctas, max_list, ents, num_groups;
+};
+
+// Partial rows of an item piece: where piece `c` of item q keeps row m (own
+// place in the tile). Split pieces: two tiles of 128 rows per CTA (a CTA has
+// at most one item that began before its share and one that goes on after
+// it); whole items that are joined with others: by list row and query head.
+__device__ __forceinline__ long long partial_row(const AttnPlan& P, const AttnItem& it, int head,
+                                                 int Hq, int G, unsigned long long off,
+                                                 unsigned long long share, int c, int m) {
+  const unsigned long long c0 = off / share, c1 = (off + it.cost - 1) / share;
+  if (c0 != c1) return (long long)(2 * c + (c == (int)c0 ? 1 : 0)) * kAttnM + m;
+  const int mi = it.m0 + m, i = mi / G, hq = head * G + mi - i * G;
+  const long long base = (long long)2 * P.ctas * kAttnM;
+  if (it.kind == ITEM_JOINED) return base + (long long)(it.list + i) * Hq + hq;
+  return base + ((long long)P.max_list + it.row_base + i) * Hq + hq;
+}
+
+// Tiles [t0, t1) of an item that CTA c has.
+__device__ __forceinline__ void piece_tiles(const AttnItem& it, unsigned long long off,
+                                            unsigned long long share, int c, int& t0, int& t1) {
+  const unsigned long long a = (unsigned long long)c * share, b = a + share, e = off + it.cost;
+  t0 = a <= off ? 0 : (int)((a - off) * it.tiles / it.cost);
+  t1 = b >= e ? it.tiles : (int)((b - off) * it.tiles / it.cost);
+}
+
+int attn_ctas_per_sm(int D);
+AttnLayout attn_layout(const AttnDims& A, const KvBatch& B);
+cudaError_t launch_attn_plan(const AttnDims& A, const KvBatch& B, void* plan, int32_t* status,
+                             cudaStream_t s);
+cudaError_t launch_attn_join(const AttnDims& A, const KvBatch& B, int io, const void* plan,
+                             const void* ws, void* o, float* lse, cudaStream_t s);
+// tk, tv: CUtensorMaps of the caches (16-bit elements, [pages][Hkv * page_size][D],
+// boxes of 64 elements x min(page_size, 128) tokens, 128-byte swizzle).
+cudaError_t launch_attn(const void* tk, const void* tv, const AttnDims& A, const KvBatch& B,
+                        int io, const void* plan, const void* q, long long qs, const void* vc,
+                        void* o, float* lse, void* ws, int32_t* status, cudaStream_t s);
+
+inline AttnPlan attn_plan_view(const AttnLayout& L, const KvBatch& B, const void* plan) {
+  const char* p = (const char*)plan;
+  return AttnPlan{(const AttnHead*)p, (const int32_t*)(p + L.qfirst),
+                  (const AttnItem*)(p + L.items), (const AttnRow*)(p + L.list),
+                  (const int32_t*)(p + L.first_item), L.ctas, L.max_list, L.ents, B.num_groups};
+}
+
+}  // namespace gdn

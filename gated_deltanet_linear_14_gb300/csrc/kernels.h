@@ -10,6 +10,12 @@ namespace gdn {
 // SMs of the current device.
 int device_sms();
 
+// TMA descriptor (a CUtensorMap) of a key or value cache of 16-bit elements,
+// [pages][tokens][D] with `tokens` = heads * page size: boxes of 64 elements x
+// box_tokens, 128-byte swizzle. Implemented in api.cu.
+gdn_status encode_cache_tmap(void* tmap, const void* cache, int D, int tokens, int pages,
+                             int box_tokens);
+
 cudaError_t launch_conv(const Geom& G, const Batch& B, const Params& P, int io_bf16, int y_f32,
                         const void* x, const void* w, void* y, void* pages, int32_t* status,
                         cudaStream_t stream);
