@@ -46,7 +46,8 @@ template <int D>
 struct Cfg {
   static constexpr int NC = D / 64;                    // 64-element chunks of a head
   static constexpr int NSB = D == 256 ? 2 : 1;         // score buffers
-  static constexpr int NS = D == 64 ? 6 : D == 128 ? 5 : 10;  // ring units
+  static constexpr int NS = D == 64 ? 6 : D == 128 ? 4 : 10;  // ring units
+  static constexpr int VW = NC >= 2 ? 2 : 1;  // units of one value MMA (its N is 64 VW)
   static constexpr int CTAS = D == 256 ? 1 : 2;
   static constexpr uint32_t TM_COLS = D == 256 ? 512 : 256;
   static constexpr uint32_t TM_O = NSB * 128;
@@ -113,6 +114,48 @@ __device__ __forceinline__ void tm_store16(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
+// One lane of a converged warp. The MMA and copy instructions take their
+// operands from the warp's uniform registers: issued under this predicate in
+// code that the whole warp runs, with operands that the compiler knows to be
+// the same in all lanes, an MMA costs a few issue slots; under `lane == 0`
+// every operand was moved over one by one, about 140 cycles an MMA.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(~0u, x, 0); }
+
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// The slow end of a wait by a whole warp, bounded as umma::mbar_wait is; `dead`
+// (shared) says that another role gave up.
+__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* dead,
+                                           int32_t* status) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+    if (__all_sync(~0u, bar_try(bar, parity))) return true;
+    if ((i & 63) == 63) {
+      const uint64_t now = global_ns();
+      if (t0 == 0) t0 = now;
+      if (__any_sync(~0u, *dead || now - t0 > kWaitNs)) break;
+    }
+  }
+  *dead = 1;
+  report(status, GDN_DEV_TIMEOUT);
+  return false;
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -148,6 +191,8 @@ struct Walk {
     q = P.qfirst[c];
     // the item that holds the start of the share; if an item starts right
     // there or the previous one ended before it, q is already that one
+    Q = uniform(Q);
+    q = uniform(q);
     item = q / Hkv;
     head = q - item * Hkv;
     --head;
@@ -162,6 +207,7 @@ struct Walk {
       off = it.off + (unsigned long long)head * it.cost;
       if (off >= (unsigned long long)(c + 1) * share) return false;
       piece_tiles(it, off, share, c, t0, t1);
+      t0 = uniform(t0), t1 = uniform(t1);
       if (t0 < t1) return true;
     }
   }
@@ -204,13 +250,11 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
   const uint32_t tmem = words[0];
   pdl_begin();
 
-  // A wait that gives up ends its role; words[1] then ends the others.
+  // All lanes of a warp wait, and go on together. A wait that gives up ends
+  // its role; words[1] then ends the others.
   auto wait = [&](uint32_t bar, uint32_t parity) {
-    if (words[1]) return false;
-    if (mbar_wait(bar, parity)) return true;
-    words[1] = 1;
-    report(status, GDN_DEV_TIMEOUT);
-    return false;
+    if (__all_sync(~0u, bar_try(bar, parity))) return true;
+    return bar_wait_long(bar, parity, words + 1, status);
   };
 
   Walk W(P, A);
@@ -232,17 +276,18 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
         return 0;
       };
       auto emit = [&](const CUtensorMap& tm, int t, int page) {
-        const int key = W.it.k0 + t * kAttnKeys + lane * br;
-        const int n = __popc(__ballot_sync(~0u, page >= 0));
-        for (int c = 0; c < NC && ok; ++c) {
-          ok = wait(empty + 8 * slot, phase ^ 1);
-          ok = __all_sync(~0u, ok);
-          if (!ok) return;
-          if (lane == 0) mbar_expect_tx(full + 8 * slot, n * br * 128);
+        const int key0 = W.it.k0 + t * kAttnKeys;
+        const int n = uniform(__popc(__ballot_sync(~0u, page >= 0)));  // boxes with keys
+        for (int c = 0; c < NC; ++c) {
+          if (!(ok = wait(empty + 8 * slot, phase ^ 1))) return;
+          const uint32_t bar = full + 8 * slot, dst = ring + slot * kUnit;
+          if (elect_one()) mbar_expect_tx(bar, n * br * 128);
           __syncwarp();
-          if (page >= 0)
-            tma_load_3d(ring + slot * kUnit + lane * br * 128, &tm, c * 64,
-                        W.head * A.ps + (key & (A.ps - 1)), page, full + 8 * slot);
+          for (int x = 0; x < n; ++x) {
+            const int z = __shfl_sync(~0u, page, x);
+            const int y = W.head * A.ps + ((key0 + x * br) & (A.ps - 1));
+            if (elect_one()) tma_load_3d(dst + x * br * 128, &tm, c * 64, y, z, bar);
+          }
           if (++slot == NS) slot = 0, phase ^= 1;
           used = min(used + 1, NS);
         }
@@ -265,59 +310,68 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
     }
   } else if (warp == 5) {
     // ----------------------------------------------------------------- MMA
-    if (lane == 0) {
-      int slot = 0, g = 0;  // g: tiles so far
-      uint32_t phase = 0, items = 0;
-      bool ok = true;
-      const uint32_t id_s = idesc<T>(128, 0), id_o = idesc<T>(64, 1);
-      auto advance = [&]() {
-        mma_commit(empty + 8 * slot);
-        if (++slot == NS) slot = 0, phase ^= 1;
-      };
-      auto scores = [&](int b) {
-        for (int c = 0; c < NC; ++c) {
-          if (!(ok = wait(full + 8 * slot, phase))) return;
-          tc_fence_after();
+    int slot = 0, g = 0;  // g: tiles so far
+    uint32_t phase = 0, items = 0;
+    bool ok = true;
+    const uint32_t id_s = idesc<T>(128, 0), id_o = idesc<T>(64 * C::VW, 1), tm = uniform(tmem);
+    const uint64_t dq = sdesc(sb, 16, 1024), dk = sdesc(ring, 16, 1024);
+    const uint64_t dv = sdesc(ring, kUnit, 1024);
+    auto advance = [&]() {
+      if (++slot == NS) slot = 0, phase ^= 1;
+    };
+    auto scores = [&](int b) {
+      for (int c = 0; c < NC; ++c) {
+        if (!(ok = wait(full + 8 * slot, phase))) return;
+        if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            mma_bf16(tmem + 128 * b, sdesc(sb + c * kUnit + ks * 32, 16, 1024),
-                     sdesc(ring + slot * kUnit + ks * 32, 16, 1024), id_s, (c | ks) != 0);
-          advance();
+            mma_bf16(tm + 128 * b, dq + ((c * kUnit + ks * 32) >> 4),
+                     dk + ((slot * kUnit + ks * 32) >> 4), id_s, (c | ks) != 0);
+          mma_commit(empty + 8 * slot);
+          if (c == NC - 1) mma_commit(s_full + 8 * b);
         }
-        mma_commit(s_full + 8 * b);
-      };
-      auto values = [&](int b, bool first) {
-        for (int c = 0; c < NC; ++c) {
-          if (!(ok = wait(full + 8 * slot, phase))) return;
-          tc_fence_after();
+        __syncwarp();
+        advance();
+      }
+    };
+    // (the units of one MMA are neighbours in the ring: NC and NS are even
+    // where it takes two)
+    auto values = [&](int b, bool first) {
+      for (int c = 0; c < NC; c += C::VW) {
+        if (!(ok = wait(full + 8 * slot, phase))) return;
+        if (C::VW == 2 && !(ok = wait(full + 8 * slot + 8, phase))) return;
+        if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            mma_ts(tmem + C::TM_O + 64 * c, tmem + 128 * b + 8 * ks,
-                   sdesc(ring + slot * kUnit + ks * 2048, 16, 1024), id_o, !(first && ks == 0));
-          advance();
+            mma_ts(tm + C::TM_O + 64 * c, tm + 128 * b + 8 * ks,
+                   dv + ((slot * kUnit + ks * 2048) >> 4), id_o, !(first && ks == 0));
+          mma_commit(empty + 8 * slot);
+          if (C::VW == 2) mma_commit(empty + 8 * slot + 8);
+          if (c + C::VW == NC) mma_commit(o_full + 8 * b);
         }
-        mma_commit(o_full + 8 * b);
-      };
-      while (ok && W.next()) {
-        if (!(ok = wait(q_full, items++ & 1))) break;
-        tc_fence_after();
-        if (NSB == 2) scores(g & 1);
-        for (int t = W.t0; ok && t < W.t1; ++t, ++g) {
-          if (NSB == 1) scores(0);
-          else if (t + 1 < W.t1) scores((g + 1) & 1);
-          if (!ok) break;
-          const int b = NSB == 2 ? g & 1 : 0;
-          if (!(ok = wait(p_ready + 8 * b, (NSB == 2 ? g >> 1 : g) & 1))) break;
-          tc_fence_after();
-          values(b, t == W.t0);
-        }
+        __syncwarp();
+        advance();
+        if (C::VW == 2) advance();
       }
-      if (!ok) {  // gave up: give the issued MMAs a millisecond to finish
-        const uint64_t t = global_ns();
-        for (int i = 0; i < 1000 && global_ns() - t < 1000000; ++i) __nanosleep(1000);
+    };
+    while (ok && W.next()) {
+      if (!(ok = wait(q_full, items++ & 1))) break;
+      tc_fence_after();
+      if (NSB == 2) scores(g & 1);
+      for (int t = W.t0; ok && t < W.t1; ++t, ++g) {
+        if (NSB == 1) scores(0);
+        else if (t + 1 < W.t1) scores((g + 1) & 1);
+        if (!ok) break;
+        const int b = NSB == 2 ? g & 1 : 0;
+        if (!(ok = wait(p_ready + 8 * b, (NSB == 2 ? g >> 1 : g) & 1))) break;
+        tc_fence_after();
+        values(b, t == W.t0);
       }
     }
-    __syncwarp();
+    if (!ok) {  // gave up: give the issued MMAs a millisecond to finish
+      const uint64_t t = global_ns();
+      for (int i = 0; i < 1000 && global_ns() - t < 1000000; ++i) __nanosleep(1000);
+    }
   } else {
     // ------------------------------------------------------------- softmax
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
@@ -325,10 +379,6 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
     int g = 0;
     uint32_t units = 0, items = 0;  // ring units and items before this one
     bool ok = true;
-    // all lanes wait, and go on together
-    auto wait_all = [&](uint32_t bar, uint32_t parity) {
-      return __all_sync(~0u, wait(bar, parity)) != 0;
-    };
     for (; ok && W.next(); ++items) {
       const AttnItem& it = W.it;
       const bool rows_here = it.m_cnt > warp * 32;
@@ -366,7 +416,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
         const uint32_t ts = tmem + 128 * b + lane_base;
         const int base = it.k0 + t * kAttnKeys, nv = min(kAttnKeys, it.kend - base);
         const bool cut = mixed && base + kAttnKeys > first_seen;  // rows see different keys
-        if (!(ok = wait_all(s_full + 8 * b, (NSB == 2 ? g >> 1 : g) & 1))) break;
+        if (!(ok = wait(s_full + 8 * b, (NSB == 2 ? g >> 1 : g) & 1))) break;
         tc_fence_after();
         // every warp is past the previous item: its flag is the next item's
         if (t == W.t0 && tid == 0) words[2 + ((items + 1) & 1)] = 0;
@@ -399,7 +449,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
             m = nm;
             // O is complete up to the previous tile: with one score buffer these
             // scores came after its product, with two they did not
-            if (NSB == 2 && !(ok = wait_all(o_full + 8 * (b ^ 1), ((g - 1) >> 1) & 1))) break;
+            if (NSB == 2 && !(ok = wait(o_full + 8 * (b ^ 1), ((g - 1) >> 1) & 1))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int j = 0; j < D / 32; ++j) {
@@ -445,13 +495,13 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
           // (two score buffers: the ring slots may still belong to the previous
           // tile's values until its product is complete)
           if (NSB == 2 && t > W.t0 &&
-              !(ok = wait_all(o_full + 8 * (b ^ 1), ((g - 1) >> 1) & 1)))
+              !(ok = wait(o_full + 8 * (b ^ 1), ((g - 1) >> 1) & 1)))
             break;
           const int j = t - W.t0;
           const uint32_t at = units + NC * (NSB == 1 ? 2 * j + 1 : min(2 * j + 2, 2 * tiles - 1));
           for (int c = 0; c < NC && ok; ++c) {
             const uint32_t u = at + c, s = u % NS;
-            if (!(ok = wait_all(full + 8 * s, (u / NS) & 1))) break;
+            if (!(ok = wait(full + 8 * s, (u / NS) & 1))) break;
             uint4* vrow = reinterpret_cast<uint4*>(smem + C::RING + s * kUnit + tid * 128);
             for (int k = 0; k < 8; ++k) {
               uint4& w = vrow[(k + lane) & 7];  // all banks at once
@@ -478,7 +528,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
       if (!ok) break;
       units += 2 * NC * tiles;
       const int last = g - 1;
-      if (!(ok = wait_all(o_full + 8 * (NSB == 2 ? last & 1 : 0),
+      if (!(ok = wait(o_full + 8 * (NSB == 2 ? last & 1 : 0),
                           (NSB == 2 ? last >> 1 : last) & 1)))
         break;
       tc_fence_after();
