@@ -156,6 +156,19 @@ __device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volati
   return false;
 }
 
+// A whole 32-byte sector per lane where the address allows it: rows are a
+// lane's own, so narrower stores reach the L2 as parts of sectors.
+__device__ __forceinline__ void store32B(void* p, const uint32_t* w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -275,21 +288,31 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
         report(status, GDN_DEV_BAD_PAGE);
         return 0;
       };
+      // the units of a tile's keys or values, two at a time, page by page
+      constexpr int NU = NC < 2 ? 1 : 2;
       auto emit = [&](const CUtensorMap& tm, int t, int page) {
         const int key0 = W.it.k0 + t * kAttnKeys;
         const int n = uniform(__popc(__ballot_sync(~0u, page >= 0)));  // boxes with keys
-        for (int c = 0; c < NC; ++c) {
-          if (!(ok = wait(empty + 8 * slot, phase ^ 1))) return;
-          const uint32_t bar = full + 8 * slot, dst = ring + slot * kUnit;
-          if (elect_one()) mbar_expect_tx(bar, n * br * 128);
-          __syncwarp();
+        for (int c0 = 0; c0 < NC; c0 += NU) {
+          uint32_t at[NU], bar[NU];
+#pragma unroll
+          for (int c = 0; c < NU; ++c) {
+            if (!(ok = wait(empty + 8 * slot, phase ^ 1))) return;
+            at[c] = ring + slot * kUnit;
+            bar[c] = full + 8 * slot;
+            if (++slot == NS) slot = 0, phase ^= 1;
+            used = min(used + 1, NS);
+            if (elect_one()) mbar_expect_tx(bar[c], n * br * 128);
+          }
           for (int x = 0; x < n; ++x) {
             const int z = __shfl_sync(~0u, page, x);
             const int y = W.head * A.ps + ((key0 + x * br) & (A.ps - 1));
-            if (elect_one()) tma_load_3d(dst + x * br * 128, &tm, c * 64, y, z, bar);
+            if (elect_one()) {
+#pragma unroll
+              for (int c = 0; c < NU; ++c)
+                tma_load_3d(at[c] + x * br * 128, &tm, (c0 + c) * 64, y, z, bar[c]);
+            }
           }
-          if (++slot == NS) slot = 0, phase ^= 1;
-          used = min(used + 1, NS);
         }
       };
       int cur = page_of(W.t0), nxt = page_of(W.t0 + 1);
@@ -394,16 +417,17 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
         constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte pieces of a row, rows at once
         const unsigned long long src = (unsigned long long)(q + row * qs + (long long)hq * D);
         const int n = min(32, it.m_cnt - warp * 32), ch = lane % CH;
-#pragma unroll 4
-        for (int r0 = 0; r0 < 32; r0 += RPI) {
+        const uint32_t dst = sb + (ch >> 3) * kUnit;
+        for (int r0 = 0; r0 < n; r0 += RPI) {
           const int r = r0 + lane / CH;
-          const unsigned long long from = __shfl_sync(~0u, src, r);
-          if (r < n) {
-            const uint4 v = *reinterpret_cast<const uint4*>(from + ch * 16);
-            *reinterpret_cast<uint4*>(smem + (ch >> 3) * kUnit +
-                                      sw128_chunk(warp * 32 + r, ch & 7)) = v;
-          }
+          const unsigned long long from = __shfl_sync(~0u, src, r) + ch * 16;
+          if (r < n)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                             dst + sw128_chunk(warp * 32 + r, ch & 7)),
+                         "l"(from)
+                         : "memory");
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
       }
       fence_async_smem();
       __syncwarp();
@@ -542,6 +566,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
             direct || !mine ? 0 : partial_row(P, it, W.head, A.Hq, A.G, W.off, W.share, W.c, tid);
         T* dst = o + (row * A.Hq + hq) * D;
         float* pdst = po + part * D;
+        const bool wide = (((uintptr_t)o | (uintptr_t)po) & 31) == 0;
 #pragma unroll 1
         for (int j = 0; j < D / 32; ++j) {
           float v[32];
@@ -568,15 +593,12 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) w[e] = pack2<T>(v[2 * e] * inv, v[2 * e + 1] * inv);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              reinterpret_cast<uint4*>(dst + 32 * j)[e] =
-                  make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+            store32B(dst + 32 * j, w, wide);
+            store32B(dst + 32 * j + 16, w + 8, wide);
           } else if (mine) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              reinterpret_cast<float4*>(pdst + 32 * j)[e] =
-                  make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            for (int e = 0; e < 4; ++e)
+              store32B(pdst + 32 * j + 8 * e, reinterpret_cast<const uint32_t*>(v + 8 * e), wide);
           }
           __syncwarp();
         }
