@@ -2,7 +2,7 @@
 // cores (sm_103a).
 //
 // An item (attn_plan.cuh) is a tile Q of 128 (row, query head) pairs of one
-// key/value head and a range of keys. One pass over the keys, 128 at a time:
+// key/value head and a range of keys. One pass over the keys, 64 at a time:
 //   S = Q K^T                               (tensor cores, fp32 in TMEM)
 //   m' = max(m, max_j s_j),  p_j = 2^{c (s_j - m')},  c = scale log2 e
 //   l = l 2^{c (m - m')} + sum_j p_j,   O = O 2^{c (m - m')} + P V
@@ -13,13 +13,14 @@
 // Roles: warps 0-3 softmax, one (row, head) pair a thread (its TMEM lane, so
 // that no statistic crosses lanes); warp 4 fetches keys and values by TMA, a
 // box per page; warp 5 issues the MMAs. The ring between them holds units of
-// 128 keys x 64 elements (16 KB), K and V alike, in the order in which the
-// MMAs use them: nothing is resident but Q.
+// 64 keys x up to 128 elements, K and V alike, in the order in which the MMAs
+// use them: nothing is resident but Q.
 //
-// D <= 128 runs two CTAs per SM (256 TMEM columns each): one's softmax covers
-// the other's products, so one score buffer each is enough. D = 256 has one
-// CTA per SM with two score buffers, the next tile's scores being formed while
-// this tile's softmax runs.
+// Two score buffers: the next tile's scores are formed while this tile's
+// softmax runs, also across items (the next item's Q is fetched when the last
+// scores of this one are complete), so the softmax warps and the tensor cores
+// wait for each other only at the start. D <= 128 runs two CTAs per SM (256
+// TMEM columns each: O and 2 x 64 scores), D = 256 one.
 #include <cuda.h>
 
 #include <type_traits>
@@ -36,7 +37,8 @@ namespace {
 
 constexpr int kSoftmaxWarps = 4;
 constexpr int kAttnThreads = 32 * (kSoftmaxWarps + 2);
-constexpr uint32_t kUnit = kAttnKeys * 128;  // bytes of a ring unit
+constexpr uint32_t kQChunk = kAttnM * 128;      // bytes of 64 elements of all rows
+constexpr uint32_t kChunk = kAttnKeys * 128;    // ... of all keys of a tile
 // The running maximum is raised only when a score exceeds it by more than
 // this (in powers of two): until then p grows up to 2^8, harmless in fp32 sums
 // and in a bf16 or fp16 P, and O need not be rescaled.
@@ -44,16 +46,17 @@ constexpr float kRaise = 8.0f;
 
 template <int D>
 struct Cfg {
-  static constexpr int NC = D / 64;                    // 64-element chunks of a head
-  static constexpr int NSB = D == 256 ? 2 : 1;         // score buffers
-  static constexpr int NS = D == 64 ? 6 : D == 128 ? 4 : 10;  // ring units
-  static constexpr int VW = NC >= 2 ? 2 : 1;  // units of one value MMA (its N is 64 VW)
+  static constexpr int NC = D / 64;                  // 64-element chunks of a head
+  static constexpr int CU = NC < 2 ? 1 : 2;          // chunks of a ring unit
+  static constexpr int NU = NC / CU;                 // units of a tile's keys (or values)
+  static constexpr uint32_t UNIT = CU * kChunk;
+  static constexpr int NS = D == 64 ? 12 : D == 128 ? 5 : 10;  // units of the ring
   static constexpr int CTAS = D == 256 ? 1 : 2;
   static constexpr uint32_t TM_COLS = D == 256 ? 512 : 256;
-  static constexpr uint32_t TM_O = NSB * 128;
-  static constexpr uint32_t RING = NC * kUnit;
-  static constexpr uint32_t BARS = RING + NS * kUnit;
-  static constexpr uint32_t BYTES = BARS + 8 * (2 * NS + 7) + 16;
+  static constexpr uint32_t TM_O = 2 * kAttnKeys;    // after the two score buffers
+  static constexpr uint32_t RING = NC * kQChunk;
+  static constexpr uint32_t BARS = RING + NS * UNIT;
+  static constexpr uint32_t BYTES = BARS + 8 * (2 * NS + 7) + 32;
 };
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z,
@@ -105,12 +108,15 @@ __device__ __forceinline__ void tm_wait32(Cols& c) {
                  "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
                  "+r"(r[30]), "+r"(r[31])::"memory");
 }
-__device__ __forceinline__ void tm_store16(uint32_t taddr, const uint32_t* r) {
+__device__ __forceinline__ void tm_store32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
 
@@ -191,17 +197,17 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
 
 // The items of one CTA, walked alike by every role.
 struct Walk {
-  const AttnPlan& P;
+  const AttnPlan* P;
   int Hkv, G, c, q, Q, item, head;
   unsigned long long share, off;
   AttnItem it;
   int t0, t1;
 
   __device__ __forceinline__ Walk(const AttnPlan& P_, const AttnDims& A)
-      : P(P_), Hkv(A.Hkv), G(A.G), c(blockIdx.x) {
-    share = P.head->share;
-    Q = P.head->items * Hkv;
-    q = P.qfirst[c];
+      : P(&P_), Hkv(A.Hkv), G(A.G), c(blockIdx.x) {
+    share = P->head->share;
+    Q = P->head->items * Hkv;
+    q = P->qfirst[c];
     // the item that holds the start of the share; if an item starts right
     // there or the previous one ended before it, q is already that one
     Q = uniform(Q);
@@ -216,7 +222,7 @@ struct Walk {
       ++q;
       if (++head == Hkv) head = 0, ++item;
       if (q >= Q) return false;
-      it = P.items[item];
+      it = P->items[item];
       off = it.off + (unsigned long long)head * it.cost;
       if (off >= (unsigned long long)(c + 1) * share) return false;
       piece_tiles(it, off, share, c, t0, t1);
@@ -237,7 +243,8 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
             AttnDims A, KvBatch B, AttnPlan P, const T* q, long long qs, const T* vc, T* o,
             float* lse, float* po, float2* pml, int32_t* status) {
   using C = Cfg<D>;
-  constexpr int NC = C::NC, NS = C::NS, NSB = C::NSB;
+  constexpr int NU = C::NU, CU = C::CU, NS = C::NS;
+  constexpr uint32_t UNIT = C::UNIT;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem), ring = sb + C::RING;
   const uint32_t full = sb + C::BARS, empty = full + 8 * NS, q_full = empty + 8 * NS;
@@ -253,7 +260,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
       mbar_init(p_ready + 8 * i, kSoftmaxWarps);
     }
     for (int i = 0; i < 2; ++i) mbar_init(o_full + 8 * i, 1);
-    words[1] = words[2] = words[3] = 0;
+    words[1] = words[2] = words[3] = words[4] = 0;
     mbar_fence_init();
   }
   if (warp == 5) tmem_alloc(smem_u32((const void*)words), C::TM_COLS);
@@ -288,40 +295,33 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
         report(status, GDN_DEV_BAD_PAGE);
         return 0;
       };
-      // the units of a tile's keys or values, two at a time, page by page
-      constexpr int NU = NC < 2 ? 1 : 2;
+      // the units of a tile's keys or values, page by page
       auto emit = [&](const CUtensorMap& tm, int t, int page) {
         const int key0 = W.it.k0 + t * kAttnKeys;
         const int n = uniform(__popc(__ballot_sync(~0u, page >= 0)));  // boxes with keys
-        for (int c0 = 0; c0 < NC; c0 += NU) {
-          uint32_t at[NU], bar[NU];
-#pragma unroll
-          for (int c = 0; c < NU; ++c) {
-            if (!(ok = wait(empty + 8 * slot, phase ^ 1))) return;
-            at[c] = ring + slot * kUnit;
-            bar[c] = full + 8 * slot;
-            if (++slot == NS) slot = 0, phase ^= 1;
-            used = min(used + 1, NS);
-            if (elect_one()) mbar_expect_tx(bar[c], n * br * 128);
-          }
+        for (int u = 0; u < NU; ++u) {
+          if (!(ok = wait(empty + 8 * slot, phase ^ 1))) return;
+          const uint32_t at = ring + slot * UNIT, bar = full + 8 * slot;
+          if (elect_one()) mbar_expect_tx(bar, n * br * 128 * CU);
           for (int x = 0; x < n; ++x) {
             const int z = __shfl_sync(~0u, page, x);
             const int y = W.head * A.ps + ((key0 + x * br) & (A.ps - 1));
             if (elect_one()) {
 #pragma unroll
-              for (int c = 0; c < NU; ++c)
-                tma_load_3d(at[c] + x * br * 128, &tm, (c0 + c) * 64, y, z, bar[c]);
+              for (int c = 0; c < CU; ++c)
+                tma_load_3d(at + c * kChunk + x * br * 128, &tm, (u * CU + c) * 64, y, z, bar);
             }
           }
+          if (++slot == NS) slot = 0, phase ^= 1;
+          used = min(used + 1, NS);
         }
       };
       int cur = page_of(W.t0), nxt = page_of(W.t0 + 1);
       emit(tk, W.t0, cur);
       for (int t = W.t0; ok && t < W.t1; ++t) {
         const int after = page_of(t + 2);
-        if (NSB == 2 && t + 1 < W.t1) emit(tk, t + 1, nxt);
-        emit(tv, t, cur);
-        if (NSB == 1 && t + 1 < W.t1) emit(tk, t + 1, nxt);
+        if (t + 1 < W.t1) emit(tk, t + 1, nxt);
+        if (ok) emit(tv, t, cur);
         cur = nxt, nxt = after;
       }
     }
@@ -336,59 +336,58 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
     int slot = 0, g = 0;  // g: tiles so far
     uint32_t phase = 0, items = 0;
     bool ok = true;
-    const uint32_t id_s = idesc<T>(128, 0), id_o = idesc<T>(64 * C::VW, 1), tm = uniform(tmem);
+    const uint32_t id_s = idesc<T>(kAttnKeys, 0), id_o = idesc<T>(D, 1), tm = uniform(tmem);
     const uint64_t dq = sdesc(sb, 16, 1024), dk = sdesc(ring, 16, 1024);
-    const uint64_t dv = sdesc(ring, kUnit, 1024);
+    const uint64_t dv = sdesc(ring, kChunk, 1024);
     auto advance = [&]() {
       if (++slot == NS) slot = 0, phase ^= 1;
     };
     auto scores = [&](int b) {
-      for (int c = 0; c < NC; ++c) {
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
         if (!(ok = wait(full + 8 * slot, phase))) return;
         if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_bf16(tm + 128 * b, dq + ((c * kUnit + ks * 32) >> 4),
-                     dk + ((slot * kUnit + ks * 32) >> 4), id_s, (c | ks) != 0);
+          for (int ks = 0; ks < 4 * CU; ++ks) {
+            const uint32_t c = ks >> 2, k = (ks & 3) * 32;
+            mma_bf16(tm + kAttnKeys * b, dq + (((u * CU + c) * kQChunk + k) >> 4),
+                     dk + ((slot * UNIT + c * kChunk + k) >> 4), id_s, (u | ks) != 0);
+          }
           mma_commit(empty + 8 * slot);
-          if (c == NC - 1) mma_commit(s_full + 8 * b);
+          if (u == NU - 1) mma_commit(s_full + 8 * b);
         }
         __syncwarp();
         advance();
       }
     };
-    // (the units of one MMA are neighbours in the ring: NC and NS are even
-    // where it takes two)
+    // (one MMA covers all D columns: a tile's value units are neighbours, NS
+    // being a multiple of NU)
     auto values = [&](int b, bool first) {
-      for (int c = 0; c < NC; c += C::VW) {
-        if (!(ok = wait(full + 8 * slot, phase))) return;
-        if (C::VW == 2 && !(ok = wait(full + 8 * slot + 8, phase))) return;
-        if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_ts(tm + C::TM_O + 64 * c, tm + 128 * b + 8 * ks,
-                   dv + ((slot * kUnit + ks * 2048) >> 4), id_o, !(first && ks == 0));
-          mma_commit(empty + 8 * slot);
-          if (C::VW == 2) mma_commit(empty + 8 * slot + 8);
-          if (c + C::VW == NC) mma_commit(o_full + 8 * b);
-        }
-        __syncwarp();
-        advance();
-        if (C::VW == 2) advance();
+      for (int u = 0; u < NU; ++u)
+        if (!(ok = wait(full + 8 * (slot + u), phase))) return;
+      if (elect_one()) {
+#pragma unroll
+        for (int ks = 0; ks < kAttnKeys / 16; ++ks)
+          mma_ts(tm + C::TM_O, tm + kAttnKeys * b + 8 * ks,
+                 dv + ((slot * UNIT + ks * 2048) >> 4), id_o, !(first && ks == 0));
+#pragma unroll
+        for (int u = 0; u < NU; ++u) mma_commit(empty + 8 * (slot + u));
+        mma_commit(o_full + 8 * b);
       }
+      __syncwarp();
+#pragma unroll
+      for (int u = 0; u < NU; ++u) advance();
     };
     while (ok && W.next()) {
       if (!(ok = wait(q_full, items++ & 1))) break;
       tc_fence_after();
-      if (NSB == 2) scores(g & 1);
+      scores(g & 1);
       for (int t = W.t0; ok && t < W.t1; ++t, ++g) {
-        if (NSB == 1) scores(0);
-        else if (t + 1 < W.t1) scores((g + 1) & 1);
-        if (!ok) break;
-        const int b = NSB == 2 ? g & 1 : 0;
-        if (!(ok = wait(p_ready + 8 * b, (NSB == 2 ? g >> 1 : g) & 1))) break;
+        if (t + 1 < W.t1) scores((g + 1) & 1);
+        if (!ok || !(ok = wait(p_ready + 8 * (g & 1), (g >> 1) & 1))) break;
         tc_fence_after();
-        values(b, t == W.t0);
+        values(g & 1, t == W.t0);
       }
     }
     if (!ok) {  // gave up: give the issued MMAs a millisecond to finish
@@ -401,69 +400,88 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
     const float c2 = A.scale * 1.44269504088896341f;
     int g = 0;
     uint32_t units = 0, items = 0;  // ring units and items before this one
-    bool ok = true;
-    for (; ok && W.next(); ++items) {
+    // this thread's (row, head) pair of an item
+    auto pair_of = [&](const AttnItem& it, int head, int& i, int& hq) {
+      const int mi = it.m0 + min(tid, it.m_cnt - 1);
+      i = mi / A.G;
+      hq = head * A.G + mi - i * A.G;
+      return it.kind == ITEM_GROUP ? P.list[it.row_base + i].row : it.row_base + i;
+    };
+    // start copying the warp's rows of an item's Q to shared memory
+    auto fetch_q = [&](const Walk& V) {
+      if (V.it.m_cnt <= warp * 32) return;
+      constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte pieces of a row, rows at once
+      int i, hq;
+      const long long row = pair_of(V.it, V.head, i, hq);
+      const unsigned long long src = (unsigned long long)(q + row * qs + (long long)hq * D);
+      const int n = min(32, V.it.m_cnt - warp * 32), ch = lane % CH;
+      const uint32_t dst = sb + (ch >> 3) * kQChunk;
+      for (int r0 = 0; r0 < n; r0 += RPI) {
+        const int r = r0 + lane / CH;
+        const unsigned long long from = __shfl_sync(~0u, src, r) + ch * 16;
+        if (r < n)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                           dst + sw128_chunk(warp * 32 + r, ch & 7)),
+                       "l"(from)
+                       : "memory");
+      }
+    };
+    auto publish_q = [&]() {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    };
+
+    bool ok = true, more = W.next();
+    if (more) {
+      fetch_q(W);
+      publish_q();
+    }
+    for (; more; ++items) {
+      Walk N = W;
+      more = N.next();
       const AttnItem& it = W.it;
       const bool rows_here = it.m_cnt > warp * 32;
-      // this thread's (row, head) pair
-      const int mi = it.m0 + min(tid, it.m_cnt - 1), i = mi / A.G, hq = W.head * A.G + mi - i * A.G;
+      int i, hq;
+      const long long row = pair_of(it, W.head, i, hq);
       const bool group = it.kind == ITEM_GROUP;
-      const long long row = group ? P.list[it.row_base + i].row : it.row_base + i;
       const int seen = group ? it.kend : it.vis0 + i;  // keys below this
       const int first_seen = group ? it.kend : it.vis0 + it.m0 / A.G;
       const bool mixed = !group && it.m0 / A.G != (it.m0 + it.m_cnt - 1) / A.G;
 
-      if (rows_here) {
-        constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte pieces of a row, rows at once
-        const unsigned long long src = (unsigned long long)(q + row * qs + (long long)hq * D);
-        const int n = min(32, it.m_cnt - warp * 32), ch = lane % CH;
-        const uint32_t dst = sb + (ch >> 3) * kUnit;
-        for (int r0 = 0; r0 < n; r0 += RPI) {
-          const int r = r0 + lane / CH;
-          const unsigned long long from = __shfl_sync(~0u, src, r) + ch * 16;
-          if (r < n)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                             dst + sw128_chunk(warp * 32 + r, ch & 7)),
-                         "l"(from)
-                         : "memory");
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
-
       float m = -INFINITY, l = 0.0f;
       const int tiles = W.t1 - W.t0;
       for (int t = W.t0; t < W.t1; ++t, ++g) {
-        const int b = NSB == 2 ? g & 1 : 0;
-        const uint32_t ts = tmem + 128 * b + lane_base;
+        const int b = g & 1;
+        const uint32_t ts = tmem + kAttnKeys * b + lane_base;
         const int base = it.k0 + t * kAttnKeys, nv = min(kAttnKeys, it.kend - base);
         const bool cut = mixed && base + kAttnKeys > first_seen;  // rows see different keys
-        if (!(ok = wait(s_full + 8 * b, (NSB == 2 ? g >> 1 : g) & 1))) break;
+        if (!(ok = wait(s_full + 8 * b, (g >> 1) & 1))) break;
         tc_fence_after();
-        // every warp is past the previous item: its flag is the next item's
-        if (t == W.t0 && tid == 0) words[2 + ((items + 1) & 1)] = 0;
+        // every warp is past the item before the previous one: its flag is the
+        // next item's
+        if (t == W.t0 && tid == 0) words[2 + (items + 1) % 3] = 0;
+        // the item's scores are complete: Q makes way for the next item's
+        if (more && t + 1 == W.t1) fetch_q(N);
         if (rows_here) {
           const bool masked = cut || nv < kAttnKeys;
           const int lim = min(seen, it.kend) - base;
-          Cols x;
-          float mx = -INFINITY;
+          Cols x[2];
+          tm_load32(ts, x[0]);
+          tm_load32(ts + 32, x[1]);
+          tm_wait32(x[0]);
+          tm_wait32(x[1]);
+          if (masked) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            tm_load32(ts + 32 * j, x);
-            tm_wait32(x);
-            if (masked) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                mx = fmaxf(mx, 32 * j + e < lim ? __uint_as_float(x.r[e]) : -INFINITY);
-            } else {
-              float m4[4] = {mx, mx, mx, mx};
-#pragma unroll
-              for (int e = 0; e < 32; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(x.r[e]));
-              mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-            }
+            for (int e = 0; e < 64; ++e)
+              if (e >= lim) x[e >> 5].r[e & 31] = 0xFF800000u;  // -inf
           }
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(x[e >> 5].r[e & 31]));
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           if (t == W.t0) {
             m = mx;
           } else if (__any_sync(~0u, (mx - m) * c2 > kRaise || (m == -INFINITY && mx > m))) {
@@ -471,9 +489,8 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
             const float f = nm == -INFINITY ? 1.0f : ex2((m - nm) * c2);
             l *= f;
             m = nm;
-            // O is complete up to the previous tile: with one score buffer these
-            // scores came after its product, with two they did not
-            if (NSB == 2 && !(ok = wait(o_full + 8 * (b ^ 1), ((g - 1) >> 1) & 1))) break;
+            // O is complete up to the previous tile
+            if (!(ok = wait(o_full + 8 * (b ^ 1), ((g - 1) >> 1) & 1))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int j = 0; j < D / 32; ++j) {
@@ -487,27 +504,19 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
           const float mc = m == -INFINITY ? 0.0f : m * c2;
           float2 sum = make_float2(0.0f, 0.0f), sum2 = sum;
           const float2 cc = make_float2(c2, c2), nm2 = make_float2(-mc, -mc);
+          uint32_t p[32];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            tm_load32(ts + 32 * j, x);
-            tm_wait32(x);
-            uint32_t p[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float2 s = make_float2(__uint_as_float(x.r[2 * e]), __uint_as_float(x.r[2 * e + 1]));
-              s = __ffma2_rn(s, cc, nm2);
-              s.x = ex2(s.x);
-              s.y = ex2(s.y);
-              if (masked) {
-                if (32 * j + 2 * e >= lim) s.x = 0.0f;
-                if (32 * j + 2 * e + 1 >= lim) s.y = 0.0f;
-              }
-              if (e & 1) sum2 = __fadd2_rn(sum2, s);
-              else sum = __fadd2_rn(sum, s);
-              p[e] = pack2<T>(s.x, s.y);
-            }
-            tm_store16(ts + 16 * j, p);
+          for (int e = 0; e < 32; ++e) {
+            const uint32_t* r = x[e >> 4].r + 2 * (e & 15);
+            float2 s = make_float2(__uint_as_float(r[0]), __uint_as_float(r[1]));
+            s = __ffma2_rn(s, cc, nm2);
+            s.x = ex2(s.x);
+            s.y = ex2(s.y);
+            if (e & 1) sum2 = __fadd2_rn(sum2, s);
+            else sum = __fadd2_rn(sum, s);
+            p[e] = pack2<T>(s.x, s.y);
           }
+          tm_store32(ts, p);
           l += (sum.x + sum.y) + (sum2.x + sum2.y);
           tmem_st_wait();
         }
@@ -516,32 +525,35 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
         // infinite and NaN values are zeroed too and added at the end to the
         // rows that see them.
         if (cut || nv < kAttnKeys) {
-          // (two score buffers: the ring slots may still belong to the previous
-          // tile's values until its product is complete)
-          if (NSB == 2 && t > W.t0 &&
-              !(ok = wait(o_full + 8 * (b ^ 1), ((g - 1) >> 1) & 1)))
-            break;
+          // (the ring slots may still belong to the previous tile's values
+          // until its product is complete)
+          if (t > W.t0 && !(ok = wait(o_full + 8 * (b ^ 1), ((g - 1) >> 1) & 1))) break;
           const int j = t - W.t0;
-          const uint32_t at = units + NC * (NSB == 1 ? 2 * j + 1 : min(2 * j + 2, 2 * tiles - 1));
-          for (int c = 0; c < NC && ok; ++c) {
-            const uint32_t u = at + c, s = u % NS;
-            if (!(ok = wait(full + 8 * s, (u / NS) & 1))) break;
-            uint4* vrow = reinterpret_cast<uint4*>(smem + C::RING + s * kUnit + tid * 128);
-            for (int k = 0; k < 8; ++k) {
-              uint4& w = vrow[(k + lane) & 7];  // all banks at once
-              if (tid >= nv) {
-                w = make_uint4(0, 0, 0, 0);
-              } else if (cut) {
-                uint4 v = w;
-                const uint4 bad = make_uint4(not_finite<T>(v.x), not_finite<T>(v.y),
-                                             not_finite<T>(v.z), not_finite<T>(v.w));
-                if (bad.x | bad.y | bad.z | bad.w) {
-                  words[2 + (items & 1)] = 1;
-                  w = make_uint4(v.x & ~bad.x, v.y & ~bad.y, v.z & ~bad.z, v.w & ~bad.w);
+          const uint32_t at = units + NU * min(2 * j + 2, 2 * tiles - 1);
+          const int key = tid & (kAttnKeys - 1);
+          for (int u = 0; u < NU && ok; ++u) {
+            const uint32_t s = (at + u) % NS;
+            if (!(ok = wait(full + 8 * s, ((at + u) / NS) & 1))) break;
+            for (int c = tid / kAttnKeys; c < CU; c += 2) {
+              uint4* vrow =
+                  reinterpret_cast<uint4*>(smem + C::RING + s * UNIT + c * kChunk + key * 128);
+              for (int k = 0; k < 8; ++k) {
+                uint4& w = vrow[(k + lane) & 7];  // all banks at once
+                if (key >= nv) {
+                  w = make_uint4(0, 0, 0, 0);
+                } else if (cut) {
+                  const uint4 v = w;
+                  const uint4 bad = make_uint4(not_finite<T>(v.x), not_finite<T>(v.y),
+                                               not_finite<T>(v.z), not_finite<T>(v.w));
+                  if (bad.x | bad.y | bad.z | bad.w) {
+                    words[2 + items % 3] = 1;
+                    w = make_uint4(v.x & ~bad.x, v.y & ~bad.y, v.z & ~bad.z, v.w & ~bad.w);
+                  }
                 }
               }
             }
           }
+          __syncwarp();
           fence_async_smem();
           if (!ok) break;
         }
@@ -550,14 +562,13 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
         if (lane == 0) mbar_arrive(p_ready + 8 * b);
       }
       if (!ok) break;
-      units += 2 * NC * tiles;
+      if (more) publish_q();
+      units += 2 * NU * tiles;
       const int last = g - 1;
-      if (!(ok = wait(o_full + 8 * (NSB == 2 ? last & 1 : 0),
-                          (NSB == 2 ? last >> 1 : last) & 1)))
-        break;
+      if (!(ok = wait(o_full + 8 * (last & 1), (last >> 1) & 1))) break;
       tc_fence_after();
       // whether an infinite or NaN value was taken out of a tile of this item
-      const bool strange = words[2 + (items & 1)] != 0;
+      const bool strange = words[2 + items % 3] != 0;
       if (rows_here) {
         const bool direct = it.kind == ITEM_OWN && !W.split();
         const bool mine = tid < it.m_cnt;
@@ -606,6 +617,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
         if (mine && !direct) pml[part] = make_float2(m * c2, l);
       }
       tc_fence_before();
+      W = N;
     }
   }
   __syncthreads();

@@ -5,7 +5,7 @@
 // head, with the keys they read: of one request (its own keys), or of a group
 // (the keys that its requests share, the rows of all its requests side by
 // side). Items repeat for every key/value head; item q = item * Hkv + head.
-// The items lie end to end on a line of cost (kTileCost per tile of 128 keys,
+// The items lie end to end on a line of cost (kTileCost per tile of 64 keys,
 // kItemCost per item and head) that is cut into equal shares, one per CTA, so
 // every CTA has the same work whatever the lengths are. An item that crosses a
 // share's end is finished by the next CTA; the pieces are joined afterwards.
@@ -16,8 +16,8 @@
 namespace gdn {
 
 constexpr int kAttnM = 128;      // (row, head) pairs of an item: the tensor core's M
-constexpr int kAttnKeys = 128;   // keys of a tile
-constexpr unsigned kTileCost = 4, kItemCost = 3;
+constexpr int kAttnKeys = 64;    // keys of a tile
+constexpr unsigned kTileCost = 4, kItemCost = 12;
 // A request joins its group's shared pass with up to this many (row, head)
 // pairs; above, its own tiles are full enough to read the shared keys alone.
 constexpr int kJoinRows = 64;
@@ -29,7 +29,7 @@ enum { ITEM_OWN = 0, ITEM_JOINED = 1, ITEM_GROUP = 2 };
 struct AttnItem {
   unsigned long long off;  // of head 0 on the cost line
   uint32_t cost;           // of each head
-  int32_t tiles;           // of 128 keys, from k0 on
+  int32_t tiles;           // of 64 keys, from k0 on
   int32_t row_base;        // first packed row (own), first entry of the row list (group)
   int32_t m0, m_cnt;       // the tile's place among the item's (row, head) pairs
   int32_t req;             // whose page table is read
@@ -100,7 +100,7 @@ cudaError_t launch_attn_plan(const AttnDims& A, const KvBatch& B, void* plan, in
 cudaError_t launch_attn_join(const AttnDims& A, const KvBatch& B, int io, const void* plan,
                              const void* ws, void* o, float* lse, cudaStream_t s);
 // tk, tv: CUtensorMaps of the caches (16-bit elements, [pages][Hkv * page_size][D],
-// boxes of 64 elements x min(page_size, 128) tokens, 128-byte swizzle).
+// boxes of 64 elements x min(page_size, 64) tokens, 128-byte swizzle).
 cudaError_t launch_attn(const void* tk, const void* tv, const AttnDims& A, const KvBatch& B,
                         int io, const void* plan, const void* q, long long qs, const void* vc,
                         void* o, float* lse, void* ws, int32_t* status, cudaStream_t s);
