@@ -198,41 +198,42 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
 // The items of one CTA, walked alike by every role.
 struct Walk {
   const AttnPlan* P;
-  int Hkv, G, c, q, Q, item, head;
-  unsigned long long share, off;
+  int Hkv, c, q, Q, item, head;
+  unsigned long long share;
   AttnItem it;
+  AttnSpan span;
   int t0, t1;
 
   __device__ __forceinline__ Walk(const AttnPlan& P_, const AttnDims& A)
-      : P(&P_), Hkv(A.Hkv), G(A.G), c(blockIdx.x) {
+      : P(&P_), Hkv(A.Hkv), c(blockIdx.x) {
     share = P->head->share;
-    Q = P->head->items * Hkv;
-    q = P->qfirst[c];
-    // the item that holds the start of the share; if an item starts right
-    // there or the previous one ended before it, q is already that one
-    Q = uniform(Q);
-    q = uniform(q);
+    Q = uniform(P->head->items * Hkv);
+    q = uniform(P->qfirst[c]);  // the item that holds the start of the share
     item = q / Hkv;
-    head = q - item * Hkv;
-    --head;
+    head = q - item * Hkv - 1;
     --q;
   }
-  __device__ __forceinline__ bool next() {
+  // The next piece with tiles; `empty` is called for those without (a share's
+  // end can fall so close to an item's that no tile is left).
+  template <class F>
+  __device__ __forceinline__ bool next(F empty) {
     while (true) {
       ++q;
       if (++head == Hkv) head = 0, ++item;
       if (q >= Q) return false;
+      span = P->spans[q];
+      if (uniform(span.c0) > c) return false;
       it = P->items[item];
-      off = it.off + (unsigned long long)head * it.cost;
-      if (off >= (unsigned long long)(c + 1) * share) return false;
-      piece_tiles(it, off, share, c, t0, t1);
+      piece_tiles(it, it.off + (unsigned long long)head * it.cost, share, span, c, t0, t1);
       t0 = uniform(t0), t1 = uniform(t1);
       if (t0 < t1) return true;
+      empty();
     }
   }
-  __device__ __forceinline__ bool split() const {
-    return off / share != (off + it.cost - 1) / share;
+  __device__ __forceinline__ bool next() {
+    return next([] {});
   }
+  __device__ __forceinline__ bool split() const { return span.c0 != span.c1; }
 };
 
 }  // namespace
@@ -433,14 +434,22 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
       if (lane == 0) mbar_arrive(q_full);
     };
 
-    bool ok = true, more = W.next();
+    // the next piece; one without tiles adds nothing to its rows
+    auto advance = [&](Walk& V) {
+      return V.next([&] {
+        if (tid < V.it.m_cnt)
+          pml[partial_row(P, V.it, V.head, A.Hq, A.G, V.span, V.c, tid)] =
+              make_float2(-INFINITY, 0.0f);
+      });
+    };
+    bool ok = true, more = advance(W);
     if (more) {
       fetch_q(W);
       publish_q();
     }
     for (; more; ++items) {
       Walk N = W;
-      more = N.next();
+      more = advance(N);
       const AttnItem& it = W.it;
       const bool rows_here = it.m_cnt > warp * 32;
       int i, hq;
@@ -574,7 +583,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
         const bool mine = tid < it.m_cnt;
         const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
         const long long part =
-            direct || !mine ? 0 : partial_row(P, it, W.head, A.Hq, A.G, W.off, W.share, W.c, tid);
+            direct || !mine ? 0 : partial_row(P, it, W.head, A.Hq, A.G, W.span, W.c, tid);
         T* dst = o + (row * A.Hq + hq) * D;
         float* pdst = po + part * D;
         const bool wide = (((uintptr_t)o | (uintptr_t)po) & 31) == 0;
@@ -632,7 +641,7 @@ cudaError_t go(const void* tk, const void* tv, const AttnDims& A, const KvBatch&
                void* ws, int32_t* status, cudaStream_t s) {
   constexpr int bytes = Cfg<D>::BYTES;
   const AttnLayout L = attn_layout(A, B);
-  const AttnPlan P = attn_plan_view(L, B, plan);
+  const AttnPlan P = attn_plan_view(L, plan);
   cudaError_t e = ensure_smem_limit<attn_kernel<T, D>>(bytes);
   if (e != cudaSuccess) return e;
   e = launch_pdl(attn_kernel<T, D>, dim3(L.ctas), dim3(kAttnThreads), bytes, s,

@@ -22,6 +22,7 @@ AttnLayout attn_layout(const AttnDims& A, const KvBatch& B) {
   size_t at = up(sizeof(AttnHead));
   L.qfirst = at, at = up(at + 4 * ((size_t)L.ctas + 1));
   L.items = at, at = up(at + sizeof(AttnItem) * (size_t)L.max_items);
+  L.spans = at, at = up(at + sizeof(AttnSpan) * (size_t)L.max_items * A.Hkv);
   L.list = at, at = up(at + sizeof(AttnRow) * (size_t)L.max_list);
   L.first_item = at, at = up(at + 4 * ((size_t)L.ents + 1));
   L.k0 = at, at = up(at + 4 * (size_t)B.R);
@@ -73,6 +74,7 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
   AttnHead* head = (AttnHead*)plan;
   int32_t* qfirst = (int32_t*)(plan + L.qfirst);
   AttnItem* items = (AttnItem*)(plan + L.items);
+  AttnSpan* spans = (AttnSpan*)(plan + L.spans);
   AttnRow* list = (AttnRow*)(plan + L.list);
   int32_t* first_item = (int32_t*)(plan + L.first_item);
   int32_t* req_k0 = (int32_t*)(plan + L.k0);
@@ -95,7 +97,7 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
     req_k0[r] = 0;
     req_list[r] = -1;
   }
-  for (int i = tid; i < L.max_list; i += kPlanThreads) list[i].req = -1;
+  for (int i = tid; i < L.max_list; i += kPlanThreads) list[i].own_item = -1;
   // groups: the keys that every joining member's rows all see, in whole pages
   for (int g = warp; g < NG; g += kPlanThreads / 32) {
     const int a = B.group_start[g], n = B.group_len[g];
@@ -155,7 +157,7 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
         req_k0[r] = shared;
         req_list[r] = off + pos;
         for (int i = 0; i < len; ++i)
-          list[off + pos + i] = AttnRow{start + i, r, g, i * A.G, (pos + i) * A.G, {0, 0, 0}};
+          list[off + pos + i] = AttnRow{start + i, r, g, i * A.G, (pos + i) * A.G, {0, 0, 0}};  // see below
       }
       at += __shfl_sync(~0u, x, 31);
     }
@@ -202,7 +204,7 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
         it.row_base = g_off[lo];
         it.m_cnt = min(kAttnM, g_rows[lo] * A.G - it.m0);
         it.kend = g_shared[lo];
-        it.req = list[it.row_base].req;
+        it.req = list[it.row_base].own_item;
       } else {
         int start, len, kv;
         it.req = lo - NG;
@@ -234,8 +236,16 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
     const int i = q / A.Hkv;
     const uint32_t cost = items[i].cost;
     const unsigned long long off = items[i].off + (unsigned long long)(q - i * A.Hkv) * cost;
-    for (unsigned long long c = (off + share - 1) / share; c * share < off + cost; ++c)
-      qfirst[c] = q;
+    const int c0 = (int)(off / share), c1 = (int)((off + cost - 1) / share);
+    spans[q] = AttnSpan{c0, c1};
+    for (int c = (unsigned long long)c0 * share == off ? c0 : c0 + 1; c <= c1; ++c) qfirst[c] = q;
+  }
+  // the list's entries name a request and a group so far: now their items
+  for (int i = tid; i < min(list_rows, L.max_list); i += kPlanThreads) {
+    const AttnRow lr = list[i];
+    if (lr.own_item < 0) continue;
+    list[i].own_item = first_item[NG + lr.own_item];
+    list[i].group_item = first_item[lr.group_item];
   }
 }
 
@@ -250,103 +260,103 @@ cudaError_t launch_attn_plan(const AttnDims& A, const KvBatch& B, void* plan, in
 // Pieces of a row hold m (the maximum, in base-2 exponent units), l = sum
 // 2^{s - m} and o = sum 2^{s - m} v, so with M = max m
 //   o = sum 2^{m_p - M} o_p / sum 2^{m_p - M} l_p.
-// One warp per (row, query head): the lanes fetch the pieces' m and l at
-// once, then the warp adds up the pieces' o in their order. Blocks
-// [0, 4 ctas) take the items that are cut by a share's end, the others the
-// rows of the list.
+// A warp per (row, query head): the lanes fetch the pieces' m and l at once,
+// then the warp adds up the pieces' o in their order. Blocks [0, 4 ctas) take
+// the items that are cut by a share's end, the others the rows of the list. What a warp reads of
+// the plan it reads before the attention kernel ends (the plan was complete
+// when that kernel began), so only the pieces' own latency follows.
 
 constexpr int kJoinWarps = 4;
 
-struct JoinPart {
-  int n, c0;  // pieces, and the CTA of the first
-};
-
 template <class T, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps)
-attn_join_kernel(AttnDims A, AttnPlan P, const float* po, const float2* pml, T* o, float* lse) {
+attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
+                 const float2* __restrict__ pml, T* __restrict__ o, float* __restrict__ lse) {
   constexpr int E = D / 32;
-  pdl_begin();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, Q = P.head->items * A.Hkv;
-  const unsigned long long share = P.head->share;
-  int q1 = -1, q2 = -1, m1 = 0, m2 = 0, row = 0, hq = 0, step = 0, m_end = 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int split_blocks = 4 * P.ctas;
-  if ((int)blockIdx.x < split_blocks) {
+  const bool cut = (int)blockIdx.x < split_blocks;
+  int q1 = 0, head = 0, m1 = 0, m2 = 0, m_end = 0, step = 1, row = 0, hq = 0;
+  bool work = false;
+  AttnItem it1{}, it2{};
+  AttnSpan s1{0, 0}, s2{0, -1};
+  if (cut) {
     const int c = blockIdx.x >> 2;
     q1 = P.qfirst[c + 1];  // holds the start of share c + 1
-    if (q1 >= Q) return;
-    const AttnItem& it = P.items[q1 / A.Hkv];
-    const unsigned long long off = it.off + (unsigned long long)(q1 % A.Hkv) * it.cost;
-    // cut there, begun in share c, and not joined with another item
-    if (it.kind != ITEM_OWN || off == (c + 1) * share || off / share != (unsigned long long)c)
-      return;
-    m1 = (blockIdx.x & 3) * kJoinWarps + warp;
-    m_end = it.m_cnt;
-    step = 4 * kJoinWarps;
+    if (q1 < P.head->items * A.Hkv) {
+      it1 = P.items[q1 / A.Hkv];
+      s1 = P.spans[q1];
+      head = q1 % A.Hkv;
+      // cut there, begun in share c, and not joined with another item (an
+      // item that begins exactly there has its first piece in share c + 1)
+      work = it1.kind == ITEM_OWN && s1.c0 == c && s1.c1 > c;
+      m1 = (blockIdx.x & 3) * kJoinWarps + warp;
+      m_end = it1.m_cnt;
+      step = 4 * kJoinWarps;
+    }
   } else {
     const int idx = (blockIdx.x - split_blocks) * kJoinWarps + warp;
     const int i = idx / A.Hq;
-    if (i >= P.head->list_rows) return;
-    const AttnRow lr = P.list[i];
-    if (lr.req < 0) return;
-    hq = idx - i * A.Hq;
-    row = lr.row;
-    const int head = hq / A.G, hg = hq - head * A.G;
-    q1 = P.first_item[P.num_groups + lr.req] * A.Hkv + head;
-    m1 = lr.own_m + hg;
-    const int gm = lr.group_m + hg;
-    q2 = (P.first_item[lr.group] + gm / kAttnM) * A.Hkv + head;
-    m2 = gm % kAttnM;
-    m_end = m1 + 1;
-    step = 1;
+    if (i < P.head->list_rows) {
+      const AttnRow lr = P.list[i];
+      if (lr.own_item >= 0) {
+        work = true;
+        hq = idx - i * A.Hq;
+        head = hq / A.G;
+        const int hg = hq - head * A.G;
+        row = lr.row;
+        q1 = lr.own_item * A.Hkv + head;
+        it1 = P.items[lr.own_item];
+        s1 = P.spans[q1];
+        m1 = lr.own_m + hg;
+        m_end = m1 + 1;
+        const int gm = lr.group_m + hg, gi = lr.group_item + gm / kAttnM;
+        m2 = gm % kAttnM;
+        it2 = P.items[gi];
+        s2 = P.spans[gi * A.Hkv + head];
+      }
+    }
   }
-  const AttnItem it1 = P.items[q1 / A.Hkv], it2 = P.items[(q2 < 0 ? q1 : q2) / A.Hkv];
-  const int h1 = q1 % A.Hkv, h2 = q2 < 0 ? 0 : q2 % A.Hkv;
-  const unsigned long long off1 = it1.off + (unsigned long long)h1 * it1.cost;
-  const unsigned long long off2 = it2.off + (unsigned long long)h2 * it2.cost;
-  const JoinPart p1{(int)((off1 + it1.cost - 1) / share - off1 / share) + 1, (int)(off1 / share)};
-  const JoinPart p2{q2 < 0 ? 0 : (int)((off2 + it2.cost - 1) / share - off2 / share) + 1,
-                    (int)(off2 / share)};
+  pdl_begin();
+  if (!work) return;
   for (; m1 < m_end; m1 += step) {
-    if (q2 < 0) {
+    if (cut) {
       const int mi = it1.m0 + m1, i = mi / A.G;
       row = it1.row_base + i;
-      hq = h1 * A.G + mi - i * A.G;
+      hq = head * A.G + mi - i * A.G;
     }
+    const int n1 = s1.c1 - s1.c0 + 1, n = n1 + s2.c1 - s2.c0 + 1;
     float top = -INFINITY, sum = 0.0f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    for (int b = 0; b < p1.n + p2.n; b += 32) {
+    for (int b = 0; b < n; b += 32) {
       const int p = b + lane;
-      long long at = -1;
-      if (p < p1.n + p2.n) {
-        const bool own = p < p1.n;
-        const int c = own ? p1.c0 + p : p2.c0 + p - p1.n;
-        int t0, t1;
-        piece_tiles(own ? it1 : it2, own ? off1 : off2, share, c, t0, t1);
-        if (t0 < t1)
-          at = own ? partial_row(P, it1, h1, A.Hq, A.G, off1, share, c, m1)
-                   : partial_row(P, it2, h2, A.Hq, A.G, off2, share, c, m2);
+      long long at = 0;
+      float2 ml = make_float2(-INFINITY, 0.0f);
+      if (p < n) {
+        at = p < n1 ? partial_row(P, it1, head, A.Hq, A.G, s1, s1.c0 + p, m1)
+                    : partial_row(P, it2, head, A.Hq, A.G, s2, s2.c0 + p - n1, m2);
+        ml = pml[at];
       }
-      const float2 ml = at >= 0 ? pml[at] : make_float2(-INFINITY, 0.0f);
       float mx = ml.x;
 #pragma unroll
       for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
       const float nt = fmaxf(top, mx), ref = nt == -INFINITY ? 0.0f : nt;
-      const float back = exp2f(top - ref);
-      const float w = at >= 0 ? exp2f(ml.x - ref) : 0.0f;
-      float s = at >= 0 ? w * ml.y : 0.0f;
+      const float back = exp2f(top - ref), w = exp2f(ml.x - ref);
+      float s = w * ml.y;
 #pragma unroll
       for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
       sum = sum * back + s;
       top = nt;
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] *= back;
-      const int n = min(32, p1.n + p2.n - b);
+      const int k_end = min(32, n - b);
 #pragma unroll 4
-      for (int k = 0; k < n; ++k) {
+      for (int k = 0; k < k_end; ++k) {
         const long long from = __shfl_sync(~0u, at, k);
         const float wk = __shfl_sync(~0u, w, k);
-        if (from < 0) continue;
+        // a piece without tiles has weight 0 and no o
+        if (wk == 0.0f) continue;
         float v[E];
         const float* src = po + from * D + lane * E;
         if constexpr (E == 2) {
@@ -365,8 +375,8 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* po, const float2* pml, T* 
     for (int e = 0; e < E; e += 2) out[e / 2] = pack2<T>(acc[e] * inv, acc[e + 1] * inv);
     T* dst = o + ((size_t)row * A.Hq + hq) * D + lane * E;
     if constexpr (E == 2) *(uint32_t*)dst = out[0];
-    else if constexpr (E == 4) *(uint2*)dst = *(uint2*)out;
-    else *(uint4*)dst = *(uint4*)out;
+    else if constexpr (E == 4) *(uint2*)dst = make_uint2(out[0], out[1]);
+    else *(uint4*)dst = make_uint4(out[0], out[1], out[2], out[3]);
     if (lse && lane == 0)
       lse[(size_t)row * A.Hq + hq] = (top + log2f(sum)) * 0.693147180559945309f;
   }
@@ -375,7 +385,7 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* po, const float2* pml, T* 
 cudaError_t launch_attn_join(const AttnDims& A, const KvBatch& B, int io, const void* plan,
                              const void* ws, void* o, float* lse, cudaStream_t s) {
   const AttnLayout L = attn_layout(A, B);
-  const AttnPlan P = attn_plan_view(L, B, plan);
+  const AttnPlan P = attn_plan_view(L, plan);
   const float* po = (const float*)ws;
   const float2* pml = (const float2*)((const char*)ws + L.ws_ml);
   const long long rows = (long long)L.max_list * A.Hq;

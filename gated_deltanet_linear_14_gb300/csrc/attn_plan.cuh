@@ -17,7 +17,7 @@ namespace gdn {
 
 constexpr int kAttnM = 128;      // (row, head) pairs of an item: the tensor core's M
 constexpr int kAttnKeys = 64;    // keys of a tile
-constexpr unsigned kTileCost = 4, kItemCost = 12;
+constexpr unsigned kTileCost = 4, kItemCost = 20;
 // A request joins its group's shared pass with up to this many (row, head)
 // pairs; above, its own tiles are full enough to read the shared keys alone.
 constexpr int kJoinRows = 64;
@@ -43,9 +43,15 @@ static_assert(sizeof(AttnItem) == 64, "one item is 64 bytes");
 
 // A row of the list: rows of requests that join a group's pass.
 struct AttnRow {
-  int32_t row, req, group;
+  int32_t row;
+  int32_t own_item, group_item;  // the request's item (-1: none) and the group's first
   int32_t own_m, group_m;  // of its head 0 in the request's item and among the group's pairs
   int32_t pad[3];
+};
+
+// The CTAs that hold the first and the last piece of item q.
+struct AttnSpan {
+  int32_t c0, c1;
 };
 
 struct AttnHead {
@@ -56,7 +62,7 @@ struct AttnHead {
 // Byte offsets inside the plan, and the bounds they come from.
 struct AttnLayout {
   int ctas, max_items, max_list, ents;  // ents: groups, then requests
-  size_t qfirst, items, list, first_item, k0, req_list, g_shared, g_rows, g_off, bytes;
+  size_t qfirst, items, spans, list, first_item, k0, req_list, g_shared, g_rows, g_off, bytes;
   size_t ws_ml, ws_bytes;  // partial rows: fp32 o, then (m, l)
   long long ws_rows;
 };
@@ -65,9 +71,9 @@ struct AttnPlan {
   const AttnHead* head;
   const int32_t* qfirst;      // [ctas + 1]: the item that holds the start of a CTA's share
   const AttnItem* items;
+  const AttnSpan* spans;      // of item q
   const AttnRow* list;
-  const int32_t* first_item;  // [ents + 1]
-  int ctas, max_list, ents, num_groups;
+  int ctas, max_list;
 };
 
 // Partial rows of an item piece: where piece `c` of item q keeps row m (own
@@ -75,22 +81,21 @@ struct AttnPlan {
 // at most one item that began before its share and one that goes on after
 // it); whole items that are joined with others: by list row and query head.
 __device__ __forceinline__ long long partial_row(const AttnPlan& P, const AttnItem& it, int head,
-                                                 int Hq, int G, unsigned long long off,
-                                                 unsigned long long share, int c, int m) {
-  const unsigned long long c0 = off / share, c1 = (off + it.cost - 1) / share;
-  if (c0 != c1) return (long long)(2 * c + (c == (int)c0 ? 1 : 0)) * kAttnM + m;
+                                                 int Hq, int G, AttnSpan sp, int c, int m) {
+  if (sp.c0 != sp.c1) return (long long)(2 * c + (c == sp.c0 ? 1 : 0)) * kAttnM + m;
   const int mi = it.m0 + m, i = mi / G, hq = head * G + mi - i * G;
   const long long base = (long long)2 * P.ctas * kAttnM;
   if (it.kind == ITEM_JOINED) return base + (long long)(it.list + i) * Hq + hq;
   return base + ((long long)P.max_list + it.row_base + i) * Hq + hq;
 }
 
-// Tiles [t0, t1) of an item that CTA c has.
+// Tiles [t0, t1) of the item at `off` on the cost line that CTA c has.
 __device__ __forceinline__ void piece_tiles(const AttnItem& it, unsigned long long off,
-                                            unsigned long long share, int c, int& t0, int& t1) {
-  const unsigned long long a = (unsigned long long)c * share, b = a + share, e = off + it.cost;
-  t0 = a <= off ? 0 : (int)((a - off) * it.tiles / it.cost);
-  t1 = b >= e ? it.tiles : (int)((b - off) * it.tiles / it.cost);
+                                            unsigned long long share, AttnSpan sp, int c, int& t0,
+                                            int& t1) {
+  const unsigned long long a = (unsigned long long)c * share;
+  t0 = c == sp.c0 ? 0 : (int)((a - off) * it.tiles / it.cost);
+  t1 = c == sp.c1 ? it.tiles : (int)((a + share - off) * it.tiles / it.cost);
 }
 
 int attn_ctas_per_sm(int D);
@@ -105,11 +110,11 @@ cudaError_t launch_attn(const void* tk, const void* tv, const AttnDims& A, const
                         int io, const void* plan, const void* q, long long qs, const void* vc,
                         void* o, float* lse, void* ws, int32_t* status, cudaStream_t s);
 
-inline AttnPlan attn_plan_view(const AttnLayout& L, const KvBatch& B, const void* plan) {
+inline AttnPlan attn_plan_view(const AttnLayout& L, const void* plan) {
   const char* p = (const char*)plan;
   return AttnPlan{(const AttnHead*)p, (const int32_t*)(p + L.qfirst),
-                  (const AttnItem*)(p + L.items), (const AttnRow*)(p + L.list),
-                  (const int32_t*)(p + L.first_item), L.ctas, L.max_list, L.ents, B.num_groups};
+                  (const AttnItem*)(p + L.items), (const AttnSpan*)(p + L.spans),
+                  (const AttnRow*)(p + L.list), L.ctas, L.max_list};
 }
 
 }  // namespace gdn
