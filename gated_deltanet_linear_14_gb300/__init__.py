@@ -108,11 +108,14 @@ class KvBatch(ctypes.Structure):
 
 _lock = threading.Lock()
 _lib = None
+_raw_stream = None  # -> handle of the current stream
 
 
 def load_library(path: str = LIB_PATH):
     """Load libgdn.so (raises if it was not built: there is no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -171,8 +174,18 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: building a Stream object costs as much as a launch
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            raw, device = (getattr(torch._C, n, None) for n in
+                           ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+            if raw is not None and device is not None:
+                torch.cuda.init()
+                _raw_stream = lambda: raw(device())  # noqa: E731
+            else:
+                _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        return _raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -323,10 +336,11 @@ def _rows(t):
     contiguous within a row, e.g. a slice of a projection's output."""
     if t is None:
         return None, 0
-    heads, dim = t.shape[1], t.shape[2]
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+    rows, heads, dim = t.shape
+    between, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != dim):
         raise GdnError(CODES["GDN_ERR_INVALID_ARG"], "row tensor: heads not contiguous")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else heads * dim)
+    return t.data_ptr(), (between if rows > 1 else heads * dim)
 
 
 def gdn_rope(dims, rope, q, q_out, k=None, k_out=None, inverse=False, stream=None):

@@ -4,17 +4,18 @@
 // A pair (x, y) of a head turns by the angle t = position * inv_freq:
 //   x' = x cos t - y sin t,  y' = y cos t + x sin t.
 // Both calls move every element once each way and do six flops a pair, so
-// they are bound by memory: a block stages the cosines and sines of its rows
-// in shared memory (one evaluation per row and pair, shared by all heads),
-// then every thread keeps its pairs' values in registers and streams the
-// heads of one row through, four heads in flight at a time.
+// they are bound by memory: a block evaluates the cosines and sines of its
+// rows once (one evaluation per row and pair, in shared memory, for all
+// heads) while the first heads' loads are in flight, then every thread keeps
+// its pairs' values in registers and streams its heads of one row through.
 #include "attn.cuh"
 #include "kernels.h"
 
 namespace gdn {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeHeads = 4;  // heads a thread has in flight
+constexpr int kRopeThreads = 128;
+constexpr int kRopeBlocks = 8;  // per SM: 64 registers a thread
+constexpr int kRopeHeads = 2;  // heads a thread has in flight: 64 bytes
 
 // cos and sin of pos * f. The product is formed in turns, f / (2 pi) as a sum
 // of two fp32 values, and the position in two parts (upper bits and lower 12)
@@ -40,19 +41,52 @@ __device__ __forceinline__ float2 cos_sin(int pos, float f) {
 // first rd / (2 VEC) units hold VEC pairs each (half pairing: elements VEC u
 // and rd/2 + VEC u on; interleaved: 2 VEC u on), the others pass through.
 template <class T, int VEC, bool INTER, bool APPEND>
-__global__ void __launch_bounds__(kRopeThreads)
-rope_kernel(RopeCall C, Rope P, AttnDims A, KvBatch B, int U, int TY, int RB, int32_t* status) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
+rope_kernel(RopeCall C, Rope P, AttnDims A, KvBatch B, int U, int TY, int RB, int packed,
+            int32_t* status) {
   extern __shared__ float2 cs_tab[];  // [RB][rd / 2]
   pdl_begin();
-  const int half = P.rd >> 1;
+  const int half = P.rd >> 1, tid = threadIdx.x;
   long long row0 = (long long)blockIdx.x * RB;
   int rows = 0, kv0 = 0;
   const int32_t* table = nullptr;
   if (APPEND) {
-    const int r = blockIdx.y;
+    int r = blockIdx.y;
+    if (packed) {
+      // the request that holds this block among all requests' blocks of RB rows
+      __shared__ int found[2], sums[kRopeThreads / 32];
+      const int lane = tid & 31, w = tid >> 5, bx = blockIdx.x;
+      if (tid == 0) found[0] = -1;
+      int at = 0;
+      for (int r0 = 0; r0 < B.R && at <= bx; r0 += kRopeThreads) {
+        const int len = r0 + tid < B.R ? B.row_len[r0 + tid] : 0;
+        // (a length out of bounds has one block, which reports it)
+        const int n = len < 0 || len > B.max_rows ? 1 : (len + RB - 1) / RB;
+        int x = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int y = __shfl_up_sync(~0u, x, d);
+          if (lane >= d) x += y;
+        }
+        if (lane == 31) sums[w] = x;
+        __syncthreads();
+        int before = at, all = 0;
+        for (int k = 0; k < kRopeThreads / 32; ++k) {
+          if (k < w) before += sums[k];
+          all += sums[k];
+        }
+        const int first = before + x - n;
+        if (first <= bx && bx < first + n) found[0] = r0 + tid, found[1] = bx - first;
+        at += all;
+        __syncthreads();
+      }
+      if (found[0] < 0) return;
+      r = found[0];
+      row0 = (long long)found[1] * RB;
+    }
     const int start = B.row_start[r], len = B.row_len[r], kv = B.kv_len[r];
     if (!kv_request_ok(B, A.ps, start, len, kv)) {
-      if (blockIdx.x == 0 && threadIdx.x == 0) report(status, GDN_DEV_BAD_ROWS);
+      if (row0 == 0 && tid == 0) report(status, GDN_DEV_BAD_ROWS);
       return;
     }
     if (row0 >= len) return;
@@ -63,97 +97,100 @@ rope_kernel(RopeCall C, Rope P, AttnDims A, KvBatch B, int U, int TY, int RB, in
   } else {
     rows = (int)min((long long)RB, C.num_rows - row0);
   }
-  for (int i = threadIdx.x; i < rows * half; i += kRopeThreads) {
-    const int row = i / half, j = i - row * half;
-    int ax = P.axis ? P.axis[j] : 0;
-    if (ax < 0 || ax >= P.axes) ax = 0;
-    const int pos = P.pos[(size_t)ax * P.num_rows + row0 + row];
-    float2 cs = cos_sin(pos, P.inv_freq[j]);
-    cs.y *= P.sign;
-    cs_tab[i] = cs;
-  }
-  __syncthreads();
+  const int D = C.D, Hk = C.Hq + C.Hkv, H = Hk + (APPEND ? C.Hkv : 0);
+  const int n_rot = P.rd / (2 * VEC), total = rows * TY * U;
 
-  const int D = C.D, H = C.Hq + (APPEND ? 2 : 1) * C.Hkv;
-  const int n_rot = P.rd / (2 * VEC);
-  for (int i = threadIdx.x; i < rows * TY * U; i += kRopeThreads) {
-    const int u = i % U, ty = (i / U) % TY, row = i / (U * TY);
-    const long long gr = row0 + row;
-    const bool rot = u < n_rot;
-    const int ea = (INTER || !rot) ? 2 * VEC * u : VEC * u;
-    const int eb = (INTER || !rot) ? ea + VEC : half + VEC * u;
-    // the vectors of a pass-through unit start after the rotated elements:
-    // 2 VEC n_rot = rd, so 2 VEC u is their own offset
+  // (every thread goes through the first turn, in which the table is filled)
+  for (int i = tid; i == tid || i < total; i += kRopeThreads) {
+    const int u = i % U, ty = i / U % TY, row = i / (U * TY);
+    const bool here = i < total, rot = u < n_rot;
+    // a unit that passes through lies at its own offset: the rotated ones hold
+    // rd = 2 VEC n_rot elements together
+    const int pa = 2 * VEC * u, ea = (INTER || !rot) ? pa : VEC * u;
+    const int eb = (INTER || !rot) ? pa + VEC : half + VEC * u;
+    const T *qsrc = nullptr, *ksrc = nullptr, *vsrc = nullptr;
+    T *qdst = nullptr, *kdst = nullptr, *vdst = nullptr;
+    int kstep = D;
+    if (here) {
+      const long long gr = row0 + row;
+      qsrc = (const T*)C.q + gr * C.qs;
+      qdst = (T*)C.q_out + gr * C.qos;
+      ksrc = (const T*)C.k + gr * C.ks;
+      if (APPEND) {
+        vsrc = (const T*)C.v + gr * C.vs;
+        const int at = kv0 + row, page = table[at >> A.ps_log2];
+        if (page >= 0 && page < B.num_pages) {
+          const size_t off = ((size_t)page * C.Hkv * A.ps + (at & (A.ps - 1))) * D;
+          kdst = (T*)C.k_out + off;
+          vdst = (T*)C.v_out + off;
+        } else if (u == 0 && ty == 0) {
+          report(status, GDN_DEV_BAD_PAGE);
+        }
+        kstep = A.ps * D;
+      } else {
+        kdst = (T*)C.k_out + gr * C.kos;
+      }
+    }
+    Vec<T, VEC> a[kRopeHeads], b[kRopeHeads];
+    auto fetch = [&](int h0) {
+#pragma unroll
+      for (int n = 0; n < kRopeHeads; ++n) {
+        const int h = h0 + n * TY;
+        if (!here || h >= H) continue;
+        const bool plain = APPEND && h >= Hk;
+        const T* src = h < C.Hq ? qsrc + h * D : plain ? vsrc + (h - Hk) * D : ksrc + (h - C.Hq) * D;
+        a[n].load(src + (plain ? pa : ea));
+        b[n].load(src + (plain ? pa + VEC : eb));
+      }
+    };
+    fetch(ty);
+    if (i == tid) {
+      for (int x = tid; x < rows * half; x += kRopeThreads) {
+        const int xr = x / half, j = x - xr * half;
+        int ax = P.axis ? P.axis[j] : 0;
+        if (ax < 0 || ax >= P.axes) ax = 0;
+        float2 cs = cos_sin(P.pos[(size_t)ax * P.num_rows + row0 + xr], P.inv_freq[j]);
+        cs.y *= P.sign;
+        cs_tab[x] = cs;
+      }
+      __syncthreads();
+    }
+    if (!here) continue;
     float2 cs[VEC];
     if (rot) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) cs[e] = cs_tab[row * half + VEC * u + e];
     }
-    size_t slot_off = 0;
-    bool write_kv = true;
-    if (APPEND) {
-      const int at = kv0 + row;
-      const int page = table[at >> A.ps_log2];
-      write_kv = page >= 0 && page < B.num_pages;
-      if (!write_kv && u == 0 && ty == 0) report(status, GDN_DEV_BAD_PAGE);
-      slot_off = ((size_t)(write_kv ? page : 0) * C.Hkv * A.ps + (at & (A.ps - 1))) * D;
-    }
-    const T* qsrc = (const T*)C.q + gr * C.qs;
-    const T* ksrc = (const T*)C.k + gr * C.ks;
-    const T* vsrc = (const T*)C.v + gr * C.vs;
-    T* qdst = (T*)C.q_out + gr * C.qos;
-    for (int h0 = ty; h0 < H; h0 += TY * kRopeHeads) {
-      Vec<T, VEC> a[kRopeHeads], b[kRopeHeads];
+    for (int h0 = ty; h0 < H;) {
 #pragma unroll
       for (int n = 0; n < kRopeHeads; ++n) {
         const int h = h0 + n * TY;
-        if (h < H) {
-          const T* src = h < C.Hq ? qsrc + h * D
-                         : (!APPEND || h < C.Hq + C.Hkv) ? ksrc + (h - C.Hq) * D
-                                                         : vsrc + (h - C.Hq - C.Hkv) * D;
-          const bool turned = !APPEND || h < C.Hq + C.Hkv;
-          a[n].load(src + (turned ? ea : 2 * VEC * u));
-          b[n].load(src + (turned ? eb : 2 * VEC * u + VEC));
-        }
-      }
+        if (h >= H) continue;
+        const bool plain = APPEND && h >= Hk;
+        if (!plain && rot) {
 #pragma unroll
-      for (int n = 0; n < kRopeHeads; ++n) {
-        const int h = h0 + n * TY;
-        if (h >= H) break;
-        const bool turned = !APPEND || h < C.Hq + C.Hkv;
-        if (turned && rot) {
-          if (INTER) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              // pair e of the unit: elements 2e, 2e+1 of a|b
-              T& ex = 2 * e < VEC ? a[n].e[(2 * e) % VEC] : b[n].e[(2 * e) % VEC];
-              T& ey = 2 * e + 1 < VEC ? a[n].e[(2 * e + 1) % VEC] : b[n].e[(2 * e + 1) % VEC];
-              const float x = elem_to_f(ex), y = elem_to_f(ey);
-              elem_from_f(x * cs[e].x - y * cs[e].y, ex);
-              elem_from_f(y * cs[e].x + x * cs[e].y, ey);
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
+          for (int e = 0; e < VEC; ++e) {
+            if constexpr (INTER && VEC > 1) {
+              // pair e of the unit: elements 2e, 2e + 1 of a|b
+              Vec<T, VEC>& v = 2 * e < VEC ? a[n] : b[n];
+              const int f = 2 * e < VEC ? 2 * e : 2 * e - VEC;
+              const float x = elem_to_f(v.e[f]), y = elem_to_f(v.e[f + 1]);
+              elem_from_f(x * cs[e].x - y * cs[e].y, v.e[f]);
+              elem_from_f(y * cs[e].x + x * cs[e].y, v.e[f + 1]);
+            } else {
               const float x = elem_to_f(a[n].e[e]), y = elem_to_f(b[n].e[e]);
               elem_from_f(x * cs[e].x - y * cs[e].y, a[n].e[e]);
               elem_from_f(y * cs[e].x + x * cs[e].y, b[n].e[e]);
             }
           }
         }
-        T* dst;
-        if (h < C.Hq) {
-          dst = qdst + h * D;
-        } else if (!APPEND) {
-          dst = (T*)C.k_out + gr * C.kos + (h - C.Hq) * D;
-        } else {
-          if (!write_kv) continue;
-          const int hk = turned ? h - C.Hq : h - C.Hq - C.Hkv;
-          dst = (T*)(turned ? C.k_out : C.v_out) + slot_off + (size_t)hk * A.ps * D;
-        }
-        a[n].store(dst + (turned ? ea : 2 * VEC * u));
-        b[n].store(dst + (turned ? eb : 2 * VEC * u + VEC));
+        T* dst = h < C.Hq ? qdst + h * D : plain ? vdst + (h - Hk) * kstep : kdst + (h - C.Hq) * kstep;
+        if (APPEND && h >= C.Hq && !kdst) continue;
+        a[n].store(dst + (plain ? pa : ea));
+        b[n].store(dst + (plain ? pa + VEC : eb));
       }
+      h0 += TY * kRopeHeads;
+      if (h0 < H) fetch(h0);
     }
   }
 }
@@ -164,23 +201,33 @@ template <class T, int VEC, bool APPEND>
 cudaError_t go(const RopeCall& C, const Rope& P, const AttnDims& A, const KvBatch& B,
                int32_t* status, cudaStream_t s) {
   const int U = C.D / (2 * VEC), H = C.Hq + (APPEND ? 2 : 1) * C.Hkv;
-  // threads over the heads of a row: as many as keep a row within a block,
-  // halved while the rows alone fill the GPU (a thread then reuses its
-  // cosines over more heads)
+  // threads over the heads of a row: about six heads each (a cosine in
+  // registers then serves as many), more threads where the rows are too few to
+  // fill the SMs
+  const long long full = (long long)device_sms() * kRopeBlocks * kRopeThreads;
   int TY = 1;
-  while (2 * TY <= H && 2 * TY * U <= kRopeThreads) TY *= 2;
-  const long long full = (long long)device_sms() * 2048;
-  while (TY > 1 && (long long)C.num_rows * U * (TY / 2) >= 2 * full && H > 2 * TY) TY /= 2;
+  while (2 * TY <= H && 2 * TY * U <= kRopeThreads &&
+         (H > 8 * TY || (long long)C.num_rows * U * TY < full))
+    TY *= 2;
   const int RB = U * TY >= kRopeThreads ? 1 : kRopeThreads / (U * TY);
   const size_t smem = (size_t)RB * (P.rd / 2) * sizeof(float2);
   dim3 grid;
-  if (APPEND) grid = dim3((B.max_rows + RB - 1) / RB, B.R);
-  else grid = dim3((C.num_rows + RB - 1) / RB);
+  int packed = 0;
+  if (APPEND) {
+    // a block per request and RB rows of the longest; where most of those
+    // would be empty (a few prompts among short requests), every block looks
+    // its request up instead, about a microsecond each
+    const long long each = (B.max_rows + RB - 1) / RB, all = (long long)B.num_rows / RB + B.R;
+    packed = each * B.R > 2 * all && B.R <= 4096;
+    grid = packed ? dim3((unsigned)all) : dim3((unsigned)each, B.R);
+  } else {
+    grid = dim3((C.num_rows + RB - 1) / RB);
+  }
   if (C.interleaved)
     return launch_pdl(rope_kernel<T, VEC, true, APPEND>, grid, dim3(kRopeThreads), smem, s, C, P,
-                      A, B, U, TY, RB, status);
+                      A, B, U, TY, RB, packed, status);
   return launch_pdl(rope_kernel<T, VEC, false, APPEND>, grid, dim3(kRopeThreads), smem, s, C, P,
-                    A, B, U, TY, RB, status);
+                    A, B, U, TY, RB, packed, status);
 }
 
 }  // namespace

@@ -364,9 +364,9 @@ def test_attn_on_another_stream():
     c = Cache([1, 8], [3000, 2000], 16, 2, 128, 64, seed=13)
     c.plan()
     ref, _ = c.attn()
-    side = torch.cuda.Stream()
-    side.wait_stream(torch.cuda.current_stream())
     o = torch.zeros_like(ref)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())  # after all that the call reads and writes
     with torch.cuda.stream(side):
         gdn.gdn_attn(c.dims, c.batch, c.plan_buf, c.q, c.k, c.v, o, None, c.ws, c.ws.numel(),
                      c.status)
