@@ -491,13 +491,15 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
           for (int e = 0; e < 64; ++e)
             m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(x[e >> 5].r[e & 31]));
           const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          // (each row by itself: its rounding depends on no other row, nor on
+          // the lanes past the last one)
+          const bool raise = (mx - m) * c2 > kRaise && tid < it.m_cnt;
           if (t == W.t0) {
             m = mx;
-          } else if (__any_sync(~0u, (mx - m) * c2 > kRaise || (m == -INFINITY && mx > m))) {
-            const float nm = fmaxf(m, mx);
-            const float f = nm == -INFINITY ? 1.0f : ex2((m - nm) * c2);
+          } else if (__any_sync(~0u, raise)) {
+            const float f = raise ? ex2((m - mx) * c2) : 1.0f;
             l *= f;
-            m = nm;
+            if (raise) m = mx;
             // O is complete up to the previous tile
             if (!(ok = wait(o_full + 8 * (b ^ 1), ((g - 1) >> 1) & 1))) break;
             tc_fence_after();

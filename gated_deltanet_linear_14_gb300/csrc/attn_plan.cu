@@ -24,6 +24,7 @@ AttnLayout attn_layout(const AttnDims& A, const KvBatch& B) {
   L.items = at, at = up(at + sizeof(AttnItem) * (size_t)L.max_items);
   L.spans = at, at = up(at + sizeof(AttnSpan) * (size_t)L.max_items * A.Hkv);
   L.list = at, at = up(at + sizeof(AttnRow) * (size_t)L.max_list);
+  L.joins = at, at = up(at + sizeof(AttnJoin) * (size_t)L.max_list * A.Hkv);
   L.first_item = at, at = up(at + 4 * ((size_t)L.ents + 1));
   L.k0 = at, at = up(at + 4 * (size_t)B.R);
   L.req_list = at, at = up(at + 4 * (size_t)B.R);
@@ -76,6 +77,7 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
   AttnItem* items = (AttnItem*)(plan + L.items);
   AttnSpan* spans = (AttnSpan*)(plan + L.spans);
   AttnRow* list = (AttnRow*)(plan + L.list);
+  AttnJoin* join = (AttnJoin*)(plan + L.joins);
   int32_t* first_item = (int32_t*)(plan + L.first_item);
   int32_t* req_k0 = (int32_t*)(plan + L.k0);
   int32_t* req_list = (int32_t*)(plan + L.req_list);
@@ -97,7 +99,7 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
     req_k0[r] = 0;
     req_list[r] = -1;
   }
-  for (int i = tid; i < L.max_list; i += kPlanThreads) list[i].own_item = -1;
+  for (int i = tid; i < L.max_list; i += kPlanThreads) list[i].row = -1;
   // groups: the keys that every joining member's rows all see, in whole pages
   for (int g = warp; g < NG; g += kPlanThreads / 32) {
     const int a = B.group_start[g], n = B.group_len[g];
@@ -157,7 +159,7 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
         req_k0[r] = shared;
         req_list[r] = off + pos;
         for (int i = 0; i < len; ++i)
-          list[off + pos + i] = AttnRow{start + i, r, g, i * A.G, (pos + i) * A.G, {0, 0, 0}};  // see below
+          list[off + pos + i] = AttnRow{start + i, r, g, i * A.G, (pos + i) * A.G, {0, 0, 0}};
       }
       at += __shfl_sync(~0u, x, 31);
     }
@@ -204,7 +206,7 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
         it.row_base = g_off[lo];
         it.m_cnt = min(kAttnM, g_rows[lo] * A.G - it.m0);
         it.kend = g_shared[lo];
-        it.req = list[it.row_base].own_item;
+        it.req = list[it.row_base].req;
       } else {
         int start, len, kv;
         it.req = lo - NG;
@@ -240,12 +242,17 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
     spans[q] = AttnSpan{c0, c1};
     for (int c = (unsigned long long)c0 * share == off ? c0 : c0 + 1; c <= c1; ++c) qfirst[c] = q;
   }
-  // the list's entries name a request and a group so far: now their items
-  for (int i = tid; i < min(list_rows, L.max_list); i += kPlanThreads) {
+  __syncthreads();
+  const int joins_n = min(list_rows, L.max_list) * A.Hkv;
+  for (int x = tid; x < joins_n; x += kPlanThreads) {
+    const int i = x / A.Hkv, h = x - i * A.Hkv;
     const AttnRow lr = list[i];
-    if (lr.own_item < 0) continue;
-    list[i].own_item = first_item[NG + lr.own_item];
-    list[i].group_item = first_item[lr.group_item];
+    if (lr.row < 0) continue;
+    const int gi = first_item[lr.group] + lr.group_m / kAttnM;
+    const int gj = first_item[lr.group] + (lr.group_m + A.G - 1) / kAttnM;
+    join[x] = AttnJoin{spans[first_item[NG + lr.req] * A.Hkv + h],
+                       {spans[gi * A.Hkv + h], spans[gj * A.Hkv + h]},
+                       {0, 0}};
   }
 }
 
@@ -261,71 +268,66 @@ cudaError_t launch_attn_plan(const AttnDims& A, const KvBatch& B, void* plan, in
 // 2^{s - m} and o = sum 2^{s - m} v, so with M = max m
 //   o = sum 2^{m_p - M} o_p / sum 2^{m_p - M} l_p.
 // A warp per (row, query head): the lanes fetch the pieces' m and l at once,
-// then the warp adds up the pieces' o in their order. Blocks [0, 4 ctas) take
-// the items that are cut by a share's end, the others the rows of the list. What a warp reads of
+// then the warp adds up the pieces' o in their order. The first blocks take
+// the rows of the list, 4 ctas more the items that are cut by a share's end. What a warp reads of
 // the plan it reads before the attention kernel ends (the plan was complete
 // when that kernel began), so only the pieces' own latency follows.
 
-constexpr int kJoinWarps = 4;
+constexpr int kJoinWarps = 4, kJoinBatch = 4;
 
 template <class T, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
-                 const float2* __restrict__ pml, T* __restrict__ o, float* __restrict__ lse) {
+                 const float2* __restrict__ pml, T* __restrict__ o, float* __restrict__ lse,
+                 int list_blocks) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int split_blocks = 4 * P.ctas;
-  const bool cut = (int)blockIdx.x < split_blocks;
-  int q1 = 0, head = 0, m1 = 0, m2 = 0, m_end = 0, step = 1, row = 0, hq = 0;
+  const bool cut = (int)blockIdx.x >= list_blocks;
+  int head = 0, m1 = 0, m2 = 0, m_end = 0, step = 1, row = 0, hq = 0, entry = 0;
   bool work = false;
-  AttnItem it1{}, it2{};
+  AttnItem it{};
   AttnSpan s1{0, 0}, s2{0, -1};
   if (cut) {
-    const int c = blockIdx.x >> 2;
-    q1 = P.qfirst[c + 1];  // holds the start of share c + 1
-    if (q1 < P.head->items * A.Hkv) {
-      it1 = P.items[q1 / A.Hkv];
-      s1 = P.spans[q1];
-      head = q1 % A.Hkv;
+    const int c = (blockIdx.x - list_blocks) >> 2;
+    const int q = P.qfirst[c + 1];  // holds the start of share c + 1
+    if (q < P.head->items * A.Hkv) {
+      it = P.items[q / A.Hkv];
+      s1 = P.spans[q];
+      head = q % A.Hkv;
       // cut there, begun in share c, and not joined with another item (an
       // item that begins exactly there has its first piece in share c + 1)
-      work = it1.kind == ITEM_OWN && s1.c0 == c && s1.c1 > c;
-      m1 = (blockIdx.x & 3) * kJoinWarps + warp;
-      m_end = it1.m_cnt;
+      work = it.kind == ITEM_OWN && s1.c0 == c && s1.c1 > c;
+      m1 = ((blockIdx.x - list_blocks) & 3) * kJoinWarps + warp;
+      m_end = it.m_cnt;
       step = 4 * kJoinWarps;
     }
   } else {
-    const int idx = (blockIdx.x - split_blocks) * kJoinWarps + warp;
-    const int i = idx / A.Hq;
-    if (i < P.head->list_rows) {
-      const AttnRow lr = P.list[i];
-      if (lr.own_item >= 0) {
-        work = true;
-        hq = idx - i * A.Hq;
-        head = hq / A.G;
-        const int hg = hq - head * A.G;
-        row = lr.row;
-        q1 = lr.own_item * A.Hkv + head;
-        it1 = P.items[lr.own_item];
-        s1 = P.spans[q1];
-        m1 = lr.own_m + hg;
-        m_end = m1 + 1;
-        const int gm = lr.group_m + hg, gi = lr.group_item + gm / kAttnM;
-        m2 = gm % kAttnM;
-        it2 = P.items[gi];
-        s2 = P.spans[gi * A.Hkv + head];
-      }
+    const int idx = blockIdx.x * kJoinWarps + warp;
+    entry = idx / A.Hq;
+    if (entry < P.head->list_rows) {
+      hq = idx - entry * A.Hq;
+      head = hq / A.G;
+      const AttnRow lr = P.list[entry];
+      const AttnJoin jn = P.joins[(long long)entry * A.Hkv + head];
+      const int hg = hq - head * A.G;
+      work = lr.row >= 0;
+      row = lr.row;
+      s1 = jn.own;
+      m1 = lr.own_m + hg;
+      m_end = m1 + 1;
+      s2 = jn.group[(lr.group_m + hg) / kAttnM != lr.group_m / kAttnM ? 1 : 0];
+      m2 = (lr.group_m + hg) % kAttnM;
     }
   }
   pdl_begin();
   if (!work) return;
+  const int n1 = s1.c1 - s1.c0 + 1, n = n1 + s2.c1 - s2.c0 + 1;
   for (; m1 < m_end; m1 += step) {
     if (cut) {
-      const int mi = it1.m0 + m1, i = mi / A.G;
-      row = it1.row_base + i;
+      const int mi = it.m0 + m1, i = mi / A.G;
+      row = it.row_base + i;
       hq = head * A.G + mi - i * A.G;
     }
-    const int n1 = s1.c1 - s1.c0 + 1, n = n1 + s2.c1 - s2.c0 + 1;
     float top = -INFINITY, sum = 0.0f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
@@ -334,8 +336,10 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
       long long at = 0;
       float2 ml = make_float2(-INFINITY, 0.0f);
       if (p < n) {
-        at = p < n1 ? partial_row(P, it1, head, A.Hq, A.G, s1, s1.c0 + p, m1)
-                    : partial_row(P, it2, head, A.Hq, A.G, s2, s2.c0 + p - n1, m2);
+        const AttnSpan sp = p < n1 ? s1 : s2;
+        at = sp.c0 == sp.c1 ? whole_row(P, A.Hq, p >= n1, entry, hq)
+             : p < n1       ? split_row(sp, sp.c0 + p, m1)
+                            : split_row(sp, sp.c0 + p - n1, m2);
         ml = pml[at];
       }
       float mx = ml.x;
@@ -351,22 +355,29 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] *= back;
       const int k_end = min(32, n - b);
-#pragma unroll 4
-      for (int k = 0; k < k_end; ++k) {
-        const long long from = __shfl_sync(~0u, at, k);
-        const float wk = __shfl_sync(~0u, w, k);
-        // a piece without tiles has weight 0 and no o
-        if (wk == 0.0f) continue;
-        float v[E];
-        const float* src = po + from * D + lane * E;
-        if constexpr (E == 2) {
-          *(float2*)v = *(const float2*)src;
-        } else {
+      for (int k = 0; k < k_end; k += kJoinBatch) {
+        float v[kJoinBatch][E], wk[kJoinBatch];
 #pragma unroll
-          for (int e = 0; e < E; e += 4) *(float4*)(v + e) = *(const float4*)(src + e);
+        for (int x = 0; x < kJoinBatch; ++x) {
+          // past the last piece: any row of this chunk, with weight 0
+          const int from_lane = min(k + x, k_end - 1);
+          const long long from = __shfl_sync(~0u, at, from_lane);
+          wk[x] = __shfl_sync(~0u, w, from_lane);
+          if (k + x >= k_end) wk[x] = 0.0f;
+          const float* src = po + from * D + lane * E;
+          if constexpr (E == 2) {
+            *(float2*)v[x] = *(const float2*)src;
+          } else {
+#pragma unroll
+            for (int e = 0; e < E; e += 4) *(float4*)(v[x] + e) = *(const float4*)(src + e);
+          }
         }
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += wk * v[e];
+        for (int x = 0; x < kJoinBatch; ++x) {
+#pragma unroll
+          for (int e = 0; e < E; ++e)  // a piece without tiles has weight 0 and no o
+            acc[e] = wk[x] == 0.0f ? acc[e] : acc[e] + wk[x] * v[x][e];
+        }
       }
     }
     const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
@@ -388,13 +399,14 @@ cudaError_t launch_attn_join(const AttnDims& A, const KvBatch& B, int io, const 
   const AttnPlan P = attn_plan_view(L, plan);
   const float* po = (const float*)ws;
   const float2* pml = (const float2*)((const char*)ws + L.ws_ml);
-  const long long rows = (long long)L.max_list * A.Hq;
-  const dim3 grid((unsigned)(4 * L.ctas + (rows + kJoinWarps - 1) / kJoinWarps));
+  const int list_blocks =
+      (int)(((long long)L.max_list * A.Hq + kJoinWarps - 1) / kJoinWarps);
+  const dim3 grid(list_blocks + 4 * L.ctas);
   const dim3 block(32 * kJoinWarps);
   auto go = [&](auto t, auto d) {
     using T = decltype(t);
     return launch_pdl(attn_join_kernel<T, decltype(d)::value>, grid, block, 0, s, A, P, po, pml,
-                      (T*)o, lse);
+                      (T*)o, lse, list_blocks);
   };
   auto by_dim = [&](auto t) {
     if (A.D == 64) return go(t, std::integral_constant<int, 64>());

@@ -41,17 +41,24 @@ struct AttnItem {
 };
 static_assert(sizeof(AttnItem) == 64, "one item is 64 bytes");
 
+// The CTAs that hold the first and the last piece of item q.
+struct AttnSpan {
+  int32_t c0, c1;
+};
+
 // A row of the list: rows of requests that join a group's pass.
 struct AttnRow {
-  int32_t row;
-  int32_t own_item, group_item;  // the request's item (-1: none) and the group's first
+  int32_t row;             // packed row, -1: none
+  int32_t req, group;
   int32_t own_m, group_m;  // of its head 0 in the request's item and among the group's pairs
   int32_t pad[3];
 };
 
-// The CTAs that hold the first and the last piece of item q.
-struct AttnSpan {
-  int32_t c0, c1;
+// What the join reads of a list row and key/value head: the pieces of the
+// request's item and of the group's (its heads may lie in two tiles).
+struct AttnJoin {
+  AttnSpan own, group[2];
+  int32_t pad[2];
 };
 
 struct AttnHead {
@@ -62,7 +69,7 @@ struct AttnHead {
 // Byte offsets inside the plan, and the bounds they come from.
 struct AttnLayout {
   int ctas, max_items, max_list, ents;  // ents: groups, then requests
-  size_t qfirst, items, spans, list, first_item, k0, req_list, g_shared, g_rows, g_off, bytes;
+  size_t qfirst, items, spans, list, joins, first_item, k0, req_list, g_shared, g_rows, g_off, bytes;
   size_t ws_ml, ws_bytes;  // partial rows: fp32 o, then (m, l)
   long long ws_rows;
 };
@@ -73,6 +80,7 @@ struct AttnPlan {
   const AttnItem* items;
   const AttnSpan* spans;      // of item q
   const AttnRow* list;
+  const AttnJoin* joins;      // of list row * Hkv + head
   int ctas, max_list;
 };
 
@@ -80,13 +88,19 @@ struct AttnPlan {
 // place in the tile). Split pieces: two tiles of 128 rows per CTA (a CTA has
 // at most one item that began before its share and one that goes on after
 // it); whole items that are joined with others: by list row and query head.
+__device__ __forceinline__ long long split_row(AttnSpan sp, int c, int m) {
+  return (long long)(2 * c + (c == sp.c0 ? 1 : 0)) * kAttnM + m;
+}
+__device__ __forceinline__ long long whole_row(const AttnPlan& P, int Hq, bool group, int entry,
+                                               int hq) {
+  return (long long)2 * P.ctas * kAttnM + ((long long)(group ? P.max_list : 0) + entry) * Hq + hq;
+}
 __device__ __forceinline__ long long partial_row(const AttnPlan& P, const AttnItem& it, int head,
                                                  int Hq, int G, AttnSpan sp, int c, int m) {
-  if (sp.c0 != sp.c1) return (long long)(2 * c + (c == sp.c0 ? 1 : 0)) * kAttnM + m;
+  if (sp.c0 != sp.c1) return split_row(sp, c, m);
   const int mi = it.m0 + m, i = mi / G, hq = head * G + mi - i * G;
-  const long long base = (long long)2 * P.ctas * kAttnM;
-  if (it.kind == ITEM_JOINED) return base + (long long)(it.list + i) * Hq + hq;
-  return base + ((long long)P.max_list + it.row_base + i) * Hq + hq;
+  const bool group = it.kind == ITEM_GROUP;
+  return whole_row(P, Hq, group, (group ? it.row_base : it.list) + i, hq);
 }
 
 // Tiles [t0, t1) of the item at `off` on the cost line that CTA c has.
@@ -114,7 +128,7 @@ inline AttnPlan attn_plan_view(const AttnLayout& L, const void* plan) {
   const char* p = (const char*)plan;
   return AttnPlan{(const AttnHead*)p, (const int32_t*)(p + L.qfirst),
                   (const AttnItem*)(p + L.items), (const AttnSpan*)(p + L.spans),
-                  (const AttnRow*)(p + L.list), L.ctas, L.max_list};
+                  (const AttnRow*)(p + L.list), (const AttnJoin*)(p + L.joins), L.ctas, L.max_list};
 }
 
 }  // namespace gdn

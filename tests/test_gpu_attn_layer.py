@@ -350,6 +350,23 @@ def test_attn_strided_rows_no_lse_and_repeats():
     assert none is None and torch.equal(o1, o2)  # run to run the same bits
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attn_repeats_bit_for_bit_whatever_ran_before(D):
+    """Tiles with few rows: what other calls left in shared and tensor memory
+    does not reach them, and a request's bits do not change with its neighbours' values."""
+    c = Cache([1, 8, 2], [3000, 2000, 700], 16, 2, D, 64, seed=21)
+    other = Cache([5, 40], [900, 1500], 16, 2, D, 32, seed=22)
+    other.q.mul_(30)
+    ref, z = c.attn()
+    for _ in range(4):
+        other.attn()
+        o, y = c.attn()
+        assert torch.equal(o, ref) and torch.equal(y, z)
+    c.q[1:9].mul_(8)  # request 1's rows; the plan and the others' values stay
+    o, _ = c.attn()
+    assert torch.equal(o[0], ref[0]) and torch.equal(o[9:], ref[9:])
+
+
 def test_attn_rows_outside_any_request_are_not_written():
     c = Cache([2, 3], [40, 50], 4, 2, 64, 16, seed=12)
     c.T += 4
