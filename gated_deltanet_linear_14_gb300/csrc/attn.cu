@@ -16,11 +16,12 @@
 // 64 keys x up to 128 elements, K and V alike, in the order in which the MMAs
 // use them: nothing is resident but Q.
 //
-// Two score buffers: the next tile's scores are formed while this tile's
-// softmax runs, also across items (the next item's Q is fetched when the last
-// scores of this one are complete), so the softmax warps and the tensor cores
-// wait for each other only at the start. D <= 128 runs two CTAs per SM (256
-// TMEM columns each: O and 2 x 64 scores), D = 256 one.
+// Two or three score buffers: the scores of the next tiles are formed while
+// this tile's softmax runs, also across items (the next item's Q is fetched
+// when the last scores of this one are complete), so the softmax warps and the
+// tensor cores wait for each other only at the start. D <= 128 runs two CTAs
+// per SM (256 TMEM columns each: O and the scores), D = 256 one, with Q in
+// tensor memory too.
 #include <cuda.h>
 
 #include <type_traits>
@@ -39,6 +40,7 @@ constexpr int kSoftmaxWarps = 4;
 constexpr int kAttnThreads = 32 * (kSoftmaxWarps + 2);
 constexpr uint32_t kQChunk = kAttnM * 128;      // bytes of 64 elements of all rows
 constexpr uint32_t kChunk = kAttnKeys * 128;    // ... of all keys of a tile
+constexpr int kBoxes = kAttnKeys / 16;          // pages of a tile, at most
 // The running maximum is raised only when a score exceeds it by more than
 // this (in powers of two): until then p grows up to 2^8, harmless in fp32 sums
 // and in a bf16 or fp16 P, and O need not be rescaled.
@@ -50,13 +52,23 @@ struct Cfg {
   static constexpr int CU = NC < 2 ? 1 : 2;          // chunks of a ring unit
   static constexpr int NU = NC / CU;                 // units of a tile's keys (or values)
   static constexpr uint32_t UNIT = CU * kChunk;
-  static constexpr int NS = D == 64 ? 12 : D == 128 ? 5 : 10;  // units of the ring
+  static constexpr int NS = D == 64 ? 8 : D == 128 ? 4 : 10;  // units of the ring
   static constexpr int CTAS = D == 256 ? 1 : 2;
   static constexpr uint32_t TM_COLS = D == 256 ? 512 : 256;
-  static constexpr uint32_t TM_O = 2 * kAttnKeys;    // after the two score buffers
-  static constexpr uint32_t RING = NC * kQChunk;
+  // Score buffers, O, and for D = 256 Q as the A operand in TMEM. (A product
+  // with N = 64 and both operands in shared memory is bound by reading A, 48
+  // cycles against 32 measured; and at D = 256 Q, K and V together asked for
+  // 1.5 times the shared memory bandwidth that the products need with Q in
+  // TMEM. D = 128 has no columns left for it, D = 64 is bound by the softmax
+  // and takes a third score buffer instead.)
+  static constexpr int NSB = D == 64 ? 3 : 2;
+  static constexpr bool QT = D == 256;
+  static constexpr uint32_t TM_O = NSB * kAttnKeys;
+  static constexpr uint32_t TM_Q = TM_O + D;
+  static_assert(TM_Q + (QT ? D / 2 : 0) <= TM_COLS, "tensor memory columns");
+  static constexpr uint32_t RING = QT ? 0 : NC * kQChunk;
   static constexpr uint32_t BARS = RING + NS * UNIT;
-  static constexpr uint32_t BYTES = BARS + 8 * (2 * NS + 7) + 32;
+  static constexpr uint32_t BYTES = BARS + 8 * (2 * NS + 1 + 3 * NSB) + 32;
 };
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z,
@@ -162,17 +174,10 @@ __device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volati
   return false;
 }
 
-// A whole 32-byte sector per lane where the address allows it: rows are a
-// lane's own, so narrower stores reach the L2 as parts of sectors.
-__device__ __forceinline__ void store32B(void* p, const uint32_t* w, bool wide) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]),
-                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -244,23 +249,23 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
             AttnDims A, KvBatch B, AttnPlan P, const T* q, long long qs, const T* vc, T* o,
             float* lse, float* po, float2* pml, int32_t* status) {
   using C = Cfg<D>;
-  constexpr int NU = C::NU, CU = C::CU, NS = C::NS;
+  constexpr int NU = C::NU, CU = C::CU, NS = C::NS, NSB = C::NSB;
   constexpr uint32_t UNIT = C::UNIT;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem), ring = sb + C::RING;
   const uint32_t full = sb + C::BARS, empty = full + 8 * NS, q_full = empty + 8 * NS;
-  const uint32_t s_full = q_full + 8, p_ready = s_full + 16, o_full = p_ready + 16;
-  volatile uint32_t* words = reinterpret_cast<uint32_t*>(smem + C::BARS + 8 * (2 * NS + 7));
+  const uint32_t s_full = q_full + 8, p_ready = s_full + 8 * NSB, o_full = p_ready + 8 * NSB;
+  volatile uint32_t* words = reinterpret_cast<uint32_t*>(smem + C::BARS + 8 * (2 * NS + 1 + 3 * NSB));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
     mbar_init(q_full, kSoftmaxWarps);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NSB; ++i) {
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_ready + 8 * i, kSoftmaxWarps);
+      mbar_init(o_full + 8 * i, 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(o_full + 8 * i, 1);
     words[1] = words[2] = words[3] = words[4] = 0;
     mbar_fence_init();
   }
@@ -296,34 +301,52 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
         report(status, GDN_DEV_BAD_PAGE);
         return 0;
       };
-      // the units of a tile's keys or values, page by page
+      // The units of a tile's keys or values, page by page: the pages are made
+      // uniform first, then one lane issues a unit's copies in one go.
       auto emit = [&](const CUtensorMap& tm, int t, int page) {
-        const int key0 = W.it.k0 + t * kAttnKeys;
+        const int key0 = W.it.k0 + t * kAttnKeys, in_page = A.ps - 1;
         const int n = uniform(__popc(__ballot_sync(~0u, page >= 0)));  // boxes with keys
+        int z[kBoxes], y[kBoxes];
+#pragma unroll
+        for (int x = 0; x < kBoxes; ++x) {
+          z[x] = __shfl_sync(~0u, page, x);
+          y[x] = W.head * A.ps + ((key0 + x * br) & in_page);
+        }
+#pragma unroll
         for (int u = 0; u < NU; ++u) {
           if (!(ok = wait(empty + 8 * slot, phase ^ 1))) return;
-          const uint32_t at = ring + slot * UNIT, bar = full + 8 * slot;
-          if (elect_one()) mbar_expect_tx(bar, n * br * 128 * CU);
-          for (int x = 0; x < n; ++x) {
-            const int z = __shfl_sync(~0u, page, x);
-            const int y = W.head * A.ps + ((key0 + x * br) & (A.ps - 1));
-            if (elect_one()) {
+          if (elect_one()) {
+            const uint32_t at = ring + slot * UNIT, bar = full + 8 * slot;
+            mbar_expect_tx(bar, n * br * 128 * CU);
 #pragma unroll
-              for (int c = 0; c < CU; ++c)
-                tma_load_3d(at + c * kChunk + x * br * 128, &tm, (u * CU + c) * 64, y, z, bar);
+            for (int x = 0; x < kBoxes; ++x) {
+              if (x < n) {
+#pragma unroll
+                for (int c = 0; c < CU; ++c)
+                  tma_load_3d(at + c * kChunk + x * br * 128, &tm, (u * CU + c) * 64, y[x], z[x],
+                              bar);
+              }
             }
           }
+          __syncwarp();
           if (++slot == NS) slot = 0, phase ^= 1;
           used = min(used + 1, NS);
         }
       };
-      int cur = page_of(W.t0), nxt = page_of(W.t0 + 1);
-      emit(tk, W.t0, cur);
+      // keys run NSB - 1 tiles ahead of the values
+      int pages[NSB];  // of tiles t .. t + NSB - 1
+#pragma unroll
+      for (int x = 0; x < NSB; ++x) pages[x] = page_of(W.t0 + x);
+#pragma unroll
+      for (int x = 0; x < NSB - 1; ++x)
+        if (ok && W.t0 + x < W.t1) emit(tk, W.t0 + x, pages[x]);
       for (int t = W.t0; ok && t < W.t1; ++t) {
-        const int after = page_of(t + 2);
-        if (t + 1 < W.t1) emit(tk, t + 1, nxt);
-        if (ok) emit(tv, t, cur);
-        cur = nxt, nxt = after;
+        const int after = page_of(t + NSB);
+        if (t + NSB - 1 < W.t1) emit(tk, t + NSB - 1, pages[NSB - 1]);
+        if (ok) emit(tv, t, pages[0]);
+#pragma unroll
+        for (int x = 0; x + 1 < NSB; ++x) pages[x] = pages[x + 1];
+        pages[NSB - 1] = after;
       }
     }
     if (!ok) {  // gave up: let the copies in flight land
@@ -334,7 +357,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
     }
   } else if (warp == 5) {
     // ----------------------------------------------------------------- MMA
-    int slot = 0, g = 0;  // g: tiles so far
+    int slot = 0;
     uint32_t phase = 0, items = 0;
     bool ok = true;
     const uint32_t id_s = idesc<T>(kAttnKeys, 0), id_o = idesc<T>(D, 1), tm = uniform(tmem);
@@ -351,8 +374,13 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
 #pragma unroll
           for (int ks = 0; ks < 4 * CU; ++ks) {
             const uint32_t c = ks >> 2, k = (ks & 3) * 32;
-            mma_bf16(tm + kAttnKeys * b, dq + (((u * CU + c) * kQChunk + k) >> 4),
-                     dk + ((slot * UNIT + c * kChunk + k) >> 4), id_s, (u | ks) != 0);
+            const uint64_t key = dk + ((slot * UNIT + c * kChunk + k) >> 4);
+            if (C::QT)
+              mma_ts(tm + kAttnKeys * b, tm + C::TM_Q + 8 * (4 * CU * u + ks), key, id_s,
+                     (u | ks) != 0);
+            else
+              mma_bf16(tm + kAttnKeys * b, dq + (((u * CU + c) * kQChunk + k) >> 4), key, id_s,
+                       (u | ks) != 0);
           }
           mma_commit(empty + 8 * slot);
           if (u == NU - 1) mma_commit(s_full + 8 * b);
@@ -380,15 +408,24 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
 #pragma unroll
       for (int u = 0; u < NU; ++u) advance();
     };
+    int sb_next = 0, b = 0;  // buffers of the next scores and of this tile
+    uint32_t pb = 0;         // phase of this tile's buffer
+    auto next_scores = [&]() {
+      scores(sb_next);
+      if (++sb_next == NSB) sb_next = 0;
+    };
     while (ok && W.next()) {
       if (!(ok = wait(q_full, items++ & 1))) break;
       tc_fence_after();
-      scores(g & 1);
-      for (int t = W.t0; ok && t < W.t1; ++t, ++g) {
-        if (t + 1 < W.t1) scores((g + 1) & 1);
-        if (!ok || !(ok = wait(p_ready + 8 * (g & 1), (g >> 1) & 1))) break;
+#pragma unroll
+      for (int x = 0; x < NSB - 1; ++x)
+        if (ok && W.t0 + x < W.t1) next_scores();
+      for (int t = W.t0; ok && t < W.t1; ++t) {
+        if (t + NSB - 1 < W.t1) next_scores();
+        if (!ok || !(ok = wait(p_ready + 8 * b, pb))) break;
         tc_fence_after();
-        values(g & 1, t == W.t0);
+        values(b, t == W.t0);
+        if (++b == NSB) b = 0, pb ^= 1;
       }
     }
     if (!ok) {  // gave up: give the issued MMAs a millisecond to finish
@@ -399,7 +436,8 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
     // ------------------------------------------------------------- softmax
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
     const float c2 = A.scale * 1.44269504088896341f;
-    int g = 0;
+    int b = 0;          // score buffer of this tile, and its phase
+    uint32_t pb = 0;
     uint32_t units = 0, items = 0;  // ring units and items before this one
     // this thread's (row, head) pair of an item
     auto pair_of = [&](const AttnItem& it, int head, int& i, int& hq) {
@@ -410,8 +448,8 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
     };
     // start copying the warp's rows of an item's Q to shared memory
     auto fetch_q = [&](const Walk& V) {
-      if (V.it.m_cnt <= warp * 32) return;
-      constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte pieces of a row, rows at once
+      if (C::QT || V.it.m_cnt <= warp * 32) return;
+      constexpr int CH = D / 8, RPI = CH < 32 ? 32 / CH : 1;  // 16-byte pieces of a row, rows at once
       int i, hq;
       const long long row = pair_of(V.it, V.head, i, hq);
       const unsigned long long src = (unsigned long long)(q + row * qs + (long long)hq * D);
@@ -427,9 +465,31 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
                        : "memory");
       }
     };
-    auto publish_q = [&]() {
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_async_smem();
+    // ... and wait for it; or bring each thread's row to its TMEM lane
+    auto publish_q = [&](const Walk& V) {
+      if (C::QT) {
+        if (V.it.m_cnt > warp * 32) {
+          int i, hq;
+          const long long row = pair_of(V.it, V.head, i, hq);
+          const uint4* src = reinterpret_cast<const uint4*>(q + row * qs + (long long)hq * D);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t w[64];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const uint4 v = src[16 * h + e];
+              w[4 * e] = v.x, w[4 * e + 1] = v.y, w[4 * e + 2] = v.z, w[4 * e + 3] = v.w;
+            }
+            tm_store32(tmem + C::TM_Q + lane_base + 64 * h, w);
+            tm_store32(tmem + C::TM_Q + lane_base + 64 * h + 32, w + 32);
+          }
+          tmem_st_wait();
+        }
+        tc_fence_before();
+      } else {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_async_smem();
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
     };
@@ -438,14 +498,14 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
     auto advance = [&](Walk& V) {
       return V.next([&] {
         if (tid < V.it.m_cnt)
-          pml[partial_row(P, V.it, V.head, A.Hq, A.G, V.span, V.c, tid)] =
+          pml[partial(P, V.it, V.head, A.Hq, A.G, V.span, V.c, tid, D).row] =
               make_float2(-INFINITY, 0.0f);
       });
     };
     bool ok = true, more = advance(W);
     if (more) {
       fetch_q(W);
-      publish_q();
+      publish_q(W);
     }
     for (; more; ++items) {
       Walk N = W;
@@ -461,12 +521,13 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
 
       float m = -INFINITY, l = 0.0f;
       const int tiles = W.t1 - W.t0;
-      for (int t = W.t0; t < W.t1; ++t, ++g) {
-        const int b = g & 1;
+      int b1 = 0;  // the previous tile's buffer, and its phase
+      uint32_t pb1 = 0;
+      for (int t = W.t0; t < W.t1; ++t) {
         const uint32_t ts = tmem + kAttnKeys * b + lane_base;
         const int base = it.k0 + t * kAttnKeys, nv = min(kAttnKeys, it.kend - base);
         const bool cut = mixed && base + kAttnKeys > first_seen;  // rows see different keys
-        if (!(ok = wait(s_full + 8 * b, (g >> 1) & 1))) break;
+        if (!(ok = wait(s_full + 8 * b, pb))) break;
         tc_fence_after();
         // every warp is past the item before the previous one: its flag is the
         // next item's
@@ -488,8 +549,9 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
           }
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
-            m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(x[e >> 5].r[e & 31]));
+          for (int e = 0; e < 64; e += 2)
+            m4[(e >> 1) & 3] = max3(m4[(e >> 1) & 3], __uint_as_float(x[e >> 5].r[e & 31]),
+                                    __uint_as_float(x[e >> 5].r[(e & 31) + 1]));
           const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           // (each row by itself: its rounding depends on no other row, nor on
           // the lanes past the last one)
@@ -501,7 +563,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
             l *= f;
             if (raise) m = mx;
             // O is complete up to the previous tile
-            if (!(ok = wait(o_full + 8 * (b ^ 1), ((g - 1) >> 1) & 1))) break;
+            if (!(ok = wait(o_full + 8 * b1, pb1))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int j = 0; j < D / 32; ++j) {
@@ -538,9 +600,9 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
         if (cut || nv < kAttnKeys) {
           // (the ring slots may still belong to the previous tile's values
           // until its product is complete)
-          if (t > W.t0 && !(ok = wait(o_full + 8 * (b ^ 1), ((g - 1) >> 1) & 1))) break;
+          if (t > W.t0 && !(ok = wait(o_full + 8 * b1, pb1))) break;
           const int j = t - W.t0;
-          const uint32_t at = units + NU * min(2 * j + 2, 2 * tiles - 1);
+          const uint32_t at = units + NU * (j + min(j + NSB, tiles));
           const int key = tid & (kAttnKeys - 1);
           for (int u = 0; u < NU && ok; ++u) {
             const uint32_t s = (at + u) % NS;
@@ -571,12 +633,13 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_ready + 8 * b);
+        b1 = b, pb1 = pb;
+        if (++b == NSB) b = 0, pb ^= 1;
       }
       if (!ok) break;
-      if (more) publish_q();
+      if (more) publish_q(N);
       units += 2 * NU * tiles;
-      const int last = g - 1;
-      if (!(ok = wait(o_full + 8 * (last & 1), (last >> 1) & 1))) break;
+      if (!(ok = wait(o_full + 8 * b1, pb1))) break;
       tc_fence_after();
       // whether an infinite or NaN value was taken out of a tile of this item
       const bool strange = words[2 + items % 3] != 0;
@@ -584,10 +647,10 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
         const bool direct = it.kind == ITEM_OWN && !W.split();
         const bool mine = tid < it.m_cnt;
         const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-        const long long part =
-            direct || !mine ? 0 : partial_row(P, it, W.head, A.Hq, A.G, W.span, W.c, tid);
+        const AttnPart part = direct || !mine ? AttnPart{0, 0, 0}
+                                              : partial(P, it, W.head, A.Hq, A.G, W.span, W.c, tid, D);
         T* dst = o + (row * A.Hq + hq) * D;
-        float* pdst = po + part * D;
+        float* pdst = po + part.at;
         const bool wide = (((uintptr_t)o | (uintptr_t)po) & 31) == 0;
 #pragma unroll 1
         for (int j = 0; j < D / 32; ++j) {
@@ -620,12 +683,12 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
           } else if (mine) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              store32B(pdst + 32 * j + 8 * e, reinterpret_cast<const uint32_t*>(v + 8 * e), wide);
+              store32B(pdst + (4 * j + e) * part.step, reinterpret_cast<const uint32_t*>(v + 8 * e), wide);
           }
           __syncwarp();
         }
         if (mine && direct && lse) lse[row * A.Hq + hq] = m * A.scale + logf(l);
-        if (mine && !direct) pml[part] = make_float2(m * c2, l);
+        if (mine && !direct) pml[part.row] = make_float2(m * c2, l);
       }
       tc_fence_before();
       W = N;

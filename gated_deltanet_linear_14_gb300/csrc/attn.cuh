@@ -83,6 +83,19 @@ struct Vec {
   __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<raw*>(p) = u; }
 };
 
+// A whole 32-byte sector per lane where the address allows it: rows are a
+// lane's own, so narrower stores reach the L2 as parts of sectors.
+__device__ __forceinline__ void store32B(void* p, const uint32_t* w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 // --------------------------------------------------------------- launchers
 
 // Rotate q rows to q_out and k rows to k_out, or (append) k rows and v rows to

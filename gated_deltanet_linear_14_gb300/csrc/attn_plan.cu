@@ -267,54 +267,49 @@ cudaError_t launch_attn_plan(const AttnDims& A, const KvBatch& B, void* plan, in
 // Pieces of a row hold m (the maximum, in base-2 exponent units), l = sum
 // 2^{s - m} and o = sum 2^{s - m} v, so with M = max m
 //   o = sum 2^{m_p - M} o_p / sum 2^{m_p - M} l_p.
-// A warp per (row, query head): the lanes fetch the pieces' m and l at once,
-// then the warp adds up the pieces' o in their order. The first blocks take
-// the rows of the list, 4 ctas more the items that are cut by a share's end. What a warp reads of
-// the plan it reads before the attention kernel ends (the plan was complete
-// when that kernel began), so only the pieces' own latency follows.
-
-constexpr int kJoinWarps = 4, kJoinBatch = 4;
+// A thread takes 16 elements of a (row, query head) pair, the lanes of a warp
+// 32 neighbouring pairs of a tile, whose partial rows lie side by side. Blocks
+// are 32 pairs x D / 16: first the pairs of the list's rows, head by head,
+// then four per CTA for the items that are cut by a share's end. What a thread
+// reads of the plan it reads before the attention kernel ends (the plan was
+// complete when that kernel began), so only the pieces' own latency follows.
 
 template <class T, int D>
-__global__ void __launch_bounds__(32 * kJoinWarps)
+__global__ void __launch_bounds__(2 * D)
 attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
                  const float2* __restrict__ pml, T* __restrict__ o, float* __restrict__ lse,
-                 int list_blocks) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool cut = (int)blockIdx.x >= list_blocks;
-  int head = 0, m1 = 0, m2 = 0, m_end = 0, step = 1, row = 0, hq = 0, entry = 0;
+                 int list_blocks, bool wide) {
+  const int lane = threadIdx.x & 31, d = (threadIdx.x >> 5) * 16;
+  int m1 = 0, m2 = 0, row = 0, hq = 0, entry = 0;
   bool work = false;
-  AttnItem it{};
   AttnSpan s1{0, 0}, s2{0, -1};
-  if (cut) {
+  if ((int)blockIdx.x >= list_blocks) {
     const int c = (blockIdx.x - list_blocks) >> 2;
     const int q = P.qfirst[c + 1];  // holds the start of share c + 1
     if (q < P.head->items * A.Hkv) {
-      it = P.items[q / A.Hkv];
+      const AttnItem it = P.items[q / A.Hkv];
       s1 = P.spans[q];
-      head = q % A.Hkv;
+      m1 = ((blockIdx.x - list_blocks) & 3) * 32 + lane;
       // cut there, begun in share c, and not joined with another item (an
       // item that begins exactly there has its first piece in share c + 1)
-      work = it.kind == ITEM_OWN && s1.c0 == c && s1.c1 > c;
-      m1 = ((blockIdx.x - list_blocks) & 3) * kJoinWarps + warp;
-      m_end = it.m_cnt;
-      step = 4 * kJoinWarps;
+      work = it.kind == ITEM_OWN && s1.c0 == c && s1.c1 > c && m1 < it.m_cnt;
+      const int mi = it.m0 + m1, i = mi / A.G;
+      row = it.row_base + i;
+      hq = q % A.Hkv * A.G + mi - i * A.G;
     }
   } else {
-    const int idx = blockIdx.x * kJoinWarps + warp;
-    entry = idx / A.Hq;
+    const int blocks = list_blocks / A.Hkv, head = blockIdx.x / blocks;
+    const int x = (blockIdx.x - head * blocks) * 32 + lane;
+    entry = x / A.G;
     if (entry < P.head->list_rows) {
-      hq = idx - entry * A.Hq;
-      head = hq / A.G;
+      const int hg = x - entry * A.G;
       const AttnRow lr = P.list[entry];
       const AttnJoin jn = P.joins[(long long)entry * A.Hkv + head];
-      const int hg = hq - head * A.G;
       work = lr.row >= 0;
       row = lr.row;
+      hq = head * A.G + hg;
       s1 = jn.own;
       m1 = lr.own_m + hg;
-      m_end = m1 + 1;
       s2 = jn.group[(lr.group_m + hg) / kAttnM != lr.group_m / kAttnM ? 1 : 0];
       m2 = (lr.group_m + hg) % kAttnM;
     }
@@ -322,75 +317,51 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
   pdl_begin();
   if (!work) return;
   const int n1 = s1.c1 - s1.c0 + 1, n = n1 + s2.c1 - s2.c0 + 1;
-  for (; m1 < m_end; m1 += step) {
-    if (cut) {
-      const int mi = it.m0 + m1, i = mi / A.G;
-      row = it.row_base + i;
-      hq = head * A.G + mi - i * A.G;
-    }
-    float top = -INFINITY, sum = 0.0f, acc[E];
+  auto part = [&](int p) {
+    const AttnSpan sp = p < n1 ? s1 : s2;
+    return sp.c0 == sp.c1 ? whole_part(P, A.Hq, p >= n1, entry, hq, D)
+           : p < n1       ? split_part(sp, sp.c0 + p, m1, D)
+                          : split_part(sp, sp.c0 + p - n1, m2, D);
+  };
+  float top = -INFINITY, sum = 0.0f, acc[16];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    for (int b = 0; b < n; b += 32) {
-      const int p = b + lane;
-      long long at = 0;
-      float2 ml = make_float2(-INFINITY, 0.0f);
-      if (p < n) {
-        const AttnSpan sp = p < n1 ? s1 : s2;
-        at = sp.c0 == sp.c1 ? whole_row(P, A.Hq, p >= n1, entry, hq)
-             : p < n1       ? split_row(sp, sp.c0 + p, m1)
-                            : split_row(sp, sp.c0 + p - n1, m2);
-        ml = pml[at];
-      }
-      float mx = ml.x;
+  for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
+  // four pieces in flight; past the last one, that one again with weight 0
+  for (int p = 0; p < n; p += 4) {
+    float2 ml[4];
+    float v[4][16];
 #pragma unroll
-      for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
-      const float nt = fmaxf(top, mx), ref = nt == -INFINITY ? 0.0f : nt;
-      const float back = exp2f(top - ref), w = exp2f(ml.x - ref);
-      float s = w * ml.y;
+    for (int k = 0; k < 4; ++k) {
+      const AttnPart at = part(min(p + k, n - 1));
+      ml[k] = pml[at.row];
+      const float* src = po + at.at + (d >> 3) * at.step;
 #pragma unroll
-      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-      sum = sum * back + s;
-      top = nt;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] *= back;
-      const int k_end = min(32, n - b);
-      for (int k = 0; k < k_end; k += kJoinBatch) {
-        float v[kJoinBatch][E], wk[kJoinBatch];
-#pragma unroll
-        for (int x = 0; x < kJoinBatch; ++x) {
-          // past the last piece: any row of this chunk, with weight 0
-          const int from_lane = min(k + x, k_end - 1);
-          const long long from = __shfl_sync(~0u, at, from_lane);
-          wk[x] = __shfl_sync(~0u, w, from_lane);
-          if (k + x >= k_end) wk[x] = 0.0f;
-          const float* src = po + from * D + lane * E;
-          if constexpr (E == 2) {
-            *(float2*)v[x] = *(const float2*)src;
-          } else {
-#pragma unroll
-            for (int e = 0; e < E; e += 4) *(float4*)(v[x] + e) = *(const float4*)(src + e);
-          }
-        }
-#pragma unroll
-        for (int x = 0; x < kJoinBatch; ++x) {
-#pragma unroll
-          for (int e = 0; e < E; ++e)  // a piece without tiles has weight 0 and no o
-            acc[e] = wk[x] == 0.0f ? acc[e] : acc[e] + wk[x] * v[x][e];
-        }
+      for (int e = 0; e < 8; e += 4) {
+        *(float4*)(v[k] + e) = *(const float4*)(src + e);
+        *(float4*)(v[k] + 8 + e) = *(const float4*)(src + at.step + e);
       }
     }
-    const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-    uint32_t out[E / 2];
+    const float nt = fmaxf(fmaxf(top, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
+    const float ref = nt == -INFINITY ? 0.0f : nt, back = exp2f(top - ref);
+    top = nt;
+    sum *= back;
 #pragma unroll
-    for (int e = 0; e < E; e += 2) out[e / 2] = pack2<T>(acc[e] * inv, acc[e + 1] * inv);
-    T* dst = o + ((size_t)row * A.Hq + hq) * D + lane * E;
-    if constexpr (E == 2) *(uint32_t*)dst = out[0];
-    else if constexpr (E == 4) *(uint2*)dst = make_uint2(out[0], out[1]);
-    else *(uint4*)dst = make_uint4(out[0], out[1], out[2], out[3]);
-    if (lse && lane == 0)
-      lse[(size_t)row * A.Hq + hq] = (top + log2f(sum)) * 0.693147180559945309f;
+    for (int e = 0; e < 16; ++e) acc[e] *= back;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float w = p + k < n ? exp2f(ml[k].x - ref) : 0.0f;
+      if (p + k < n) sum += w * ml[k].y;
+#pragma unroll
+      for (int e = 0; e < 16; ++e)  // a piece without tiles has weight 0 and no o
+        acc[e] = w == 0.0f ? acc[e] : acc[e] + w * v[k][e];
+    }
   }
+  const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+  uint32_t out[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) out[e] = pack2<T>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  store32B(o + ((size_t)row * A.Hq + hq) * D + d, out, wide);
+  if (lse && d == 0) lse[(size_t)row * A.Hq + hq] = (top + log2f(sum)) * 0.693147180559945309f;
 }
 
 cudaError_t launch_attn_join(const AttnDims& A, const KvBatch& B, int io, const void* plan,
@@ -399,14 +370,13 @@ cudaError_t launch_attn_join(const AttnDims& A, const KvBatch& B, int io, const 
   const AttnPlan P = attn_plan_view(L, plan);
   const float* po = (const float*)ws;
   const float2* pml = (const float2*)((const char*)ws + L.ws_ml);
-  const int list_blocks =
-      (int)(((long long)L.max_list * A.Hq + kJoinWarps - 1) / kJoinWarps);
-  const dim3 grid(list_blocks + 4 * L.ctas);
-  const dim3 block(32 * kJoinWarps);
+  const int list_blocks = (int)(((long long)L.max_list * A.G + 31) / 32) * A.Hkv;
+  const dim3 grid(list_blocks + 4 * L.ctas), block(2 * A.D);
+  const bool wide = ((uintptr_t)o & 31) == 0;
   auto go = [&](auto t, auto d) {
     using T = decltype(t);
     return launch_pdl(attn_join_kernel<T, decltype(d)::value>, grid, block, 0, s, A, P, po, pml,
-                      (T*)o, lse, list_blocks);
+                      (T*)o, lse, list_blocks, wide);
   };
   auto by_dim = [&](auto t) {
     if (A.D == 64) return go(t, std::integral_constant<int, 64>());

@@ -84,23 +84,33 @@ struct AttnPlan {
   int ctas, max_list;
 };
 
-// Partial rows of an item piece: where piece `c` of item q keeps row m (own
-// place in the tile). Split pieces: two tiles of 128 rows per CTA (a CTA has
-// at most one item that began before its share and one that goes on after
-// it); whole items that are joined with others: by list row and query head.
-__device__ __forceinline__ long long split_row(AttnSpan sp, int c, int m) {
-  return (long long)(2 * c + (c == sp.c0 ? 1 : 0)) * kAttnM + m;
+// Where piece `c` of an item keeps the partial o of its row m (own place in
+// the tile). Split pieces: two tiles per CTA (a CTA has at most one item that
+// began before its share and one that goes on after it), elements in groups
+// of 8 with the rows side by side, so that the lanes of a warp, a row each,
+// write whole lines: element d at d / 8 * 8 * kAttnM + d % 8. Whole items that
+// are joined with others: by list row and query head, a row's elements
+// together. `row` numbers the (m, l) pairs.
+struct AttnPart {
+  long long row, at;  // at: of element 0, in elements of a D-wide row
+  int step;           // from one group of 8 elements to the next
+};
+__device__ __forceinline__ AttnPart split_part(AttnSpan sp, int c, int m, int D) {
+  const long long tile = 2 * c + (c == sp.c0 ? 1 : 0);
+  return {tile * kAttnM + m, tile * kAttnM * D + m * 8, 8 * kAttnM};
 }
-__device__ __forceinline__ long long whole_row(const AttnPlan& P, int Hq, bool group, int entry,
-                                               int hq) {
-  return (long long)2 * P.ctas * kAttnM + ((long long)(group ? P.max_list : 0) + entry) * Hq + hq;
+__device__ __forceinline__ AttnPart whole_part(const AttnPlan& P, int Hq, bool group, int entry,
+                                               int hq, int D) {
+  const long long row = (long long)2 * P.ctas * kAttnM +
+                        ((long long)(group ? P.max_list : 0) + entry) * Hq + hq;
+  return {row, row * D, 8};
 }
-__device__ __forceinline__ long long partial_row(const AttnPlan& P, const AttnItem& it, int head,
-                                                 int Hq, int G, AttnSpan sp, int c, int m) {
-  if (sp.c0 != sp.c1) return split_row(sp, c, m);
+__device__ __forceinline__ AttnPart partial(const AttnPlan& P, const AttnItem& it, int head, int Hq,
+                                            int G, AttnSpan sp, int c, int m, int D) {
+  if (sp.c0 != sp.c1) return split_part(sp, c, m, D);
   const int mi = it.m0 + m, i = mi / G, hq = head * G + mi - i * G;
   const bool group = it.kind == ITEM_GROUP;
-  return whole_row(P, Hq, group, (group ? it.row_base : it.list) + i, hq);
+  return whole_part(P, Hq, group, (group ? it.row_base : it.list) + i, hq, D);
 }
 
 // Tiles [t0, t1) of the item at `off` on the cost line that CTA c has.
