@@ -274,6 +274,8 @@ cudaError_t launch_attn_plan(const AttnDims& A, const KvBatch& B, void* plan, in
 // reads of the plan it reads before the attention kernel ends (the plan was
 // complete when that kernel began), so only the pieces' own latency follows.
 
+constexpr int kJoinBatch = 4;
+
 template <class T, int D>
 __global__ void __launch_bounds__(2 * D)
 attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
@@ -314,6 +316,9 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
       m2 = (lr.group_m + hg) % kAttnM;
     }
   }
+  // (the first block always waits: the grid must not end before the attention
+  // kernel has)
+  if (blockIdx.x != 0 && !__any_sync(~0u, work)) return;
   pdl_begin();
   if (!work) return;
   const int n1 = s1.c1 - s1.c0 + 1, n = n1 + s2.c1 - s2.c0 + 1;
@@ -326,12 +331,12 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
   float top = -INFINITY, sum = 0.0f, acc[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
-  // four pieces in flight; past the last one, that one again with weight 0
-  for (int p = 0; p < n; p += 4) {
-    float2 ml[4];
-    float v[4][16];
+  // kJoinBatch pieces in flight; past the last one, that one again with weight 0
+  for (int p = 0; p < n; p += kJoinBatch) {
+    float2 ml[kJoinBatch];
+    float v[kJoinBatch][16];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kJoinBatch; ++k) {
       const AttnPart at = part(min(p + k, n - 1));
       ml[k] = pml[at.row];
       const float* src = po + at.at + (d >> 3) * at.step;
@@ -341,14 +346,16 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
         *(float4*)(v[k] + 8 + e) = *(const float4*)(src + at.step + e);
       }
     }
-    const float nt = fmaxf(fmaxf(top, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
+    float nt = top;
+#pragma unroll
+    for (int k = 0; k < kJoinBatch; ++k) nt = fmaxf(nt, ml[k].x);
     const float ref = nt == -INFINITY ? 0.0f : nt, back = exp2f(top - ref);
     top = nt;
     sum *= back;
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[e] *= back;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kJoinBatch; ++k) {
       const float w = p + k < n ? exp2f(ml[k].x - ref) : 0.0f;
       if (p + k < n) sum += w * ml[k].y;
 #pragma unroll
