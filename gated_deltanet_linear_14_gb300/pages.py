@@ -1,4 +1,4 @@
-"""Typed views of state pages and slot pools (host-side marshalling only).
+"""Typed views of state pages, slot pools and key/value caches (host-side marshalling only).
 
 A page pool is one ``uint8`` CUDA tensor of ``num_pages * page_bytes`` bytes;
 the byte layout comes from ``gdn_page_layout`` (see include/gdn.h). These
@@ -9,9 +9,9 @@ from __future__ import annotations
 
 import torch
 
-from . import (GDN_BF16, Dims, gdn_page_layout, gdn_slot_layout)
+from . import (GDN_BF16, AttnDims, Dims, gdn_page_layout, gdn_slot_layout)
 
-_TORCH = {0: torch.float32, 1: torch.bfloat16}
+_TORCH = {0: torch.float32, 1: torch.bfloat16, 2: torch.float16}
 
 
 def torch_dtype(code: int):
@@ -101,3 +101,16 @@ class SlotPool:
         nbytes = (d.conv_width - 1) * self.C * (2 if d.io_dtype == GDN_BF16 else 4)
         v = self._bytes(p, i, self.layout.window_offset, nbytes)
         return v.view(torch_dtype(d.io_dtype)).view(d.conv_width - 1, self.C)
+
+
+class KvCache:
+    """A paged key/value cache for attention layers: ``k`` and ``v``, each
+    [num_pages][Hkv][page_size][D] in the io dtype. Slots that hold no token are never read,
+    so the memory need not be cleared."""
+
+    def __init__(self, dims: AttnDims, num_pages: int, device="cuda"):
+        self.dims = dims
+        self.num_pages = int(num_pages)
+        shape = (self.num_pages, dims.num_kv_heads, dims.page_size, dims.head_dim)
+        self.k, self.v = (torch.empty(shape, dtype=torch_dtype(dims.io_dtype), device=device)
+                          for _ in range(2))

@@ -13,7 +13,11 @@
  *                      step from the page's record, checkpoint the state,
  *                      run the new candidates (row count 0 = commit);
  *   gdn_chunk_prefill  the chunked (WY) form of the same rule for long
- *                      prompts, contractions on the tcgen05 tensor cores.
+ *                      prompts, contractions on the tcgen05 tensor cores;
+ *
+ * and, for the softmax-attention layers that hybrid stacks put between GDN
+ * layers, rotary positions (gdn_rope), a paged key/value cache
+ * (gdn_kv_append) and the attention over it (gdn_attn_plan, gdn_attn).
  *
  * Sources (the method is described, not printed, on these pages):
  *   - r9700-stack v0.2.4 release notes, "What it does": one state page per
@@ -53,8 +57,9 @@
  *     zero *status before the call and read it when convenient. Kernels never
  *     trap.
  *   - Results for a request depend only on that request's inputs, never on
- *     the composition or order of the batch, and are run-to-run identical
- *     (no floating-point atomics anywhere).
+ *     the composition or order of the batch (gdn_attn: up to the order of
+ *     additions), and are run-to-run identical (no floating-point atomics
+ *     anywhere).
  *
  * Layouts (row-major, innermost last)
  *   rows:    x, y (conv'd) [num_rows][C], C = 2*Hk*Dk + Hv*Dv, channel
@@ -503,7 +508,9 @@ typedef struct {
  * same for the requests group_start[g] .. + group_len[g] - 1. Results do not
  * depend on the groups (up to the order of additions); keys that are declared
  * shared are read once for the group instead of once per request. Groups do
- * not overlap. */
+ * not overlap. (Requests with more than 64 (row, query head) pairs per
+ * key/value head read the shared keys by themselves, as do groups that share
+ * fewer than 256 tokens or have fewer than two shorter requests.) */
 typedef struct {
   int32_t num_requests;        /* R                                            */
   int32_t num_rows;            /* rows in the packed q/k/v/o buffers           */
@@ -578,7 +585,10 @@ gdn_status gdn_attn_plan(const gdn_attn_dims* dims, const gdn_kv_batch* batch, v
  *   lse        device [num_rows][Hq] fp32 (natural logarithm) or NULL
  *   workspace  device, 16-byte aligned, at least gdn_attn_workspace_bytes;
  *              overwritten, in use until the launches complete
- * Cache slots past a request's kv_len are never used, whatever they hold.
+ * Cache slots past a request's kv_len are never used, whatever they hold, and
+ * an infinite or NaN key or value reaches only the rows that see it. Run to
+ * run the bits are the same; how the keys are divided, and with it the order
+ * of additions, depends on the lengths of the whole step.
  * D in {64, 128, 256}, page_size a power of two in [16, 256], bf16 or fp16,
  * Hq / Hkv <= 128. Rows of no request are not written. Device error:
  * GDN_DEV_BAD_PAGE (a page index out of range: the outputs of that request are

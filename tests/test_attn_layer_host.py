@@ -1,6 +1,9 @@
 """Host-side checks of the attention-layer calls that need no GPU: bad
 arguments are refused before anything is launched, sizes are as declared."""
 import ctypes
+import os
+import shutil
+import subprocess
 
 import pytest
 
@@ -168,3 +171,31 @@ def test_plan_buffers_refused(lib):
     assert call_plan(lib, plan=24) == INVALID
     need = lib.gdn_attn_plan_bytes(R(dims()), R(batch()))
     assert need > 0 and call_plan(lib, n=need - 1) == WORKSPACE
+
+
+def test_structs_match_the_header(tmp_path):
+    """A C client sees the binding's sizes and offsets."""
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    pairs = [(gdn.AttnDims, "gdn_attn_dims"), (gdn.RopeParams, "gdn_rope_params"),
+             (gdn.KvBatch, "gdn_kv_batch")]
+    lines, want = [], []
+    for cls, name in pairs:
+        lines.append(f'printf("%zu\\n", sizeof({name}));')
+        want.append(ctypes.sizeof(cls))
+        for field, _ in cls._fields_:
+            lines.append(f'printf("%zu\\n", offsetof({name}, {field}));')
+            want.append(getattr(cls, field).offset)
+    lines.append('printf("%d\\n", GDN_F16);')
+    want.append(gdn.GDN_F16)
+    src = tmp_path / "sizes.c"
+    src.write_text('#include <stdio.h>\n#include "gdn.h"\nint main(void) {\n'
+                   + "\n".join(lines) + "\nreturn 0; }\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    exe = tmp_path / "sizes"
+    subprocess.run([cc, "-std=c99", "-Wall", "-Werror", "-I", os.path.join(root, "include"),
+                    str(src), "-o", str(exe)], check=True)
+    got = [int(x) for x in subprocess.run([str(exe)], check=True, capture_output=True,
+                                          text=True).stdout.split()]
+    assert got == want
