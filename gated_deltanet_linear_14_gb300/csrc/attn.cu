@@ -193,11 +193,26 @@ __device__ __forceinline__ constexpr uint32_t idesc(int N, int b_mn_major) {
          ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
-// Whether any of four words holds an infinite or NaN 16-bit value.
+// The 16-bit values of a word that are infinite or NaN, as a mask.
 template <class T>
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
   constexpr uint32_t E = std::is_same<T, bf16>::value ? 0x7F80u : 0x7C00u;
   return (((w & E) == E) ? 0xFFFFu : 0u) | (((w >> 16 & E) == E) ? 0xFFFF0000u : 0u);
+}
+
+// Bits 15 and 31 of the result are set where some value of the eight is
+// infinite or NaN: an exponent of ones carries into them.
+template <class T>
+__device__ __forceinline__ uint32_t any_not_finite(const uint4& v) {
+  constexpr uint32_t E = std::is_same<T, bf16>::value ? 0x7F807F80u : 0x7C007C00u;
+  constexpr uint32_t ONE = std::is_same<T, bf16>::value ? 0x00800080u : 0x04000400u;
+  return ((v.x & E) + ONE) | ((v.y & E) + ONE) | ((v.z & E) + ONE) | ((v.w & E) + ONE);
+}
+
+// A load whose value nobody waits for.
+__device__ __forceinline__ void touch(const void* p) {
+  uint32_t x;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(x) : "l"(p));
 }
 
 // The items of one CTA, walked alike by every role.
@@ -239,6 +254,15 @@ struct Walk {
     return next([] {});
   }
   __device__ __forceinline__ bool split() const { return span.c0 != span.c1; }
+  // Bring what next() will read to the L1, while there is something else to do.
+  __device__ __forceinline__ void touch_next() const {
+    if (q + 1 >= Q) return;
+    touch(P->spans + q + 1);
+    if (head + 1 == Hkv) {
+      touch(P->items + item + 1);
+      touch(reinterpret_cast<const char*>(P->items + item + 1) + 32);
+    }
+  }
 };
 
 }  // namespace
@@ -291,6 +315,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
     uint32_t phase = 0;
     bool ok = true;
     while (ok && W.next()) {
+      W.touch_next();
       const int32_t* table = B.table + (size_t)W.it.req * B.max_pages;
       // this lane's page of tile t (-1: past the keys, or no such box)
       auto page_of = [&](int t) {
@@ -414,17 +439,21 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
       scores(sb_next);
       if (++sb_next == NSB) sb_next = 0;
     };
-    while (ok && W.next()) {
+    bool more = W.next();
+    while (ok && more) {
+      W.touch_next();
       if (!(ok = wait(q_full, items++ & 1))) break;
       tc_fence_after();
+      const int t0 = W.t0, t1 = W.t1;
 #pragma unroll
       for (int x = 0; x < NSB - 1; ++x)
-        if (ok && W.t0 + x < W.t1) next_scores();
-      for (int t = W.t0; ok && t < W.t1; ++t) {
-        if (t + NSB - 1 < W.t1) next_scores();
+        if (ok && t0 + x < t1) next_scores();
+      for (int t = t0; ok && t < t1; ++t) {
+        if (t + NSB - 1 < t1) next_scores();
+        if (t + 1 == t1) more = W.next();  // under the last tile's softmax
         if (!ok || !(ok = wait(p_ready + 8 * b, pb))) break;
         tc_fence_after();
-        values(b, t == W.t0);
+        values(b, t == t0);
         if (++b == NSB) b = 0, pb ^= 1;
       }
     }
@@ -439,28 +468,30 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
     int b = 0;          // score buffer of this tile, and its phase
     uint32_t pb = 0;
     uint32_t units = 0, items = 0;  // ring units and items before this one
-    // this thread's (row, head) pair of an item
-    auto pair_of = [&](const AttnItem& it, int head, int& i, int& hq) {
-      const int mi = it.m0 + min(tid, it.m_cnt - 1);
+    // pair m of an item
+    auto pair_of = [&](const AttnItem& it, int head, int m, int& i, int& hq) {
+      const int mi = it.m0 + min(m, it.m_cnt - 1);
       i = mi / A.G;
       hq = head * A.G + mi - i * A.G;
       return it.kind == ITEM_GROUP ? P.list[it.row_base + i].row : it.row_base + i;
     };
-    // start copying the warp's rows of an item's Q to shared memory
+    // start copying an item's Q to shared memory, every fourth row a warp (a
+    // tile with few rows is fetched by all)
     auto fetch_q = [&](const Walk& V) {
-      if (C::QT || V.it.m_cnt <= warp * 32) return;
+      if (C::QT || V.it.m_cnt <= warp) return;
       constexpr int CH = D / 8, RPI = CH < 32 ? 32 / CH : 1;  // 16-byte pieces of a row, rows at once
       int i, hq;
-      const long long row = pair_of(V.it, V.head, i, hq);
+      const long long row = pair_of(V.it, V.head, 4 * lane + warp, i, hq);
       const unsigned long long src = (unsigned long long)(q + row * qs + (long long)hq * D);
-      const int n = min(32, V.it.m_cnt - warp * 32), ch = lane % CH;
+      const int n = (V.it.m_cnt - warp + 3) >> 2, ch = lane % CH;
       const uint32_t dst = sb + (ch >> 3) * kQChunk;
+#pragma unroll 4
       for (int r0 = 0; r0 < n; r0 += RPI) {
         const int r = r0 + lane / CH;
-        const unsigned long long from = __shfl_sync(~0u, src, r) + ch * 16;
+        const unsigned long long from = __shfl_sync(~0u, src, r & 31) + ch * 16;
         if (r < n)
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                           dst + sw128_chunk(warp * 32 + r, ch & 7)),
+                           dst + sw128_chunk(4 * r + warp, ch & 7)),
                        "l"(from)
                        : "memory");
       }
@@ -470,7 +501,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
       if (C::QT) {
         if (V.it.m_cnt > warp * 32) {
           int i, hq;
-          const long long row = pair_of(V.it, V.head, i, hq);
+          const long long row = pair_of(V.it, V.head, tid, i, hq);
           const uint4* src = reinterpret_cast<const uint4*>(q + row * qs + (long long)hq * D);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -508,12 +539,12 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
       publish_q(W);
     }
     for (; more; ++items) {
-      Walk N = W;
-      more = advance(N);
+      Walk N = W;  // the next piece, looked up when this one's first scores are there
+      W.touch_next();
       const AttnItem& it = W.it;
       const bool rows_here = it.m_cnt > warp * 32;
       int i, hq;
-      const long long row = pair_of(it, W.head, i, hq);
+      const long long row = pair_of(it, W.head, tid, i, hq);
       const bool group = it.kind == ITEM_GROUP;
       const int seen = group ? it.kend : it.vis0 + i;  // keys below this
       const int first_seen = group ? it.kend : it.vis0 + it.m0 / A.G;
@@ -532,6 +563,11 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
         // every warp is past the item before the previous one: its flag is the
         // next item's
         if (t == W.t0 && tid == 0) words[2 + (items + 1) % 3] = 0;
+        if (t == W.t0) {
+          more = advance(N);
+          if (more && N.it.kind == ITEM_GROUP)
+            touch(P.list + N.it.row_base + (N.it.m0 + min(tid, N.it.m_cnt - 1)) / A.G);
+        }
         // the item's scores are complete: Q makes way for the next item's
         if (more && t + 1 == W.t1) fetch_q(N);
         if (rows_here) {
@@ -598,9 +634,6 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
         // infinite and NaN values are zeroed too and added at the end to the
         // rows that see them.
         if (cut || nv < kAttnKeys) {
-          // (the ring slots may still belong to the previous tile's values
-          // until its product is complete)
-          if (t > W.t0 && !(ok = wait(o_full + 8 * b1, pb1))) break;
           const int j = t - W.t0;
           const uint32_t at = units + NU * (j + min(j + NSB, tiles));
           const int key = tid & (kAttnKeys - 1);
@@ -610,23 +643,28 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
             for (int c = tid / kAttnKeys; c < CU; c += 2) {
               uint4* vrow =
                   reinterpret_cast<uint4*>(smem + C::RING + s * UNIT + c * kChunk + key * 128);
-              for (int k = 0; k < 8; ++k) {
-                uint4& w = vrow[(k + lane) & 7];  // all banks at once
-                if (key >= nv) {
-                  w = make_uint4(0, 0, 0, 0);
-                } else if (cut) {
-                  const uint4 v = w;
-                  const uint4 bad = make_uint4(not_finite<T>(v.x), not_finite<T>(v.y),
-                                               not_finite<T>(v.z), not_finite<T>(v.w));
-                  if (bad.x | bad.y | bad.z | bad.w) {
-                    words[2 + items % 3] = 1;
-                    w = make_uint4(v.x & ~bad.x, v.y & ~bad.y, v.z & ~bad.z, v.w & ~bad.w);
-                  }
+              if (key >= nv) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) vrow[(k + lane) & 7] = make_uint4(0, 0, 0, 0);
+              } else if (cut) {
+                uint4 v[8];  // (read from all banks at once)
+                uint32_t bad = 0;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  v[k] = vrow[(k + lane) & 7];
+                  bad |= any_not_finite<T>(v[k]);
+                }
+                if (bad & 0x80008000u) {
+                  words[2 + items % 3] = 1;
+#pragma unroll
+                  for (int k = 0; k < 8; ++k)
+                    vrow[(k + lane) & 7] = make_uint4(
+                        v[k].x & ~not_finite<T>(v[k].x), v[k].y & ~not_finite<T>(v[k].y),
+                        v[k].z & ~not_finite<T>(v[k].z), v[k].w & ~not_finite<T>(v[k].w));
                 }
               }
             }
           }
-          __syncwarp();
           fence_async_smem();
           if (!ok) break;
         }
@@ -652,10 +690,10 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
         T* dst = o + (row * A.Hq + hq) * D;
         float* pdst = po + part.at;
         const bool wide = (((uintptr_t)o | (uintptr_t)po) & 31) == 0;
-#pragma unroll 1
-        for (int j = 0; j < D / 32; ++j) {
+        auto column = [&](int j, Cols& x) {
           float v[32];
-          tmem_ld32(tmem + C::TM_O + lane_base + 32 * j, v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(x.r[e]);
           if (strange && mine) {
             // the values that were taken out, of this CTA's tiles in which rows
             // see different keys
@@ -666,6 +704,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
               if (page < 0 || page >= B.num_pages) page = 0;
               const uint32_t* src = reinterpret_cast<const uint32_t*>(
                   vc + (((size_t)page * A.Hkv + W.head) * A.ps + (key & (A.ps - 1))) * D + 32 * j);
+#pragma unroll
               for (int e = 0; e < 16; ++e) {
                 const uint32_t w = src[e], bad = not_finite<T>(w);
                 const uint16_t lo = w & 0xFFFF, hi = w >> 16;
@@ -683,9 +722,20 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
           } else if (mine) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              store32B(pdst + (4 * j + e) * part.step, reinterpret_cast<const uint32_t*>(v + 8 * e), wide);
+              store32B(pdst + (4 * j + e) * part.step, reinterpret_cast<const uint32_t*>(v + 8 * e),
+                       wide);
           }
           __syncwarp();
+        };
+#pragma unroll 1
+        for (int j = 0; j < D / 32; j += 2) {
+          Cols x0, x1;
+          tm_load32(tmem + C::TM_O + lane_base + 32 * j, x0);
+          tm_load32(tmem + C::TM_O + lane_base + 32 * j + 32, x1);
+          tm_wait32(x0);
+          tm_wait32(x1);
+          column(j, x0);
+          column(j + 1, x1);
         }
         if (mine && direct && lse) lse[row * A.Hq + hq] = m * A.scale + logf(l);
         if (mine && !direct) pml[part.row] = make_float2(m * c2, l);

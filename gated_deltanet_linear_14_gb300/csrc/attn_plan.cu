@@ -14,6 +14,7 @@ AttnLayout attn_layout(const AttnDims& A, const KvBatch& B) {
   auto up = [](size_t x) { return (x + 63) & ~(size_t)63; };
   L.ctas = device_sms() * attn_ctas_per_sm(A.D);
   L.ents = B.num_groups + B.R;
+  L.item_cost = item_cost(A, B);
   // rows that may join: at most kJoinRows / G per request
   const long long join = B.num_groups ? (long long)B.R * (kJoinRows / A.G) : 0;
   L.max_list = (int)(join < B.num_rows ? join : B.num_rows);
@@ -32,7 +33,7 @@ AttnLayout attn_layout(const AttnDims& A, const KvBatch& B) {
   L.g_rows = at, at = up(at + 4 * (size_t)B.num_groups);
   L.g_off = at, at = up(at + 4 * (size_t)B.num_groups);
   L.bytes = at;
-  L.ws_rows = (long long)2 * L.ctas * kAttnM + 2 * (long long)L.max_list * A.Hq;
+  L.ws_rows = ((long long)2 * L.ctas * kAttnM + 2 * (long long)L.max_list * A.Hq + 31) / 32 * 32;
   L.ws_ml = (size_t)L.ws_rows * A.D * 4;
   L.ws_bytes = L.ws_ml + (size_t)L.ws_rows * 8;
   return L;
@@ -220,7 +221,7 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
         it.kend = it.vis0 + (it.m0 + it.m_cnt - 1) / A.G;
       }
       it.tiles = (it.kend - it.k0 + kAttnKeys - 1) / kAttnKeys;
-      it.cost = it.tiles * kTileCost + kItemCost;
+      it.cost = it.tiles * kTileCost + L.item_cost;
     }
     unsigned long long total;
     it.off = at + block_scan((unsigned long long)it.cost * A.Hkv, total, scan64);
@@ -229,7 +230,7 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
   }
   // equal shares, none below one tile and its item's own cost
   const unsigned long long share =
-      max((at + L.ctas - 1) / L.ctas, (unsigned long long)(kTileCost + kItemCost));
+      max((at + L.ctas - 1) / L.ctas, (unsigned long long)(kTileCost + L.item_cost));
   const int Q = n_items * A.Hkv;
   for (int c = tid; c <= L.ctas; c += kPlanThreads) qfirst[c] = Q;
   if (tid == 0) *head = AttnHead{share, at, n_items, min(list_rows, L.max_list)};
@@ -324,7 +325,7 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
   const int n1 = s1.c1 - s1.c0 + 1, n = n1 + s2.c1 - s2.c0 + 1;
   auto part = [&](int p) {
     const AttnSpan sp = p < n1 ? s1 : s2;
-    return sp.c0 == sp.c1 ? whole_part(P, A.Hq, p >= n1, entry, hq, D)
+    return sp.c0 == sp.c1 ? whole_part(P, A.Hq, A.G, p >= n1, entry, hq, D)
            : p < n1       ? split_part(sp, sp.c0 + p, m1, D)
                           : split_part(sp, sp.c0 + p - n1, m2, D);
   };

@@ -6,7 +6,7 @@
 // (the keys that its requests share, the rows of all its requests side by
 // side). Items repeat for every key/value head; item q = item * Hkv + head.
 // The items lie end to end on a line of cost (kTileCost per tile of 64 keys,
-// kItemCost per item and head) that is cut into equal shares, one per CTA, so
+// item_cost per item and head) that is cut into equal shares, one per CTA, so
 // every CTA has the same work whatever the lengths are. An item that crosses a
 // share's end is finished by the next CTA; the pieces are joined afterwards.
 #pragma once
@@ -17,7 +17,16 @@ namespace gdn {
 
 constexpr int kAttnM = 128;      // (row, head) pairs of an item: the tensor core's M
 constexpr int kAttnKeys = 64;    // keys of a tile
-constexpr unsigned kTileCost = 4, kItemCost = 20;
+constexpr unsigned kTileCost = 4;
+// Cost of an item beside its tiles: its start and its end, least-squares fits
+// of CTA times. Where the step is bound by memory (short rows, nothing shared)
+// others' fetches cover it: 0.9 us against 1.3 us a tile (decode, D = 128).
+// Where it is bound by the SMs: D = 64 2.3 against 0.75 us, D = 128 3.8
+// against 0.62 us, D = 256 3.4 against 1.0 us.
+inline unsigned item_cost(const AttnDims& A, const KvBatch& B) {
+  if (B.num_groups == 0 && (long long)B.max_rows * A.G <= 64) return 3;
+  return 20;
+}
 // A request joins its group's shared pass with up to this many (row, head)
 // pairs; above, its own tiles are full enough to read the shared keys alone.
 constexpr int kJoinRows = 64;
@@ -69,6 +78,7 @@ struct AttnHead {
 // Byte offsets inside the plan, and the bounds they come from.
 struct AttnLayout {
   int ctas, max_items, max_list, ents;  // ents: groups, then requests
+  unsigned item_cost;
   size_t qfirst, items, spans, list, joins, first_item, k0, req_list, g_shared, g_rows, g_off, bytes;
   size_t ws_ml, ws_bytes;  // partial rows: fp32 o, then (m, l)
   long long ws_rows;
@@ -85,12 +95,12 @@ struct AttnPlan {
 };
 
 // Where piece `c` of an item keeps the partial o of its row m (own place in
-// the tile). Split pieces: two tiles per CTA (a CTA has at most one item that
-// began before its share and one that goes on after it), elements in groups
-// of 8 with the rows side by side, so that the lanes of a warp, a row each,
-// write whole lines: element d at d / 8 * 8 * kAttnM + d % 8. Whole items that
-// are joined with others: by list row and query head, a row's elements
-// together. `row` numbers the (m, l) pairs.
+// the tile). Elements lie in groups of 8 with the rows of a block side by
+// side, so that the lanes of a warp, a row each, write whole lines: element d
+// at d / 8 * step + d % 8. Split pieces have two tiles per CTA as blocks (a CTA
+// has at most one item that began before its share and one that goes on after
+// it); whole items that are joined with others go by key/value head, list row
+// and query head in blocks of 32 rows. `row` numbers the (m, l) pairs.
 struct AttnPart {
   long long row, at;  // at: of element 0, in elements of a D-wide row
   int step;           // from one group of 8 elements to the next
@@ -99,18 +109,19 @@ __device__ __forceinline__ AttnPart split_part(AttnSpan sp, int c, int m, int D)
   const long long tile = 2 * c + (c == sp.c0 ? 1 : 0);
   return {tile * kAttnM + m, tile * kAttnM * D + m * 8, 8 * kAttnM};
 }
-__device__ __forceinline__ AttnPart whole_part(const AttnPlan& P, int Hq, bool group, int entry,
-                                               int hq, int D) {
-  const long long row = (long long)2 * P.ctas * kAttnM +
-                        ((long long)(group ? P.max_list : 0) + entry) * Hq + hq;
-  return {row, row * D, 8};
+__device__ __forceinline__ AttnPart whole_part(const AttnPlan& P, int Hq, int G, bool group,
+                                               int entry, int hq, int D) {
+  const int head = hq / G;
+  const long long row = (long long)2 * P.ctas * kAttnM + (group ? (long long)P.max_list * Hq : 0) +
+                        ((long long)head * P.max_list + entry) * G + hq - head * G;
+  return {row, (row >> 5) * 32 * D + (row & 31) * 8, 8 * 32};
 }
 __device__ __forceinline__ AttnPart partial(const AttnPlan& P, const AttnItem& it, int head, int Hq,
                                             int G, AttnSpan sp, int c, int m, int D) {
   if (sp.c0 != sp.c1) return split_part(sp, c, m, D);
   const int mi = it.m0 + m, i = mi / G, hq = head * G + mi - i * G;
   const bool group = it.kind == ITEM_GROUP;
-  return whole_part(P, Hq, group, (group ? it.row_base : it.list) + i, hq, D);
+  return whole_part(P, Hq, G, group, (group ? it.row_base : it.list) + i, hq, D);
 }
 
 // Tiles [t0, t1) of the item at `off` on the cost line that CTA c has.
