@@ -215,36 +215,49 @@ __device__ __forceinline__ void touch(const void* p) {
   asm volatile("ld.global.u32 %0, [%1];" : "=r"(x) : "l"(p));
 }
 
-// The items of one CTA, walked alike by every role.
+// The pieces of one CTA, walked alike by every role: its units of the groups'
+// items, then its part of the requests'.
 struct Walk {
   const AttnPlan* P;
-  int Hkv, c, q, Q, item, head;
-  unsigned long long share;
+  int Hkv, c, units, next_unit, q, Q, q_item, q_head;
+  unsigned long long a, b;
   AttnItem it;
   AttnSpan span;
-  int t0, t1;
+  int head, unit, t0, t1;
 
   __device__ __forceinline__ Walk(const AttnPlan& P_, const AttnDims& A)
-      : P(&P_), Hkv(A.Hkv), c(blockIdx.x) {
-    share = P->head->share;
-    Q = uniform(P->head->items * Hkv);
-    q = uniform(P->qfirst[c]);  // the item that holds the start of the share
-    item = q / Hkv;
-    head = q - item * Hkv - 1;
+      : P(&P_), Hkv(A.Hkv), c(blockIdx.x), next_unit(blockIdx.x), span{0, 0}, unit(0) {
+    const AttnHead h = *P->head;
+    a = P->begin[c], b = P->begin[c + 1];
+    q = uniform(P->qfirst[c]);  // the item that holds the part's start
+    units = uniform(h.units);
+    Q = uniform((h.items - h.own_first) * Hkv);
+    q_item = uniform(h.own_first) + q / Hkv;
+    q_head = q - q / Hkv * Hkv - 1;
     --q;
   }
-  // The next piece with tiles; `empty` is called for those without (a share's
+  // The next piece with tiles; `empty` is called for those without (a part's
   // end can fall so close to an item's that no tile is left).
   template <class F>
   __device__ __forceinline__ bool next(F empty) {
+    if (next_unit < units) {
+      const AttnUnit u = P->units[next_unit];
+      unit = next_unit;
+      next_unit += P->ctas;
+      it = P->items[u.item];
+      head = uniform(u.head);
+      t0 = uniform(u.t0), t1 = uniform(u.t1);
+      return true;
+    }
     while (true) {
       ++q;
-      if (++head == Hkv) head = 0, ++item;
+      if (++q_head == Hkv) q_head = 0, ++q_item;
       if (q >= Q) return false;
       span = P->spans[q];
       if (uniform(span.c0) > c) return false;
-      it = P->items[item];
-      piece_tiles(it, it.off + (unsigned long long)head * it.cost, share, span, c, t0, t1);
+      it = P->items[q_item];
+      head = q_head;
+      piece_tiles(it, it.off + (unsigned long long)head * it.cost, a, b, span, c, t0, t1);
       t0 = uniform(t0), t1 = uniform(t1);
       if (t0 < t1) return true;
       empty();
@@ -253,14 +266,19 @@ struct Walk {
   __device__ __forceinline__ bool next() {
     return next([] {});
   }
-  __device__ __forceinline__ bool split() const { return span.c0 != span.c1; }
+  __device__ __forceinline__ bool direct() const {
+    return it.kind == ITEM_OWN && span.c0 == span.c1;
+  }
   // Bring what next() will read to the L1, while there is something else to do.
   __device__ __forceinline__ void touch_next() const {
-    if (q + 1 >= Q) return;
-    touch(P->spans + q + 1);
-    if (head + 1 == Hkv) {
-      touch(P->items + item + 1);
-      touch(reinterpret_cast<const char*>(P->items + item + 1) + 32);
+    if (next_unit < units) {
+      touch(P->units + next_unit);
+    } else if (q + 1 < Q) {
+      touch(P->spans + q + 1);
+      if (q_head + 1 == Hkv) {
+        touch(P->items + q_item + 1);
+        touch(reinterpret_cast<const char*>(P->items + q_item + 1) + 32);
+      }
     }
   }
 };
@@ -529,7 +547,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
     auto advance = [&](Walk& V) {
       return V.next([&] {
         if (tid < V.it.m_cnt)
-          pml[partial(P, V.it, V.head, A.Hq, A.G, V.span, V.c, tid, D).row] =
+          pml[partial(P, V.it, V.head, A.Hq, A.G, V.span, V.unit, V.c, tid, D).row] =
               make_float2(-INFINITY, 0.0f);
       });
     };
@@ -682,11 +700,11 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
       // whether an infinite or NaN value was taken out of a tile of this item
       const bool strange = words[2 + items % 3] != 0;
       if (rows_here) {
-        const bool direct = it.kind == ITEM_OWN && !W.split();
+        const bool direct = W.direct();
         const bool mine = tid < it.m_cnt;
         const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
         const AttnPart part = direct || !mine ? AttnPart{0, 0, 0}
-                                              : partial(P, it, W.head, A.Hq, A.G, W.span, W.c, tid, D);
+                                              : partial(P, it, W.head, A.Hq, A.G, W.span, W.unit, W.c, tid, D);
         T* dst = o + (row * A.Hq + hq) * D;
         float* pdst = po + part.at;
         const bool wide = (((uintptr_t)o | (uintptr_t)po) & 31) == 0;

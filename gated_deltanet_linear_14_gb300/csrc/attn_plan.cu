@@ -13,6 +13,7 @@ AttnLayout attn_layout(const AttnDims& A, const KvBatch& B) {
   AttnLayout L{};
   auto up = [](size_t x) { return (x + 63) & ~(size_t)63; };
   L.ctas = device_sms() * attn_ctas_per_sm(A.D);
+  if (L.ctas > kPlanThreads) L.ctas = kPlanThreads;  // the plan holds a CTA per thread
   L.ents = B.num_groups + B.R;
   L.item_cost = item_cost(A, B);
   // rows that may join: at most kJoinRows / G per request
@@ -20,10 +21,15 @@ AttnLayout attn_layout(const AttnDims& A, const KvBatch& B) {
   L.max_list = (int)(join < B.num_rows ? join : B.num_rows);
   const long long pairs = (long long)B.num_rows * A.G + (long long)L.max_list * A.G;
   L.max_items = (int)(pairs / kAttnM + L.ents + 2);
+  L.unit_slots = B.num_groups ? kRounds * L.ctas : 0;
+  const long long whole = ((long long)L.max_list * A.G / kAttnM + B.num_groups + 1) * A.Hkv;
+  L.max_units = B.num_groups ? (int)(whole > L.unit_slots ? whole : L.unit_slots) : 0;
   size_t at = up(sizeof(AttnHead));
+  L.begin = at, at = up(at + 8 * ((size_t)L.ctas + 1));
   L.qfirst = at, at = up(at + 4 * ((size_t)L.ctas + 1));
   L.items = at, at = up(at + sizeof(AttnItem) * (size_t)L.max_items);
   L.spans = at, at = up(at + sizeof(AttnSpan) * (size_t)L.max_items * A.Hkv);
+  L.units = at, at = up(at + sizeof(AttnUnit) * (size_t)L.max_units);
   L.list = at, at = up(at + sizeof(AttnRow) * (size_t)L.max_list);
   L.joins = at, at = up(at + sizeof(AttnJoin) * (size_t)L.max_list * A.Hkv);
   L.first_item = at, at = up(at + 4 * ((size_t)L.ents + 1));
@@ -32,8 +38,10 @@ AttnLayout attn_layout(const AttnDims& A, const KvBatch& B) {
   L.g_shared = at, at = up(at + 4 * (size_t)B.num_groups);
   L.g_rows = at, at = up(at + 4 * (size_t)B.num_groups);
   L.g_off = at, at = up(at + 4 * (size_t)B.num_groups);
+  L.g_unit = at, at = up(at + 4 * ((size_t)B.num_groups + 1));
   L.bytes = at;
-  L.ws_rows = ((long long)2 * L.ctas * kAttnM + 2 * (long long)L.max_list * A.Hq + 31) / 32 * 32;
+  L.ws_rows = ((long long)(2 * L.ctas + L.unit_slots) * kAttnM +
+               2 * (long long)L.max_list * A.Hq + 31) / 32 * 32;
   L.ws_ml = (size_t)L.ws_rows * A.D * 4;
   L.ws_bytes = L.ws_ml + (size_t)L.ws_rows * 8;
   return L;
@@ -71,12 +79,18 @@ __global__ void __launch_bounds__(kPlanThreads)
 attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* status) {
   __shared__ unsigned long long scan64[32];
   __shared__ int scan32[32];
+  // (a CTA's part of the line of cost, and what its units cost)
+  __shared__ unsigned long long begin_s[kPlanThreads + 1];
+  __shared__ unsigned long long used_s[kPlanThreads], share_s;
+  __shared__ int cut_s[kRounds], cuts_s[kRounds];
   pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, NG = B.num_groups;
   AttnHead* head = (AttnHead*)plan;
+  unsigned long long* begin = (unsigned long long*)(plan + L.begin);
   int32_t* qfirst = (int32_t*)(plan + L.qfirst);
   AttnItem* items = (AttnItem*)(plan + L.items);
   AttnSpan* spans = (AttnSpan*)(plan + L.spans);
+  AttnUnit* units = (AttnUnit*)(plan + L.units);
   AttnRow* list = (AttnRow*)(plan + L.list);
   AttnJoin* join = (AttnJoin*)(plan + L.joins);
   int32_t* first_item = (int32_t*)(plan + L.first_item);
@@ -85,6 +99,7 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
   int32_t* g_shared = (int32_t*)(plan + L.g_shared);
   int32_t* g_rows = (int32_t*)(plan + L.g_rows);
   int32_t* g_off = (int32_t*)(plan + L.g_off);
+  int32_t* g_unit = (int32_t*)(plan + L.g_unit);
 
   auto valid = [&](int r, int& start, int& len, int& kv) {
     start = B.row_start[r], len = B.row_len[r], kv = B.kv_len[r];
@@ -190,6 +205,40 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
   }
   if (tid == 0) first_item[L.ents] = n_items;
   __syncthreads();
+  const int own_first = first_item[NG];
+  auto tiles_of = [&](int g) { return (g_shared[g] + kAttnKeys - 1) / kAttnKeys; };
+  auto rows_of = [&](int g) { return first_item[g + 1] - first_item[g]; };  // tiles of pairs
+
+  // Warp x: the shortest pieces of which there are at most x + 1 per CTA.
+  if (warp < kRounds && own_first > 0) {
+    const long long most = (long long)(warp + 1) * L.ctas;
+    auto count = [&](int len) {
+      long long n = 0;
+      for (int g = lane; g < NG; g += 32)
+        if (g_rows[g]) n += (long long)rows_of(g) * ((tiles_of(g) + len - 1) / len);
+#pragma unroll
+      for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(~0u, n, d);
+      return n * A.Hkv;
+    };
+    int longest = 0;
+    for (int g = lane; g < NG; g += 32)
+      if (g_rows[g]) longest = max(longest, tiles_of(g));
+#pragma unroll
+    for (int d = 16; d; d >>= 1) longest = max(longest, __shfl_xor_sync(~0u, longest, d));
+    int lo = 1, hi = longest;
+    const bool can = count(hi) <= most;
+    while (can && lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (count(mid) <= most) hi = mid;
+      else lo = mid + 1;
+    }
+    const long long n = count(hi);
+    if (lane == 0) {
+      cut_s[warp] = can ? hi : longest;
+      cuts_s[warp] = can ? (int)n : -1;
+    }
+  }
+  __syncthreads();
   unsigned long long at = 0;
   for (int b = 0; b < n_items; b += kPlanThreads) {
     const int i = b + tid;
@@ -208,6 +257,7 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
         it.m_cnt = min(kAttnM, g_rows[lo] * A.G - it.m0);
         it.kend = g_shared[lo];
         it.req = list[it.row_base].req;
+        it.cost = 0;
       } else {
         int start, len, kv;
         it.req = lo - NG;
@@ -221,27 +271,131 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
         it.kend = it.vis0 + (it.m0 + it.m_cnt - 1) / A.G;
       }
       it.tiles = (it.kend - it.k0 + kAttnKeys - 1) / kAttnKeys;
-      it.cost = it.tiles * kTileCost + L.item_cost;
+      if (lo >= NG) it.cost = it.tiles * kTileCost + L.item_cost;
     }
     unsigned long long total;
     it.off = at + block_scan((unsigned long long)it.cost * A.Hkv, total, scan64);
     if (i < n_items) items[i] = it;
     at += total;
   }
-  // equal shares, none below one tile and its item's own cost
-  const unsigned long long share =
-      max((at + L.ctas - 1) / L.ctas, (unsigned long long)(kTileCost + L.item_cost));
-  const int Q = n_items * A.Hkv;
-  for (int c = tid; c <= L.ctas; c += kPlanThreads) qfirst[c] = Q;
-  if (tid == 0) *head = AttnHead{share, at, n_items, min(list_rows, L.max_list)};
   __syncthreads();
+  // Of the ways to cut the groups' items, the one that ends first: its longest
+  // CTA, or everybody's part where the requests' items fill that up.
+  int len = 0, rounds = 0;
+  if (own_first > 0) {
+    unsigned long long keys = 0, best = ~0ull;
+    for (int g = tid; g < NG; g += kPlanThreads)
+      if (g_rows[g]) keys += (unsigned long long)rows_of(g) * tiles_of(g);
+    unsigned long long all;
+    block_scan(keys, all, scan64);
+    for (int x = 0; x < kRounds; ++x) {
+      if (cuts_s[x] < 0) continue;
+      const unsigned long long longest =
+          (unsigned long long)(x + 1) * (cut_s[x] * kTileCost + L.item_cost);
+      const unsigned long long part =
+          (at + all * A.Hkv * kTileCost + (unsigned long long)cuts_s[x] * L.item_cost) / L.ctas + 1;
+      const unsigned long long end = max(longest, part);
+      if (end >= best) continue;
+      best = end;
+      rounds = x + 1;
+      // longer pieces where everybody's part has room for them: fewer to join
+      const long long room = ((long long)(part / rounds) - L.item_cost) / kTileCost;
+      len = max(cut_s[x], (int)min(room, (long long)0x7fffffff));
+    }
+    if (rounds == 0) len = cut_s[0];  // more items than kRounds per CTA: none is cut
+  }
+  int n_units = 0;
+  for (int b = 0; b < NG; b += kPlanThreads) {
+    const int g = b + tid;
+    const int n = g < NG && g_rows[g] && len
+                      ? rows_of(g) * ((tiles_of(g) + len - 1) / len) * A.Hkv
+                      : 0;
+    int total;
+    const int off = n_units + block_scan(n, total, scan32);
+    if (g < NG) g_unit[g] = off;
+    n_units += total;
+  }
+  if (tid == 0) g_unit[NG] = n_units;
+  n_units = min(n_units, L.max_units);
+  __syncthreads();
+  for (int k = tid; k < n_units; k += kPlanThreads) {
+    int lo = 0, hi = NG;  // the last group that starts at or before unit k
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (g_unit[mid] <= k) lo = mid;
+      else hi = mid;
+    }
+    const int T = tiles_of(lo), np = (T + len - 1) / len, mt = rows_of(lo), x = k - g_unit[lo];
+    const int m = x % mt, piece = x / mt % np, h = x / (mt * np);
+    units[k] = AttnUnit{first_item[lo] + m, h, (int)((long long)piece * T / np),
+                        (int)((long long)(piece + 1) * T / np)};
+    if (piece == 0 && h == 0) items[first_item[lo] + m].pieces = np;
+  }
+  __syncthreads();
+  // What is left to each CTA beside its units, so that all end together; less
+  // than one tile and an item's own cost is not worth beginning.
+  const unsigned least = kTileCost + L.item_cost;
+  unsigned long long used = 0;
+  if (tid < L.ctas)
+    for (int k = tid; k < n_units; k += L.ctas)
+      used += (units[k].t1 - units[k].t0) * kTileCost + L.item_cost;
+  used_s[tid] = used;
+  __syncthreads();
+  if (warp == 0) {
+    auto room = [&](unsigned long long share) {
+      unsigned long long n = 0;
+      for (int c = lane; c < L.ctas; c += 32)
+        n += share >= used_s[c] + least ? share - used_s[c] : 0;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(~0u, n, d);
+      return n;
+    };
+    unsigned long long most = 0;
+    for (int c = lane; c < L.ctas; c += 32) most = max(most, used_s[c]);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) most = max(most, __shfl_xor_sync(~0u, most, d));
+    unsigned long long lo = max((at + L.ctas - 1) / L.ctas, (unsigned long long)least);
+    unsigned long long hi = lo + most + least;
+    while (lo < hi) {
+      const unsigned long long mid = (lo + hi) >> 1;
+      if (room(mid) >= at) hi = mid;
+      else lo = mid + 1;
+    }
+    if (lane == 0) share_s = hi;
+  }
+  __syncthreads();
+  {
+    const unsigned long long share = share_s;
+    const unsigned long long n =
+        tid < L.ctas && share >= used + least ? share - used : 0;
+    unsigned long long total;
+    const unsigned long long off = block_scan(n, total, scan64);
+    if (tid < L.ctas) begin[tid] = begin_s[tid] = off;
+    if (tid == 0) begin[L.ctas] = begin_s[L.ctas] = total;
+  }
+  const int Q = (n_items - own_first) * A.Hkv;
+  for (int c = tid; c <= L.ctas; c += kPlanThreads) qfirst[c] = Q;
+  if (tid == 0) *head = AttnHead{n_items, own_first, min(list_rows, L.max_list), n_units};
+  __syncthreads();
+  // the first part that begins at x or after it
+  auto lower = [&](unsigned long long x) {
+    int lo = 0, hi = L.ctas + 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (begin_s[mid] < x) lo = mid + 1;
+      else hi = mid;
+    }
+    return lo;
+  };
   for (int q = tid; q < Q; q += kPlanThreads) {
     const int i = q / A.Hkv;
-    const uint32_t cost = items[i].cost;
-    const unsigned long long off = items[i].off + (unsigned long long)(q - i * A.Hkv) * cost;
-    const int c0 = (int)(off / share), c1 = (int)((off + cost - 1) / share);
-    spans[q] = AttnSpan{c0, c1};
-    for (int c = (unsigned long long)c0 * share == off ? c0 : c0 + 1; c <= c1; ++c) qfirst[c] = q;
+    const uint32_t cost = items[own_first + i].cost;
+    const unsigned long long off =
+        items[own_first + i].off + (unsigned long long)(q - i * A.Hkv) * cost;
+    // the last parts that begin at or before its start, and before its end
+    const int first = lower(off), end = lower(off + cost);
+    spans[q] = AttnSpan{lower(off + 1) - 1, end - 1};
+    for (int c = first; c < end; ++c) qfirst[c] = q;
   }
   __syncthreads();
   const int joins_n = min(list_rows, L.max_list) * A.Hkv;
@@ -249,10 +403,12 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
     const int i = x / A.Hkv, h = x - i * A.Hkv;
     const AttnRow lr = list[i];
     if (lr.row < 0) continue;
-    const int gi = first_item[lr.group] + lr.group_m / kAttnM;
-    const int gj = first_item[lr.group] + (lr.group_m + A.G - 1) / kAttnM;
-    join[x] = AttnJoin{spans[first_item[NG + lr.req] * A.Hkv + h],
-                       {spans[gi * A.Hkv + h], spans[gj * A.Hkv + h]},
+    const int mt = rows_of(lr.group), np = (tiles_of(lr.group) + len - 1) / len;
+    const int first = g_unit[lr.group] + h * np * mt;
+    join[x] = AttnJoin{spans[(first_item[NG + lr.req] - own_first) * A.Hkv + h],
+                       {first + lr.group_m / kAttnM, first + (lr.group_m + A.G - 1) / kAttnM},
+                       np,
+                       mt,
                        {0, 0}};
   }
 }
@@ -285,16 +441,17 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
   const int lane = threadIdx.x & 31, d = (threadIdx.x >> 5) * 16;
   int m1 = 0, m2 = 0, row = 0, hq = 0, entry = 0;
   bool work = false;
-  AttnSpan s1{0, 0}, s2{0, -1};
+  AttnSpan s1{0, 0};
+  int unit = 0, pieces = 0, stride = 0;
   if ((int)blockIdx.x >= list_blocks) {
     const int c = (blockIdx.x - list_blocks) >> 2;
-    const int q = P.qfirst[c + 1];  // holds the start of share c + 1
-    if (q < P.head->items * A.Hkv) {
-      const AttnItem it = P.items[q / A.Hkv];
+    const int q = P.qfirst[c + 1];  // holds the start of CTA c + 1's part
+    if (q < (P.head->items - P.head->own_first) * A.Hkv) {
+      const AttnItem it = P.items[P.head->own_first + q / A.Hkv];
       s1 = P.spans[q];
       m1 = ((blockIdx.x - list_blocks) & 3) * 32 + lane;
-      // cut there, begun in share c, and not joined with another item (an
-      // item that begins exactly there has its first piece in share c + 1)
+      // cut there, begun in CTA c's part, and not joined with another item (an
+      // item that begins exactly there has its first piece in the next part)
       work = it.kind == ITEM_OWN && s1.c0 == c && s1.c1 > c && m1 < it.m_cnt;
       const int mi = it.m0 + m1, i = mi / A.G;
       row = it.row_base + i;
@@ -313,7 +470,9 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
       hq = head * A.G + hg;
       s1 = jn.own;
       m1 = lr.own_m + hg;
-      s2 = jn.group[(lr.group_m + hg) / kAttnM != lr.group_m / kAttnM ? 1 : 0];
+      unit = jn.unit[(lr.group_m + hg) / kAttnM != lr.group_m / kAttnM ? 1 : 0];
+      pieces = jn.pieces;
+      stride = jn.stride;
       m2 = (lr.group_m + hg) % kAttnM;
     }
   }
@@ -322,12 +481,13 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
   if (blockIdx.x != 0 && !__any_sync(~0u, work)) return;
   pdl_begin();
   if (!work) return;
-  const int n1 = s1.c1 - s1.c0 + 1, n = n1 + s2.c1 - s2.c0 + 1;
+  const int n1 = s1.c1 - s1.c0 + 1, n = n1 + pieces;
   auto part = [&](int p) {
-    const AttnSpan sp = p < n1 ? s1 : s2;
-    return sp.c0 == sp.c1 ? whole_part(P, A.Hq, A.G, p >= n1, entry, hq, D)
-           : p < n1       ? split_part(sp, sp.c0 + p, m1, D)
-                          : split_part(sp, sp.c0 + p - n1, m2, D);
+    if (p < n1)
+      return n1 == 1 ? whole_part(P, A.Hq, A.G, false, entry, hq, D)
+                     : split_part(s1, s1.c0 + p, m1, D);
+    return pieces == 1 ? whole_part(P, A.Hq, A.G, true, entry, hq, D)
+                       : unit_part(P, unit + (p - n1) * stride, m2, D);
   };
   float top = -INFINITY, sum = 0.0f, acc[16];
 #pragma unroll
