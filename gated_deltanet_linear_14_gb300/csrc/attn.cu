@@ -297,7 +297,9 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
   const uint32_t sb = smem_u32(smem), ring = sb + C::RING;
   const uint32_t full = sb + C::BARS, empty = full + 8 * NS, q_full = empty + 8 * NS;
   const uint32_t s_full = q_full + 8, p_ready = s_full + 8 * NSB, o_full = p_ready + 8 * NSB;
-  volatile uint32_t* words = reinterpret_cast<uint32_t*>(smem + C::BARS + 8 * (2 * NS + 1 + 3 * NSB));
+  // [0] tensor memory, [1] a role gave up, [2..4] see `strange`
+  volatile uint32_t* words =
+      reinterpret_cast<uint32_t*>(smem + C::BARS + 8 * (2 * NS + 1 + 3 * NSB));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
@@ -497,7 +499,8 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
     // tile with few rows is fetched by all)
     auto fetch_q = [&](const Walk& V) {
       if (C::QT || V.it.m_cnt <= warp) return;
-      constexpr int CH = D / 8, RPI = CH < 32 ? 32 / CH : 1;  // 16-byte pieces of a row, rows at once
+      // 16-byte pieces of a row, rows at once
+      constexpr int CH = D / 8, RPI = CH < 32 ? 32 / CH : 1;
       int i, hq;
       const long long row = pair_of(V.it, V.head, 4 * lane + warp, i, hq);
       const unsigned long long src = (unsigned long long)(q + row * qs + (long long)hq * D);
@@ -703,8 +706,9 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
         const bool direct = W.direct();
         const bool mine = tid < it.m_cnt;
         const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-        const AttnPart part = direct || !mine ? AttnPart{0, 0, 0}
-                                              : partial(P, it, W.head, A.Hq, A.G, W.span, W.unit, W.c, tid, D);
+        AttnPart part{0, 0, 0};
+        if (mine && !direct)
+          part = partial(P, it, W.head, A.Hq, A.G, W.span, W.unit, W.c, tid, D);
         T* dst = o + (row * A.Hq + hq) * D;
         float* pdst = po + part.at;
         const bool wide = (((uintptr_t)o | (uintptr_t)po) & 31) == 0;

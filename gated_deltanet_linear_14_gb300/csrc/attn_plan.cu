@@ -427,7 +427,7 @@ cudaError_t launch_attn_plan(const AttnDims& A, const KvBatch& B, void* plan, in
 // A thread takes 16 elements of a (row, query head) pair, the lanes of a warp
 // 32 neighbouring pairs of a tile, whose partial rows lie side by side. Blocks
 // are 32 pairs x D / 16: first the pairs of the list's rows, head by head,
-// then four per CTA for the items that are cut by a share's end. What a thread
+// then one per CTA for the item that its part's end cuts. What a thread
 // reads of the plan it reads before the attention kernel ends (the plan was
 // complete when that kernel began), so only the pieces' own latency follows.
 
@@ -439,37 +439,37 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
                  const float2* __restrict__ pml, T* __restrict__ o, float* __restrict__ lse,
                  int list_blocks, bool wide) {
   const int lane = threadIdx.x & 31, d = (threadIdx.x >> 5) * 16;
-  int m1 = 0, m2 = 0, row = 0, hq = 0, entry = 0;
-  bool work = false;
+  int m1 = 0, m_end = 0, m2 = 0, row = 0, hq = 0, entry = 0, head = 0;
+  AttnItem it{};
   AttnSpan s1{0, 0};
   int unit = 0, pieces = 0, stride = 0;
-  if ((int)blockIdx.x >= list_blocks) {
-    const int c = (blockIdx.x - list_blocks) >> 2;
+  const bool cut = (int)blockIdx.x >= list_blocks;
+  if (cut) {
+    const int c = blockIdx.x - list_blocks;
     const int q = P.qfirst[c + 1];  // holds the start of CTA c + 1's part
     if (q < (P.head->items - P.head->own_first) * A.Hkv) {
-      const AttnItem it = P.items[P.head->own_first + q / A.Hkv];
+      it = P.items[P.head->own_first + q / A.Hkv];
       s1 = P.spans[q];
-      m1 = ((blockIdx.x - list_blocks) & 3) * 32 + lane;
+      head = q % A.Hkv;
+      m1 = lane;
       // cut there, begun in CTA c's part, and not joined with another item (an
       // item that begins exactly there has its first piece in the next part)
-      work = it.kind == ITEM_OWN && s1.c0 == c && s1.c1 > c && m1 < it.m_cnt;
-      const int mi = it.m0 + m1, i = mi / A.G;
-      row = it.row_base + i;
-      hq = q % A.Hkv * A.G + mi - i * A.G;
+      if (it.kind == ITEM_OWN && s1.c0 == c && s1.c1 > c) m_end = it.m_cnt;
     }
   } else {
-    const int blocks = list_blocks / A.Hkv, head = blockIdx.x / blocks;
+    const int blocks = list_blocks / A.Hkv;
+    head = blockIdx.x / blocks;
     const int x = (blockIdx.x - head * blocks) * 32 + lane;
     entry = x / A.G;
     if (entry < P.head->list_rows) {
       const int hg = x - entry * A.G;
       const AttnRow lr = P.list[entry];
       const AttnJoin jn = P.joins[(long long)entry * A.Hkv + head];
-      work = lr.row >= 0;
       row = lr.row;
       hq = head * A.G + hg;
       s1 = jn.own;
       m1 = lr.own_m + hg;
+      if (row >= 0) m_end = m1 + 1;
       unit = jn.unit[(lr.group_m + hg) / kAttnM != lr.group_m / kAttnM ? 1 : 0];
       pieces = jn.pieces;
       stride = jn.stride;
@@ -478,9 +478,8 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
   }
   // (the first block always waits: the grid must not end before the attention
   // kernel has)
-  if (blockIdx.x != 0 && !__any_sync(~0u, work)) return;
+  if (blockIdx.x != 0 && !__any_sync(~0u, m1 < m_end)) return;
   pdl_begin();
-  if (!work) return;
   const int n1 = s1.c1 - s1.c0 + 1, n = n1 + pieces;
   auto part = [&](int p) {
     if (p < n1)
@@ -489,47 +488,54 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
     return pieces == 1 ? whole_part(P, A.Hq, A.G, true, entry, hq, D)
                        : unit_part(P, unit + (p - n1) * stride, m2, D);
   };
-  float top = -INFINITY, sum = 0.0f, acc[16];
+  for (; m1 < m_end; m1 += 32) {
+    if (cut) {
+      const int mi = it.m0 + m1, i = mi / A.G;
+      row = it.row_base + i;
+      hq = head * A.G + mi - i * A.G;
+    }
+    float top = -INFINITY, sum = 0.0f, acc[16];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
-  // kJoinBatch pieces in flight; past the last one, that one again with weight 0
-  for (int p = 0; p < n; p += kJoinBatch) {
-    float2 ml[kJoinBatch];
-    float v[kJoinBatch][16];
+    for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
+    // kJoinBatch pieces in flight; past the last one, that one again with weight 0
+    for (int p = 0; p < n; p += kJoinBatch) {
+      float2 ml[kJoinBatch];
+      float v[kJoinBatch][16];
 #pragma unroll
-    for (int k = 0; k < kJoinBatch; ++k) {
-      const AttnPart at = part(min(p + k, n - 1));
-      ml[k] = pml[at.row];
-      const float* src = po + at.at + (d >> 3) * at.step;
+      for (int k = 0; k < kJoinBatch; ++k) {
+        const AttnPart at = part(min(p + k, n - 1));
+        ml[k] = pml[at.row];
+        const float* src = po + at.at + (d >> 3) * at.step;
 #pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        *(float4*)(v[k] + e) = *(const float4*)(src + e);
-        *(float4*)(v[k] + 8 + e) = *(const float4*)(src + at.step + e);
+        for (int e = 0; e < 8; e += 4) {
+          *(float4*)(v[k] + e) = *(const float4*)(src + e);
+          *(float4*)(v[k] + 8 + e) = *(const float4*)(src + at.step + e);
+        }
+      }
+      float nt = top;
+#pragma unroll
+      for (int k = 0; k < kJoinBatch; ++k) nt = fmaxf(nt, ml[k].x);
+      const float ref = nt == -INFINITY ? 0.0f : nt, back = exp2f(top - ref);
+      top = nt;
+      sum *= back;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[e] *= back;
+#pragma unroll
+      for (int k = 0; k < kJoinBatch; ++k) {
+        const float w = p + k < n ? exp2f(ml[k].x - ref) : 0.0f;
+        if (p + k < n) sum += w * ml[k].y;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)  // a piece without tiles has weight 0 and no o
+          acc[e] = w == 0.0f ? acc[e] : acc[e] + w * v[k][e];
       }
     }
-    float nt = top;
+    const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+    uint32_t out[8];
 #pragma unroll
-    for (int k = 0; k < kJoinBatch; ++k) nt = fmaxf(nt, ml[k].x);
-    const float ref = nt == -INFINITY ? 0.0f : nt, back = exp2f(top - ref);
-    top = nt;
-    sum *= back;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) acc[e] *= back;
-#pragma unroll
-    for (int k = 0; k < kJoinBatch; ++k) {
-      const float w = p + k < n ? exp2f(ml[k].x - ref) : 0.0f;
-      if (p + k < n) sum += w * ml[k].y;
-#pragma unroll
-      for (int e = 0; e < 16; ++e)  // a piece without tiles has weight 0 and no o
-        acc[e] = w == 0.0f ? acc[e] : acc[e] + w * v[k][e];
-    }
+    for (int e = 0; e < 8; ++e) out[e] = pack2<T>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    store32B(o + ((size_t)row * A.Hq + hq) * D + d, out, wide);
+    if (lse && d == 0) lse[(size_t)row * A.Hq + hq] = (top + log2f(sum)) * 0.693147180559945309f;
   }
-  const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-  uint32_t out[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) out[e] = pack2<T>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  store32B(o + ((size_t)row * A.Hq + hq) * D + d, out, wide);
-  if (lse && d == 0) lse[(size_t)row * A.Hq + hq] = (top + log2f(sum)) * 0.693147180559945309f;
 }
 
 cudaError_t launch_attn_join(const AttnDims& A, const KvBatch& B, int io, const void* plan,
@@ -539,7 +545,7 @@ cudaError_t launch_attn_join(const AttnDims& A, const KvBatch& B, int io, const 
   const float* po = (const float*)ws;
   const float2* pml = (const float2*)((const char*)ws + L.ws_ml);
   const int list_blocks = (int)(((long long)L.max_list * A.G + 31) / 32) * A.Hkv;
-  const dim3 grid(list_blocks + 4 * L.ctas), block(2 * A.D);
+  const dim3 grid(list_blocks + L.ctas), block(2 * A.D);
   const bool wide = ((uintptr_t)o & 31) == 0;
   auto go = [&](auto t, auto d) {
     using T = decltype(t);

@@ -26,14 +26,14 @@ namespace gdn {
 constexpr int kAttnM = 128;      // (row, head) pairs of an item: the tensor core's M
 constexpr int kAttnKeys = 64;    // keys of a tile
 constexpr unsigned kTileCost = 4;
-// Cost of an item beside its tiles: its start and its end, least-squares fits
-// of CTA times. Where the step is bound by memory (short rows, nothing shared)
-// others' fetches cover it: 0.9 us against 1.3 us a tile (decode, D = 128).
-// Where it is bound by the SMs: D = 64 2.3 against 0.75 us, D = 128 3.8
-// against 0.62 us, D = 256 3.4 against 1.0 us.
+// Cost of an item (or a piece of a group's) beside its tiles: its start and its
+// end, as least-squares fits of CTA times gave it. Where the step is bound by
+// memory (short rows, nothing shared) others' fetches cover it: 0.9 us against
+// 1.3 us a tile (D = 128). Where it is bound by the SMs: 2.1 us against 0.75
+// (D = 64), 3.1 against 0.7 (D = 128), 4.0 against 1.1 (D = 256). (Of 8, 12, 14
+// and 20 for the latter, 20 measured best on all three.)
 inline unsigned item_cost(const AttnDims& A, const KvBatch& B) {
-  if (B.num_groups == 0 && (long long)B.max_rows * A.G <= 64) return 3;
-  return 20;
+  return B.num_groups == 0 && (long long)B.max_rows * A.G <= 64 ? 3 : 20;
 }
 // A request joins its group's shared pass with up to this many (row, head)
 // pairs; above, its own tiles are full enough to read the shared keys alone.
@@ -100,8 +100,8 @@ struct AttnLayout {
   unsigned item_cost;
   int unit_slots;  // partial tiles of units
   int max_units;
-  size_t begin, qfirst, items, spans, units, list, joins, first_item, k0, req_list, g_shared, g_rows,
-      g_off, g_unit, bytes;
+  size_t begin, qfirst, items, spans, units, list, joins, first_item, k0, req_list;
+  size_t g_shared, g_rows, g_off, g_unit, bytes;
   size_t ws_ml, ws_bytes;  // partial rows: fp32 o, then (m, l)
   long long ws_rows;
 };
