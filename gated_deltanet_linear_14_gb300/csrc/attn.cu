@@ -211,7 +211,7 @@ __device__ __forceinline__ uint32_t any_not_finite(const uint4& v) {
 
 // A load whose value nobody waits for.
 __device__ __forceinline__ void touch(const void* p) {
-  uint32_t x;
+  [[maybe_unused]] uint32_t x;
   asm volatile("ld.global.u32 %0, [%1];" : "=r"(x) : "l"(p));
 }
 

@@ -83,6 +83,8 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
   __shared__ unsigned long long begin_s[kPlanThreads + 1];
   __shared__ unsigned long long used_s[kPlanThreads], share_s;
   __shared__ int cut_s[kRounds], cuts_s[kRounds];
+  __shared__ unsigned long long saved_s;
+  __shared__ int longest_s, group_tiles_s;  // of the requests' items, of the groups'
   pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, NG = B.num_groups;
   AttnHead* head = (AttnHead*)plan;
@@ -116,6 +118,8 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
     req_list[r] = -1;
   }
   for (int i = tid; i < L.max_list; i += kPlanThreads) list[i].row = -1;
+  if (tid == 0) saved_s = 0, longest_s = 0;
+  __syncthreads();
   // groups: the keys that every joining member's rows all see, in whole pages
   for (int g = warp; g < NG; g += kPlanThreads / 32) {
     const int a = B.group_start[g], n = B.group_len[g];
@@ -137,11 +141,18 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
     }
     pages = min(pages, seen >> A.ps_log2);
     if (lane == 0) {
-      const bool on = members >= 2 && pages > 0 && ((long long)pages << A.ps_log2) >= kMinShared;
-      g_shared[g] = on ? pages << A.ps_log2 : 0;
+      const int keys = pages > 0 && members >= 2 ? pages << A.ps_log2 : 0;
+      const int saved = members - (rows * A.G + kAttnM - 1) / kAttnM;
+      const bool on = keys > 0 && saved > 0;
+      g_shared[g] = on ? keys : 0;
       g_rows[g] = on ? rows : 0;
+      if (on)
+        atomicAdd(&saved_s, (unsigned long long)saved * (keys / kAttnKeys) * A.Hkv);
     }
   }
+  __syncthreads();
+  if (saved_s <= (unsigned long long)kMinSaved * L.ctas)  // not worth the join: nobody shares
+    for (int g = tid; g < NG; g += kPlanThreads) g_shared[g] = g_rows[g] = 0;
   __syncthreads();
   int list_rows = 0;
   for (int b = 0; b < NG; b += kPlanThreads) {
@@ -234,6 +245,7 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
     }
     const long long n = count(hi);
     if (lane == 0) {
+      group_tiles_s = longest;
       cut_s[warp] = can ? hi : longest;
       cuts_s[warp] = can ? (int)n : -1;
     }
@@ -271,7 +283,10 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
         it.kend = it.vis0 + (it.m0 + it.m_cnt - 1) / A.G;
       }
       it.tiles = (it.kend - it.k0 + kAttnKeys - 1) / kAttnKeys;
-      if (lo >= NG) it.cost = it.tiles * kTileCost + L.item_cost;
+      if (lo >= NG) {
+        it.cost = it.tiles * kTileCost + L.item_cost;
+        atomicMax(&longest_s, it.tiles);
+      }
     }
     unsigned long long total;
     it.off = at + block_scan((unsigned long long)it.cost * A.Hkv, total, scan64);
@@ -301,6 +316,7 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
       // longer pieces where everybody's part has room for them: fewer to join
       const long long room = ((long long)(part / rounds) - L.item_cost) / kTileCost;
       len = max(cut_s[x], (int)min(room, (long long)0x7fffffff));
+      len = max(len, least_piece(group_tiles_s));
     }
     if (rounds == 0) len = cut_s[0];  // more items than kRounds per CTA: none is cut
   }
@@ -333,8 +349,8 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
   }
   __syncthreads();
   // What is left to each CTA beside its units, so that all end together; less
-  // than one tile and an item's own cost is not worth beginning.
-  const unsigned least = kTileCost + L.item_cost;
+  // than the shortest piece and an item's own cost is not worth beginning.
+  const unsigned least = kTileCost * least_piece(longest_s) + L.item_cost;
   unsigned long long used = 0;
   if (tid < L.ctas)
     for (int k = tid; k < n_units; k += L.ctas)
@@ -425,8 +441,9 @@ cudaError_t launch_attn_plan(const AttnDims& A, const KvBatch& B, void* plan, in
 // 2^{s - m} and o = sum 2^{s - m} v, so with M = max m
 //   o = sum 2^{m_p - M} o_p / sum 2^{m_p - M} l_p.
 // A thread takes 16 elements of a (row, query head) pair, the lanes of a warp
-// 32 neighbouring pairs of a tile, whose partial rows lie side by side. Blocks
-// are 32 pairs x D / 16: first the pairs of the list's rows, head by head,
+// neighbouring pairs of a tile, whose partial rows lie side by side: 32 of
+// them, or where there are few pairs (and so many pieces of each), 4 to 16
+// with the pieces dealt to groups of lanes. Blocks are D / 16 warps: first the pairs of the list's rows, head by head,
 // then one per CTA for the item that its part's end cuts. What a thread
 // reads of the plan it reads before the attention kernel ends (the plan was
 // complete when that kernel began), so only the pieces' own latency follows.
@@ -437,8 +454,9 @@ template <class T, int D>
 __global__ void __launch_bounds__(2 * D)
 attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
                  const float2* __restrict__ pml, T* __restrict__ o, float* __restrict__ lse,
-                 int list_blocks, bool wide) {
+                 int list_blocks, int list_pairs, bool wide) {
   const int lane = threadIdx.x & 31, d = (threadIdx.x >> 5) * 16;
+  int pairs = list_pairs;  // of a warp; lane / pairs is its group's number
   int m1 = 0, m_end = 0, m2 = 0, row = 0, hq = 0, entry = 0, head = 0;
   AttnItem it{};
   AttnSpan s1{0, 0};
@@ -451,7 +469,8 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
       it = P.items[P.head->own_first + q / A.Hkv];
       s1 = P.spans[q];
       head = q % A.Hkv;
-      m1 = lane;
+      pairs = it.m_cnt <= 4 ? 4 : it.m_cnt <= 8 ? 8 : it.m_cnt <= 16 ? 16 : 32;
+      m1 = lane % pairs;
       // cut there, begun in CTA c's part, and not joined with another item (an
       // item that begins exactly there has its first piece in the next part)
       if (it.kind == ITEM_OWN && s1.c0 == c && s1.c1 > c) m_end = it.m_cnt;
@@ -459,7 +478,7 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
   } else {
     const int blocks = list_blocks / A.Hkv;
     head = blockIdx.x / blocks;
-    const int x = (blockIdx.x - head * blocks) * 32 + lane;
+    const int x = (blockIdx.x - head * blocks) * pairs + lane % pairs;
     entry = x / A.G;
     if (entry < P.head->list_rows) {
       const int hg = x - entry * A.G;
@@ -488,7 +507,9 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
     return pieces == 1 ? whole_part(P, A.Hq, A.G, true, entry, hq, D)
                        : unit_part(P, unit + (p - n1) * stride, m2, D);
   };
-  for (; m1 < m_end; m1 += 32) {
+  const int groups = 32 / pairs, turns = cut ? (m_end + pairs - 1) / pairs : 1;
+  for (int turn = 0; turn < turns; ++turn, m1 += pairs) {
+    const bool mine = m1 < m_end;
     if (cut) {
       const int mi = it.m0 + m1, i = mi / A.G;
       row = it.row_base + i;
@@ -498,12 +519,12 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
     // kJoinBatch pieces in flight; past the last one, that one again with weight 0
-    for (int p = 0; p < n; p += kJoinBatch) {
+    for (int p = lane / pairs; mine && p < n; p += kJoinBatch * groups) {
       float2 ml[kJoinBatch];
       float v[kJoinBatch][16];
 #pragma unroll
       for (int k = 0; k < kJoinBatch; ++k) {
-        const AttnPart at = part(min(p + k, n - 1));
+        const AttnPart at = part(min(p + k * groups, n - 1));
         ml[k] = pml[at.row];
         const float* src = po + at.at + (d >> 3) * at.step;
 #pragma unroll
@@ -522,13 +543,24 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
       for (int e = 0; e < 16; ++e) acc[e] *= back;
 #pragma unroll
       for (int k = 0; k < kJoinBatch; ++k) {
-        const float w = p + k < n ? exp2f(ml[k].x - ref) : 0.0f;
-        if (p + k < n) sum += w * ml[k].y;
+        const bool is = p + k * groups < n;
+        const float w = is ? exp2f(ml[k].x - ref) : 0.0f;
+        if (is) sum += w * ml[k].y;
 #pragma unroll
         for (int e = 0; e < 16; ++e)  // a piece without tiles has weight 0 and no o
           acc[e] = w == 0.0f ? acc[e] : acc[e] + w * v[k][e];
       }
     }
+    for (int x = pairs; x < 32; x <<= 1) {  // the groups' shares of a pair
+      const float other = __shfl_xor_sync(~0u, top, x), nt = fmaxf(top, other);
+      const float ref = nt == -INFINITY ? 0.0f : nt;
+      const float back = exp2f(top - ref), theirs = exp2f(other - ref);
+      sum = sum * back + __shfl_xor_sync(~0u, sum, x) * theirs;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[e] = acc[e] * back + __shfl_xor_sync(~0u, acc[e], x) * theirs;
+      top = nt;
+    }
+    if (!mine || lane >= pairs) continue;
     const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
     uint32_t out[8];
 #pragma unroll
@@ -544,13 +576,16 @@ cudaError_t launch_attn_join(const AttnDims& A, const KvBatch& B, int io, const 
   const AttnPlan P = attn_plan_view(L, plan);
   const float* po = (const float*)ws;
   const float2* pml = (const float2*)((const char*)ws + L.ws_ml);
-  const int list_blocks = (int)(((long long)L.max_list * A.G + 31) / 32) * A.Hkv;
+  // (eight pairs a warp where that still is no more than a few blocks an SM)
+  const int list_pairs = (long long)L.max_list * A.Hq <= 8192 ? 8 : 32;
+  const int list_blocks =
+      (int)(((long long)L.max_list * A.G + list_pairs - 1) / list_pairs) * A.Hkv;
   const dim3 grid(list_blocks + L.ctas), block(2 * A.D);
   const bool wide = ((uintptr_t)o & 31) == 0;
   auto go = [&](auto t, auto d) {
     using T = decltype(t);
     return launch_pdl(attn_join_kernel<T, decltype(d)::value>, grid, block, 0, s, A, P, po, pml,
-                      (T*)o, lse, list_blocks, wide);
+                      (T*)o, lse, list_blocks, list_pairs, wide);
   };
   auto by_dim = [&](auto t) {
     if (A.D == 64) return go(t, std::integral_constant<int, 64>());

@@ -35,11 +35,24 @@ constexpr unsigned kTileCost = 4;
 inline unsigned item_cost(const AttnDims& A, const KvBatch& B) {
   return B.num_groups == 0 && (long long)B.max_rows * A.G <= 64 ? 3 : 20;
 }
+// Tiles below which an item of T is not cut: a piece more costs the join about
+// a twelfth of a tile's time, so cutting further than this pays with the join
+// what it saves in the pass.
+__host__ __device__ inline int least_piece(int T) {
+  int n = 1;
+  while (n < 64 && 12 * n * n < T) ++n;
+  return n;
+}
 // A request joins its group's shared pass with up to this many (row, head)
-// pairs; above, its own tiles are full enough to read the shared keys alone.
+// pairs; above, its own tiles are full enough to read the shared keys alone
+// (16 requests behind 4096 keys, D = 128, G = 4: 16 rows each 27 us shared
+// against 36 alone, 24 rows 43 against 39).
 constexpr int kJoinRows = 64;
-// Shared keys below which reading them per request costs less than the join.
-constexpr int kMinShared = 256;
+// Tiles of keys that sharing has to save, for each CTA (D = 128, 32/8 heads,
+// one row each: 16 requests behind 1024 keys, 6 tiles, 19 us shared against 18
+// alone; behind 2048, 13 tiles, 17.5 against 22; 64 behind 256, 7 tiles, 22
+// against 28).
+constexpr int kMinSaved = 6;
 
 enum { ITEM_OWN = 0, ITEM_JOINED = 1, ITEM_GROUP = 2 };
 
