@@ -15,7 +15,6 @@ AttnLayout attn_layout(const AttnDims& A, const KvBatch& B) {
   L.ctas = device_sms() * attn_ctas_per_sm(A.D);
   if (L.ctas > kPlanThreads) L.ctas = kPlanThreads;  // the plan holds a CTA per thread
   L.ents = B.num_groups + B.R;
-  L.item_cost = item_cost(A, B);
   // rows that may join: at most kJoinRows / G per request
   const long long join = B.num_groups ? (long long)B.R * (kJoinRows / A.G) : 0;
   L.max_list = (int)(join < B.num_rows ? join : B.num_rows);
@@ -151,8 +150,10 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
     }
   }
   __syncthreads();
-  if (saved_s <= (unsigned long long)kMinSaved * L.ctas)  // not worth the join: nobody shares
+  const bool sharing = saved_s > (unsigned long long)kMinSaved * L.ctas;
+  if (!sharing)  // not worth the join
     for (int g = tid; g < NG; g += kPlanThreads) g_shared[g] = g_rows[g] = 0;
+  const unsigned own_cost = item_cost(A, B, sharing);
   __syncthreads();
   int list_rows = 0;
   for (int b = 0; b < NG; b += kPlanThreads) {
@@ -284,7 +285,7 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
       }
       it.tiles = (it.kend - it.k0 + kAttnKeys - 1) / kAttnKeys;
       if (lo >= NG) {
-        it.cost = it.tiles * kTileCost + L.item_cost;
+        it.cost = it.tiles * kTileCost + own_cost;
         atomicMax(&longest_s, it.tiles);
       }
     }
@@ -306,15 +307,15 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
     for (int x = 0; x < kRounds; ++x) {
       if (cuts_s[x] < 0) continue;
       const unsigned long long longest =
-          (unsigned long long)(x + 1) * (cut_s[x] * kTileCost + L.item_cost);
+          (unsigned long long)(x + 1) * (cut_s[x] * kTileCost + own_cost);
       const unsigned long long part =
-          (at + all * A.Hkv * kTileCost + (unsigned long long)cuts_s[x] * L.item_cost) / L.ctas + 1;
+          (at + all * A.Hkv * kTileCost + (unsigned long long)cuts_s[x] * own_cost) / L.ctas + 1;
       const unsigned long long end = max(longest, part);
       if (end >= best) continue;
       best = end;
       rounds = x + 1;
       // longer pieces where everybody's part has room for them: fewer to join
-      const long long room = ((long long)(part / rounds) - L.item_cost) / kTileCost;
+      const long long room = ((long long)(part / rounds) - own_cost) / kTileCost;
       len = max(cut_s[x], (int)min(room, (long long)0x7fffffff));
       len = max(len, least_piece(group_tiles_s));
     }
@@ -350,11 +351,11 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
   __syncthreads();
   // What is left to each CTA beside its units, so that all end together; less
   // than the shortest piece and an item's own cost is not worth beginning.
-  const unsigned least = kTileCost * least_piece(longest_s) + L.item_cost;
+  const unsigned least = kTileCost * least_piece(longest_s) + own_cost;
   unsigned long long used = 0;
   if (tid < L.ctas)
     for (int k = tid; k < n_units; k += L.ctas)
-      used += (units[k].t1 - units[k].t0) * kTileCost + L.item_cost;
+      used += (units[k].t1 - units[k].t0) * kTileCost + own_cost;
   used_s[tid] = used;
   __syncthreads();
   if (warp == 0) {

@@ -32,8 +32,8 @@ constexpr unsigned kTileCost = 4;
 // 1.3 us a tile (D = 128). Where it is bound by the SMs: 2.1 us against 0.75
 // (D = 64), 3.1 against 0.7 (D = 128), 4.0 against 1.1 (D = 256). (Of 8, 12, 14
 // and 20 for the latter, 20 measured best on all three.)
-inline unsigned item_cost(const AttnDims& A, const KvBatch& B) {
-  return B.num_groups == 0 && (long long)B.max_rows * A.G <= 64 ? 3 : 20;
+__host__ __device__ inline unsigned item_cost(const AttnDims& A, const KvBatch& B, bool sharing) {
+  return !sharing && (long long)B.max_rows * A.G <= 64 ? 3 : 20;
 }
 // Tiles below which an item of T is not cut: a piece more costs the join about
 // a twelfth of a tile's time, so cutting further than this pays with the join
@@ -45,14 +45,15 @@ __host__ __device__ inline int least_piece(int T) {
 }
 // A request joins its group's shared pass with up to this many (row, head)
 // pairs; above, its own tiles are full enough to read the shared keys alone
-// (16 requests behind 4096 keys, D = 128, G = 4: 16 rows each 27 us shared
-// against 36 alone, 24 rows 43 against 39).
+// (16 requests behind 4096 keys, D = 128, G = 4, us shared against alone: 8
+// rows each 26 against 33, 12 rows 29 against 35, 16 rows 35.4 against 35.6,
+// 24 rows 43 against 39).
 constexpr int kJoinRows = 64;
-// Tiles of keys that sharing has to save, for each CTA (D = 128, 32/8 heads,
-// one row each: 16 requests behind 1024 keys, 6 tiles, 19 us shared against 18
-// alone; behind 2048, 13 tiles, 17.5 against 22; 64 behind 256, 7 tiles, 22
-// against 28).
-constexpr int kMinSaved = 6;
+// Tiles of keys that sharing has to save, for each CTA (one row each, us shared
+// against alone: D = 128, 64 requests behind 128 keys, 3 tiles, 22.4 against
+// 26.9; 4 behind 2048, 2.5 tiles, 13.8 against 14.2; 16 behind 256, 1.6 tiles,
+// 14.6 against 14.0; D = 256, 16 behind 512, 1.6 tiles, 16.9 against 15.4).
+constexpr int kMinSaved = 2;
 
 enum { ITEM_OWN = 0, ITEM_JOINED = 1, ITEM_GROUP = 2 };
 
@@ -110,7 +111,6 @@ constexpr int kRounds = 4;
 // Byte offsets inside the plan, and the bounds they come from.
 struct AttnLayout {
   int ctas, max_items, max_list, ents;  // ents: groups, then requests
-  unsigned item_cost;
   int unit_slots;  // partial tiles of units
   int max_units;
   size_t begin, qfirst, items, spans, units, list, joins, first_item, k0, req_list;

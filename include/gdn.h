@@ -509,8 +509,8 @@ typedef struct {
  * depend on the groups (up to the order of additions); keys that are declared
  * shared are read once for the group instead of once per request. Groups do
  * not overlap. (Requests with more than 64 (row, query head) pairs per
- * key/value head read the shared keys by themselves, as do groups that share
- * fewer than 256 tokens or have fewer than two shorter requests.) */
+ * key/value head read the shared keys by themselves, as do all where sharing
+ * would save too little to repay the joining of the parts.) */
 typedef struct {
   int32_t num_requests;        /* R                                            */
   int32_t num_rows;            /* rows in the packed q/k/v/o buffers           */
