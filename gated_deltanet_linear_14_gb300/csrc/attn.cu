@@ -22,6 +22,19 @@
 // tensor cores wait for each other only at the start. D <= 128 runs two CTAs
 // per SM (256 TMEM columns each: O and the scores), D = 256 one, with Q in
 // tensor memory too.
+//
+// What bounds it, and what it measured (GB300, join included):
+//   long keys, short rows: HBM. 64 requests of 1 row and up to 16384 keys, D =
+//     128: 300 us for 2.08 GB, 6.9 TB/s, 1.02 of the copy rate;
+//   long prompts: the tensor cores and the shared memory that feeds them (per
+//     64 keys and CTA 640 MMA cycles and 96 KB through shared memory, two CTAs
+//     an SM), and power in a row of calls. 4 x 1500..2048 rows over 8192 + ..
+//     keys, D = 128: 835 us, 1.38 PFLOP/s, 0.73 of the burst matrix product;
+//   many short items: an item's start and end, 2 to 4 us, and its fetch from
+//     the L2. 64 requests of 8 rows in four groups: 61 us for 193 MB.
+// Tiles of 128 keys with one score buffer took 1.3 times longer on prompts;
+// two tiles that share K and V on one CTA per SM gained 3 % on the longest
+// prompts and lost 10 to 30 % on the others.
 #include <cuda.h>
 
 #include <type_traits>
@@ -52,15 +65,15 @@ struct Cfg {
   static constexpr int CU = NC < 2 ? 1 : 2;          // chunks of a ring unit
   static constexpr int NU = NC / CU;                 // units of a tile's keys (or values)
   static constexpr uint32_t UNIT = CU * kChunk;
-  static constexpr int NS = D == 64 ? 8 : D == 128 ? 4 : 10;  // units of the ring
+  // Units of the ring. (As many as fit, 12, 5 and 14, measured the same or up to
+  // 3 % slower.)
+  static constexpr int NS = D == 64 ? 8 : D == 128 ? 4 : 10;
   static constexpr int CTAS = D == 256 ? 1 : 2;
   static constexpr uint32_t TM_COLS = D == 256 ? 512 : 256;
   // Score buffers, O, and for D = 256 Q as the A operand in TMEM. (A product
   // with N = 64 and both operands in shared memory is bound by reading A, 48
-  // cycles against 32 measured; and at D = 256 Q, K and V together asked for
-  // 1.5 times the shared memory bandwidth that the products need with Q in
-  // TMEM. D = 128 has no columns left for it, D = 64 is bound by the softmax
-  // and takes a third score buffer instead.)
+  // cycles against 32 measured. D = 128 has no columns left for Q, D = 64 is
+  // bound by the softmax and takes a third score buffer instead.)
   static constexpr int NSB = D == 64 ? 3 : 2;
   static constexpr bool QT = D == 256;
   static constexpr uint32_t TM_O = NSB * kAttnKeys;
@@ -394,11 +407,10 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
         pages[NSB - 1] = after;
       }
     }
-    if (!ok) {  // gave up: let the copies in flight land
-      for (int i = 0; i < used; ++i) {
-        if (--slot < 0) slot = NS - 1, phase ^= 1;
-        mbar_wait(full + 8 * slot, phase);
-      }
+    // no copy outlives the CTA, whoever gave up
+    for (int i = 0; i < used; ++i) {
+      if (--slot < 0) slot = NS - 1, phase ^= 1;
+      mbar_wait(full + 8 * slot, phase);
     }
   } else if (warp == 5) {
     // ----------------------------------------------------------------- MMA

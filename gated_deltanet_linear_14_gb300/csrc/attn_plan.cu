@@ -444,10 +444,16 @@ cudaError_t launch_attn_plan(const AttnDims& A, const KvBatch& B, void* plan, in
 // A thread takes 16 elements of a (row, query head) pair, the lanes of a warp
 // neighbouring pairs of a tile, whose partial rows lie side by side: 32 of
 // them, or where there are few pairs (and so many pieces of each), 4 to 16
-// with the pieces dealt to groups of lanes. Blocks are D / 16 warps: first the pairs of the list's rows, head by head,
-// then one per CTA for the item that its part's end cuts. What a thread
-// reads of the plan it reads before the attention kernel ends (the plan was
-// complete when that kernel began), so only the pieces' own latency follows.
+// with the pieces dealt to groups of lanes. Blocks are D / 16 warps: first the
+// pairs of the list's rows, head by head, then one per CTA for the item that
+// its part's end cuts. What a thread reads of the plan it reads before the
+// attention kernel ends (the plan was complete when that kernel began), so
+// only the pieces' own latency follows.
+//
+// Bound by that latency: 11 us for 16384 pairs of three pieces, D = 128 (34 MB,
+// 5 us at the copy rate), 5 us for 32 pairs. (A warp per pair with its lanes
+// along D, rows of partial sums end to end: 14 us, and 34 us where 300 tiles
+// of 128 rows were cut.)
 
 constexpr int kJoinBatch = 4;
 
@@ -558,7 +564,8 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
       const float back = exp2f(top - ref), theirs = exp2f(other - ref);
       sum = sum * back + __shfl_xor_sync(~0u, sum, x) * theirs;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[e] = acc[e] * back + __shfl_xor_sync(~0u, acc[e], x) * theirs;
+      for (int e = 0; e < 16; ++e)
+        acc[e] = acc[e] * back + __shfl_xor_sync(~0u, acc[e], x) * theirs;
       top = nt;
     }
     if (!mine || lane >= pairs) continue;

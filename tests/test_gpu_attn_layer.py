@@ -486,3 +486,35 @@ def test_cache_past_32_bits():
     gdn.gdn_kv_append(c.dims, c.batch, None, None, k, v, None, c.k, c.v, c.status)
     assert torch.equal(c.k[pool - 1, :, 299 - 256], k[0])
     c.check(*c.attn())
+
+
+def test_step_replayed_from_a_graph():
+    """Plan, append and attention captured once: replays read the lengths, rows and cache as
+    they are then, and give the bits of plain calls."""
+    c = Cache([1, 8, 1, 2], [300, 60, 700, 90], 8, 2, 128, 64, seed=23,
+              groups=[(0, 4, 0)])
+    k, v = (torch.randn(c.T, 2, 128, generator=c.g, device="cuda").to(BF) for _ in range(2))
+    q_rot, o = torch.empty_like(c.q), torch.empty_like(c.q)
+    _, pos, freq, axis = rope_inputs(c.T, 128, 64, 1, 24, 1 << 16)
+    rope = gdn.make_rope(64, freq, pos, axis=axis)
+    c.plan()
+
+    def step():
+        gdn.gdn_attn_plan(c.dims, c.batch, c.plan_buf, c.plan_buf.numel(), c.status)
+        gdn.gdn_kv_append(c.dims, c.batch, rope, c.q, k, v, q_rot, c.k, c.v, c.status)
+        gdn.gdn_attn(c.dims, c.batch, c.plan_buf, q_rot, c.k, c.v, o, None, c.ws, c.ws.numel(),
+                     c.status)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for shift in (0, 3, 20):  # every request goes on: within its pages
+        c.keep[2].copy_(i32(np.minimum(c.kv + shift, -(-c.kv // 64) * 64)))
+        c.q.add_(0.25)
+        o.zero_()
+        graph.replay()
+        got = o.clone()
+        step()
+        assert torch.equal(got, o) and int(c.status.item()) == 0 and bool(o.any())
