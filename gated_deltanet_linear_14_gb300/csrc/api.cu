@@ -665,7 +665,8 @@ const char* gdn_strerror(int32_t s) {
     case GDN_DEV_BAD_PAGE: return "device: page index out of range";
     case GDN_DEV_BAD_ROWS: return "device: row range out of bounds";
     case GDN_DEV_BAD_ACCEPTED: return "device: accepted count outside the record width";
-    case GDN_DEV_STALE_STEP: return "device: page step parity does not match the request";
+    case GDN_DEV_STALE_STEP:
+      return "device: page step parity does not match the request (or a plan made for other dims or counts)";
     case GDN_DEV_TOO_MANY_CANDIDATES: return "device: more candidate rows than max_candidates";
     case GDN_DEV_RECORD_OPEN: return "device: plain rows on a page whose spec record is open";
     case GDN_DEV_BAD_FLAG: return "device: corrupt page flag word (or FRESH with SPEC)";

@@ -340,6 +340,12 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
     return bar_wait_long(bar, parity, words + 1, status);
   };
 
+  if (!P.good()) {
+    if (blockIdx.x == 0 && tid == 0) report(status, GDN_DEV_STALE_STEP);
+    __syncthreads();
+    if (warp == 5) tmem_dealloc(tmem, C::TM_COLS);
+    return;
+  }
   Walk W(P, A);
   if (warp == 4) {
     // ------------------------------------------------------------ producer
@@ -790,7 +796,7 @@ cudaError_t go(const void* tk, const void* tv, const AttnDims& A, const KvBatch&
                void* ws, int32_t* status, cudaStream_t s) {
   constexpr int bytes = Cfg<D>::BYTES;
   const AttnLayout L = attn_layout(A, B);
-  const AttnPlan P = attn_plan_view(L, plan);
+  const AttnPlan P = attn_plan_view(A, B, L, plan);
   cudaError_t e = ensure_smem_limit<attn_kernel<T, D>>(bytes);
   if (e != cudaSuccess) return e;
   e = launch_pdl(attn_kernel<T, D>, dim3(L.ctas), dim3(kAttnThreads), bytes, s,

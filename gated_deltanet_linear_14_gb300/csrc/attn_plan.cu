@@ -75,7 +75,8 @@ __device__ __forceinline__ T block_scan(T v, T& total, T* sm) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads)
-attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* status) {
+attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, AttnStamp stamp, char* plan,
+                 int32_t* status) {
   __shared__ unsigned long long scan64[32];
   __shared__ int scan32[32];
   // (a CTA's part of the line of cost, and what its units cost)
@@ -392,7 +393,8 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
   }
   const int Q = (n_items - own_first) * A.Hkv;
   for (int c = tid; c <= L.ctas; c += kPlanThreads) qfirst[c] = Q;
-  if (tid == 0) *head = AttnHead{n_items, own_first, min(list_rows, L.max_list), n_units};
+  if (tid == 0) *head = AttnHead{n_items, own_first, min(list_rows, L.max_list), n_units,
+                                {stamp.v[0], stamp.v[1]}};
   __syncthreads();
   // the first part that begins at x or after it
   auto lower = [&](unsigned long long x) {
@@ -432,8 +434,9 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, char* plan, int32_t* statu
 
 cudaError_t launch_attn_plan(const AttnDims& A, const KvBatch& B, void* plan, int32_t* status,
                              cudaStream_t s) {
-  return launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, A, B, attn_layout(A, B),
-                    (char*)plan, status);
+  const AttnLayout L = attn_layout(A, B);
+  return launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, A, B, L,
+                    plan_stamp(A, B, L.ctas), (char*)plan, status);
 }
 
 // ---------------------------------------------------------------- the join
@@ -468,8 +471,10 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
   AttnItem it{};
   AttnSpan s1{0, 0};
   int unit = 0, pieces = 0, stride = 0;
-  const bool cut = (int)blockIdx.x >= list_blocks;
-  if (cut) {
+  const bool cut = (int)blockIdx.x >= list_blocks, good = P.good();
+  if (!good) {
+    // another call's plan: the attention kernel has reported it
+  } else if (cut) {
     const int c = blockIdx.x - list_blocks;
     const int q = P.qfirst[c + 1];  // holds the start of CTA c + 1's part
     if (q < (P.head->items - P.head->own_first) * A.Hkv) {
@@ -581,7 +586,7 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
 cudaError_t launch_attn_join(const AttnDims& A, const KvBatch& B, int io, const void* plan,
                              const void* ws, void* o, float* lse, cudaStream_t s) {
   const AttnLayout L = attn_layout(A, B);
-  const AttnPlan P = attn_plan_view(L, plan);
+  const AttnPlan P = attn_plan_view(A, B, L, plan);
   const float* po = (const float*)ws;
   const float2* pml = (const float2*)((const char*)ws + L.ws_ml);
   // (eight pairs a warp where that still is no more than a few blocks an SM)

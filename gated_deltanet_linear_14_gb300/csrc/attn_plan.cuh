@@ -103,7 +103,24 @@ struct AttnJoin {
 struct AttnHead {
   int32_t items, own_first;  // the groups' items come first
   int32_t list_rows, units;
+  unsigned long long stamp[2];  // see plan_stamp
 };
+
+// What a plan was made for. A gdn_attn call with other dims or counts, or a
+// plan that was never written, must not be walked: its indexes would leave the
+// buffers.
+struct AttnStamp {
+  unsigned long long v[2];
+};
+inline AttnStamp plan_stamp(const AttnDims& A, const KvBatch& B, int ctas) {
+  const int x[] = {A.Hq,       A.Hkv,      A.D,         A.ps,         B.R,
+                   B.num_rows, B.max_rows, B.max_pages, B.num_groups, ctas};
+  AttnStamp s{{0x9E3779B97F4A7C15ull, 0xC2B2AE3D27D4EB4Full}};
+  for (int w : x)  // two mixes of every count
+    for (int i = 0; i < 2; ++i)
+      s.v[i] = (s.v[i] ^ (unsigned)w) * 0x100000001B3ull + (s.v[i] >> 29) + i;
+  return s;
+}
 
 // Group items are cut into up to this many pieces per CTA.
 constexpr int kRounds = 4;
@@ -130,6 +147,10 @@ struct AttnPlan {
   const AttnRow* list;
   const AttnJoin* joins;      // of list row * Hkv + head
   int ctas, max_list, unit_slots;
+  AttnStamp stamp;
+  __device__ __forceinline__ bool good() const {
+    return head->stamp[0] == stamp.v[0] && head->stamp[1] == stamp.v[1];
+  }
 };
 
 // Where a piece of an item keeps the partial o of its row m (own place in the
@@ -192,13 +213,14 @@ cudaError_t launch_attn(const void* tk, const void* tv, const AttnDims& A, const
                         int io, const void* plan, const void* q, long long qs, const void* vc,
                         void* o, float* lse, void* ws, int32_t* status, cudaStream_t s);
 
-inline AttnPlan attn_plan_view(const AttnLayout& L, const void* plan) {
+inline AttnPlan attn_plan_view(const AttnDims& A, const KvBatch& B, const AttnLayout& L,
+                               const void* plan) {
   const char* p = (const char*)plan;
   return AttnPlan{(const AttnHead*)p,           (const unsigned long long*)(p + L.begin),
                   (const int32_t*)(p + L.qfirst), (const AttnItem*)(p + L.items),
                   (const AttnSpan*)(p + L.spans), (const AttnUnit*)(p + L.units),
                   (const AttnRow*)(p + L.list),   (const AttnJoin*)(p + L.joins),
-                  L.ctas, L.max_list, L.unit_slots};
+                  L.ctas, L.max_list, L.unit_slots, plan_stamp(A, B, L.ctas)};
 }
 
 }  // namespace gdn

@@ -95,7 +95,8 @@ typedef enum {
   GDN_DEV_BAD_PAGE = 1,       /* page index outside [0, num_pages)           */
   GDN_DEV_BAD_ROWS = 2,       /* row range outside [0, num_rows) / > max_rows */
   GDN_DEV_BAD_ACCEPTED = 3,   /* accepted count outside [0, record width)    */
-  GDN_DEV_STALE_STEP = 4,     /* page parity differs from the request's bit  */
+  GDN_DEV_STALE_STEP = 4,     /* page parity differs from the request's bit;
+                                 gdn_attn: a plan for other dims or counts   */
   GDN_DEV_TOO_MANY_CANDIDATES = 5, /* spec row count above max_candidates   */
   GDN_DEV_RECORD_OPEN = 6,    /* plain rows on a page with an open record    */
   GDN_DEV_BAD_FLAG = 7,       /* corrupt flag word, or FRESH with SPEC       */
@@ -592,7 +593,8 @@ gdn_status gdn_attn_plan(const gdn_attn_dims* dims, const gdn_kv_batch* batch, v
  * D in {64, 128, 256}, page_size a power of two in [16, 256], bf16 or fp16,
  * Hq / Hkv <= 128. Rows of no request are not written. Device error:
  * GDN_DEV_BAD_PAGE (a page index out of range: the outputs of that request are
- * undefined, the others complete), GDN_DEV_TIMEOUT. */
+ * undefined, the others complete), GDN_DEV_STALE_STEP (the plan was not written
+ * for these dims and counts: nothing is written), GDN_DEV_TIMEOUT. */
 gdn_status gdn_attn(const gdn_attn_dims* dims, const gdn_kv_batch* batch, const void* plan,
                     const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
                     void* o, float* lse, void* workspace, size_t workspace_bytes,

@@ -391,6 +391,33 @@ def test_attn_on_another_stream():
     assert torch.equal(o, ref)
 
 
+def test_attn_refuses_a_plan_for_something_else():
+    """A plan that was never written, or for other dims or counts: reported, nothing written."""
+    c = Cache([1, 4], [100, 90], 8, 2, 128, 16, seed=25)
+    good, z = c.attn()
+
+    def run(dims, batch, plan, q):
+        o = torch.full_like(q, 7.0)
+        ws = torch.empty(gdn.gdn_attn_workspace_bytes(dims, batch), dtype=torch.uint8,
+                         device="cuda")
+        gdn.gdn_attn(dims, batch, plan, q, c.k, c.v, o, None, ws, ws.numel(), c.status)
+        code = int(c.status.item())
+        c.status.zero_()
+        return code, o
+
+    bad = gdn.CODES["GDN_DEV_STALE_STEP"]
+    for fill in (0, 255, 17):
+        code, o = run(c.dims, c.batch, torch.full_like(c.plan_buf, fill), c.q)
+        assert code == bad and bool((o == 7).all())
+    code, o = run(gdn.make_attn_dims(4, 2, 128, 16), c.batch, c.plan_buf, c.q[:, :4].contiguous())
+    assert code == bad and bool((o == 7).all())
+    one = gdn.make_kv_batch(1, c.T, 4, c.batch.num_pages, *c.keep)
+    code, o = run(c.dims, one, c.plan_buf, c.q)
+    assert code == bad and bool((o == 7).all())
+    code, o = run(c.dims, c.batch, c.plan_buf, c.q)
+    assert code == 0 and torch.equal(o, good)
+
+
 def test_attn_bad_requests_are_skipped():
     rows, kv = [1, 4, 1, 2], [100, 90, 33, 60]
     c = Cache(rows, kv, 8, 2, 128, 16, seed=14)
