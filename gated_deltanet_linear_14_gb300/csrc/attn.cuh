@@ -27,13 +27,17 @@ struct KvBatch {
   const int32_t* group_pages;
 };
 
+// Tokens of a request, at most: the index one tile of keys further on still
+// fits 32 bits.
+constexpr int kMaxTokens = 0x7FFFFFFF - 256;
+
 // Whether request r's row range and length are in bounds (a row range
 // inside the packed rows, its tokens inside the page table).
 __device__ __forceinline__ bool kv_request_ok(const KvBatch& B, int ps, int start, int len,
                                               int kv) {
   return start >= 0 && len >= 0 && len <= B.max_rows &&
          (long long)start + len <= (long long)B.num_rows && kv >= len &&
-         (long long)kv <= (long long)B.max_pages * ps;
+         (long long)kv <= (long long)B.max_pages * ps && kv <= kMaxTokens;
 }
 
 struct Rope {

@@ -108,7 +108,7 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, AttnStamp stamp, char* pla
     return kv_request_ok(B, A.ps, start, len, kv);
   };
   auto joins = [&](int r, int& start, int& len, int& kv) {
-    return valid(r, start, len, kv) && len > 0 && len * A.G <= kJoinRows;
+    return valid(r, start, len, kv) && len > 0 && len <= kJoinRows / A.G;
   };
 
   for (int r = tid; r < B.R; r += kPlanThreads) {
@@ -164,7 +164,10 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, AttnStamp stamp, char* pla
     const int off = list_rows + block_scan(n, total, scan32);
     if (g < NG) {
       g_off[g] = off;
-      if ((long long)off + n > L.max_list) g_rows[g] = g_shared[g] = 0;  // groups that overlap
+      if ((long long)off + n > L.max_list) {  // groups that overlap
+        g_rows[g] = g_shared[g] = 0;
+        report(status, GDN_DEV_BAD_ROWS);
+      }
     }
     list_rows += total;
   }
@@ -186,7 +189,8 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, AttnStamp stamp, char* pla
       const int pos = at + x - len;
       if (len > 0) {
         req_k0[r] = shared;
-        req_list[r] = off + pos;
+        // (a request of two groups would read both groups' keys)
+        if (atomicExch(&req_list[r], off + pos) >= 0) report(status, GDN_DEV_BAD_ROWS);
         for (int i = 0; i < len; ++i)
           list[off + pos + i] = AttnRow{start + i, r, g, i * A.G, (pos + i) * A.G, {0, 0, 0}};
       }

@@ -550,8 +550,8 @@ gdn_status gdn_rope(const gdn_attn_dims* dims, const gdn_rope_params* rope, int3
  * batch are not read: no page that is written may be shared.
  * D in {64, 128, 256}, page_size a power of two in [16, 256], io dtype bf16 or
  * fp16. Device errors, request skipped: GDN_DEV_BAD_ROWS (row range, kv_len <
- * row_len or kv_len > max_pages * page_size); GDN_DEV_BAD_PAGE: a row whose
- * page index is out of range is not written (its q_out is). */
+ * row_len, kv_len > max_pages * page_size or >= 2^31 - 256); GDN_DEV_BAD_PAGE:
+ * a row whose page index is out of range is not written (its q_out is). */
 gdn_status gdn_kv_append(const gdn_attn_dims* dims, const gdn_kv_batch* batch,
                          const gdn_rope_params* rope, const void* q, int64_t q_stride,
                          const void* k, int64_t k_stride, const void* v, int64_t v_stride,
@@ -568,7 +568,9 @@ size_t gdn_attn_workspace_bytes(const gdn_attn_dims* dims, const gdn_kv_batch* b
  * aligned, at least gdn_attn_plan_bytes). The plan holds for every gdn_attn
  * call with these dims, counts and lengths, e.g. for all attention layers of
  * the step; it does not hold page indexes, rows or cache contents. One launch
- * on `stream`. Device error, request skipped: GDN_DEV_BAD_ROWS. */
+ * on `stream`. Device error: GDN_DEV_BAD_ROWS (as for gdn_kv_append, request
+ * skipped; or a request in two groups that both share: its results are
+ * undefined). */
 gdn_status gdn_attn_plan(const gdn_attn_dims* dims, const gdn_kv_batch* batch, void* plan,
                          size_t plan_bytes, int32_t* status, gdn_stream_t stream);
 

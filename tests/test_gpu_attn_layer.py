@@ -435,6 +435,38 @@ def test_attn_bad_requests_are_skipped():
     c.check(o, z, requests=[0, 1, 2])
 
 
+def test_attn_refuses_lengths_that_end_past_32_bits():
+    """A tile of keys past the last token must not wrap around: such a request is skipped."""
+    c = Cache([1, 1], [200, 64], 1, 1, 64, 256, seed=26)
+    width = (1 << 31) // 256
+    table = torch.zeros(2, width, dtype=torch.int32, device="cuda")
+    table[1, 0] = int(c.table[1, 0])
+    c.keep[3] = table
+    c.keep[2][0] = (1 << 31) - 200
+    c.batch = gdn.make_kv_batch(2, 2, 1, c.batch.num_pages, *c.keep)
+    o, z = c.attn()
+    assert int(c.status.item()) == gdn.CODES["GDN_DEV_BAD_ROWS"]
+    c.status.zero_()
+    c.check(o, z, requests=[1])
+    assert bool((o[0] == 7).all())
+    k0 = c.k.clone()
+    k = torch.zeros(2, 1, 64, device="cuda", dtype=BF)
+    gdn.gdn_kv_append(c.dims, c.batch, None, None, k, k, None, c.k, c.v, c.status)
+    assert int(c.status.item()) == gdn.CODES["GDN_DEV_BAD_ROWS"]
+    k0[int(c.table[1, 0]), :, 63] = 0
+    assert torch.equal(c.k, k0)
+
+
+@pytest.mark.parametrize("second", [20, 33])
+def test_attn_reports_a_request_of_two_groups(second):
+    c = Cache([1] * 64, [2600] * 64, 16, 8, 128, 64, seed=27, groups=[(0, 64, 40)])
+    c.check(*c.attn())
+    gr = [i32(v) for v in ([0, 31], [32, second], [40, 40])]
+    c.batch = gdn.make_kv_batch(64, 64, 1, c.batch.num_pages, *c.keep[:4], *gr)
+    c.plan()
+    assert int(c.status.item()) == gdn.CODES["GDN_DEV_BAD_ROWS"]
+
+
 @pytest.mark.parametrize("Hq,Hkv,D,ps,rd,axes,dt,interleaved", [
     (8, 2, 128, 16, 128, 1, BF, False), (16, 2, 256, 64, 64, 3, BF, False),
     (4, 4, 64, 256, 32, 1, HF, True), (3, 1, 64, 32, 6, 3, HF, False)])
