@@ -345,17 +345,19 @@ def _rows(t):
 
 def gdn_rope(dims, rope, q, q_out, k=None, k_out=None, inverse=False, stream=None):
     rows = (q if q is not None else k).shape[0]
-    _check(load_library().gdn_rope(ctypes.byref(dims), ctypes.byref(rope), rows, *_rows(q),
-                                   *_rows(q_out), *_rows(k), *_rows(k_out), int(inverse),
-                                   _stream(stream)), "gdn_rope")
+    # (a structure passed where a pointer is declared goes by reference)
+    code = (_lib or load_library()).gdn_rope(dims, rope, rows, *_rows(q), *_rows(q_out), *_rows(k),
+                                             *_rows(k_out), int(inverse), _stream(stream))
+    if code:
+        raise GdnError(code, "gdn_rope")
 
 
 def gdn_kv_append(dims, batch, rope, q, k, v, q_out, k_cache, v_cache, status, stream=None):
-    _check(load_library().gdn_kv_append(ctypes.byref(dims), ctypes.byref(batch),
-                                        None if rope is None else ctypes.byref(rope), *_rows(q),
-                                        *_rows(k), *_rows(v), *_rows(q_out), _ptr(k_cache),
-                                        _ptr(v_cache), _ptr(status), _stream(stream)),
-           "gdn_kv_append")
+    code = (_lib or load_library()).gdn_kv_append(dims, batch, rope, *_rows(q), *_rows(k),
+                                                  *_rows(v), *_rows(q_out), _ptr(k_cache),
+                                                  _ptr(v_cache), _ptr(status), _stream(stream))
+    if code:
+        raise GdnError(code, "gdn_kv_append")
 
 
 def gdn_attn_plan_bytes(dims, batch) -> int:
@@ -374,11 +376,11 @@ def gdn_attn_plan(dims, batch, plan, plan_bytes, status, stream=None):
 
 def gdn_attn(dims, batch, plan, q, k_cache, v_cache, o, lse, workspace, workspace_bytes, status,
              stream=None):
-    q_ptr, q_stride = _rows(q)
-    _check(load_library().gdn_attn(ctypes.byref(dims), ctypes.byref(batch), _ptr(plan), q_ptr,
-                                   q_stride, _ptr(k_cache), _ptr(v_cache), _ptr(o), _ptr(lse),
-                                   _ptr(workspace), int(workspace_bytes), _ptr(status),
-                                   _stream(stream)), "gdn_attn")
+    code = (_lib or load_library()).gdn_attn(dims, batch, _ptr(plan), *_rows(q), _ptr(k_cache),
+                                             _ptr(v_cache), _ptr(o), _ptr(lse), _ptr(workspace),
+                                             int(workspace_bytes), _ptr(status), _stream(stream))
+    if code:
+        raise GdnError(code, "gdn_attn")
 
 
 def gdn_check_bounded_wait(limit_ns, status, stream=None):
