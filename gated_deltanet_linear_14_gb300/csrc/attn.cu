@@ -241,22 +241,34 @@ struct Walk {
   AttnItem it;
   AttnSpan span;
   int head, unit, t0, t1;
+  bool ready;
 
   __device__ __forceinline__ Walk(const AttnPlan& P_, const AttnDims& A)
-      : P(&P_), Hkv(A.Hkv), c(blockIdx.x), next_unit(blockIdx.x), span{0, 0}, unit(0) {
+      : P(&P_), Hkv(A.Hkv), c(blockIdx.x) {
     const AttnHead h = *P->head;
-    a = P->begin[c], b = P->begin[c + 1];
-    q = uniform(P->qfirst[c]);  // the item that holds the part's start
+    const AttnStart s = P->start[c];
+    it = s.it, span = s.span, a = s.a, b = s.b;
+    head = uniform(s.head), unit = s.unit;
+    t0 = uniform(s.t0), t1 = uniform(s.t1);
+    ready = uniform(s.ready);
+    const bool is_unit = uniform(s.is_unit);
+    next_unit = is_unit ? c + P->ctas : c;
     units = uniform(h.units);
     Q = uniform((h.items - h.own_first) * Hkv);
-    q_item = uniform(h.own_first) + q / Hkv;
-    q_head = q - q / Hkv * Hkv - 1;
-    --q;
+    // (the item before the next one to look up)
+    const int qf = uniform(s.q), back = ready && !is_unit ? 0 : 1;
+    q = qf - back;
+    q_item = uniform(h.own_first) + qf / Hkv;
+    q_head = qf - qf / Hkv * Hkv - back;
   }
   // The next piece with tiles; `empty` is called for those without (a part's
   // end can fall so close to an item's that no tile is left).
   template <class F>
   __device__ __forceinline__ bool next(F empty) {
+    if (ready) {
+      ready = false;
+      return true;
+    }
     if (next_unit < units) {
       const AttnUnit u = P->units[next_unit];
       unit = next_unit;
@@ -344,13 +356,13 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
     return bar_wait_long(bar, parity, words + 1, status);
   };
 
+  Walk W(P, A);
   if (!P.good()) {
     if (blockIdx.x == 0 && tid == 0) report(status, GDN_DEV_STALE_STEP);
     __syncthreads();
     if (warp == 5) tmem_dealloc(tmem, C::TM_COLS);
     return;
   }
-  Walk W(P, A);
   if (warp == 4) {
     // ------------------------------------------------------------ producer
     const int br = min(A.ps, kAttnKeys), boxes = kAttnKeys / br;

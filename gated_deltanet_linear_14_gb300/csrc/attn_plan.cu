@@ -24,7 +24,7 @@ AttnLayout attn_layout(const AttnDims& A, const KvBatch& B) {
   const long long whole = ((long long)L.max_list * A.G / kAttnM + B.num_groups + 1) * A.Hkv;
   L.max_units = B.num_groups ? (int)(whole > L.unit_slots ? whole : L.unit_slots) : 0;
   size_t at = up(sizeof(AttnHead));
-  L.begin = at, at = up(at + 8 * ((size_t)L.ctas + 1));
+  L.start = at, at = up(at + sizeof(AttnStart) * 2 * (size_t)device_sms());
   L.qfirst = at, at = up(at + 4 * ((size_t)L.ctas + 1));
   L.items = at, at = up(at + sizeof(AttnItem) * (size_t)L.max_items);
   L.spans = at, at = up(at + sizeof(AttnSpan) * (size_t)L.max_items * A.Hkv);
@@ -88,7 +88,7 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, AttnStamp stamp, char* pla
   pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, NG = B.num_groups;
   AttnHead* head = (AttnHead*)plan;
-  unsigned long long* begin = (unsigned long long*)(plan + L.begin);
+  AttnStart* start_of = (AttnStart*)(plan + L.start);
   int32_t* qfirst = (int32_t*)(plan + L.qfirst);
   AttnItem* items = (AttnItem*)(plan + L.items);
   AttnSpan* spans = (AttnSpan*)(plan + L.spans);
@@ -392,8 +392,8 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, AttnStamp stamp, char* pla
         tid < L.ctas && share >= used + least ? share - used : 0;
     unsigned long long total;
     const unsigned long long off = block_scan(n, total, scan64);
-    if (tid < L.ctas) begin[tid] = begin_s[tid] = off;
-    if (tid == 0) begin[L.ctas] = begin_s[L.ctas] = total;
+    if (tid < L.ctas) begin_s[tid] = off;
+    if (tid == 0) begin_s[L.ctas] = total;
   }
   const int Q = (n_items - own_first) * A.Hkv;
   for (int c = tid; c <= L.ctas; c += kPlanThreads) qfirst[c] = Q;
@@ -421,6 +421,28 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, AttnStamp stamp, char* pla
     for (int c = first; c < end; ++c) qfirst[c] = q;
   }
   __syncthreads();
+  if (tid < L.ctas) {
+    AttnStart st{};
+    st.a = begin_s[tid], st.b = begin_s[tid + 1];
+    st.q = qfirst[tid];
+    if (tid < n_units) {
+      const AttnUnit u = units[tid];
+      st.it = items[u.item];
+      st.head = u.head, st.unit = tid, st.t0 = u.t0, st.t1 = u.t1;
+      st.ready = st.is_unit = 1;
+    } else if (st.q < Q) {
+      const int i = st.q / A.Hkv;
+      st.it = items[own_first + i];
+      st.head = st.q - i * A.Hkv;
+      st.span = spans[st.q];
+      if (st.span.c0 <= tid) {
+        piece_tiles(st.it, st.it.off + (unsigned long long)st.head * st.it.cost, st.a, st.b,
+                    st.span, tid, st.t0, st.t1);
+        st.ready = st.t0 < st.t1;
+      }
+    }
+    start_of[tid] = st;
+  }
   const int joins_n = min(list_rows, L.max_list) * A.Hkv;
   for (int x = tid; x < joins_n; x += kPlanThreads) {
     const int i = x / A.Hkv, h = x - i * A.Hkv;
