@@ -29,9 +29,11 @@
 //   long prompts: the tensor cores and the shared memory that feeds them (per
 //     64 keys and CTA 640 MMA cycles and 96 KB through shared memory, two CTAs
 //     an SM), and power in a row of calls. 4 x 1500..2048 rows over 8192 + ..
-//     keys, D = 128: 835 us, 1.38 PFLOP/s, 0.73 of the burst matrix product;
+//     keys, D = 128: 840 us, 1.37 PFLOP/s, 0.72 of the burst matrix product;
 //   many short items: an item's start and end, 2 to 4 us, and its fetch from
-//     the L2. 64 requests of 8 rows in four groups: 61 us for 193 MB.
+//     the L2. 64 requests of 8 rows in four groups: 60 us for 193 MB;
+//   D = 64: the softmax, 376 instructions a tile and warp at 59 % issue. 96
+//     requests of 32/4 heads behind 49152 keys: 56 us.
 // Tiles of 128 keys with one score buffer took 1.3 times longer on prompts;
 // two tiles that share K and V on one CTA per SM gained 3 % on the longest
 // prompts and lost 10 to 30 % on the others.
