@@ -41,66 +41,17 @@ __device__ __forceinline__ float2 cos_sin(int pos, float f) {
   return cs;
 }
 
-// One thread's unit u of a head: 2 VEC elements, as two accesses of VEC. The
-// first rd / (2 VEC) units hold VEC pairs each (half pairing: elements VEC u
-// and rd/2 + VEC u on; interleaved: 2 VEC u on), the others pass through.
+// `rows` rows from packed row `row0` on, by one block; append: tokens kv0 and on
+// of the request whose page table is `table`. One thread's unit u of a head: 2 VEC
+// elements, as two accesses of VEC. The first rd / (2 VEC) units hold VEC pairs
+// each (half pairing: elements VEC u and rd/2 + VEC u on; interleaved: 2 VEC u
+// on), the others pass through.
 template <class T, int VEC, bool INTER, bool APPEND>
-__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
-rope_kernel(RopeCall C, Rope P, AttnDims A, KvBatch B, int U, int TY, int RB, int packed,
-            int32_t* status) {
-  extern __shared__ float2 cs_tab[];  // [RB][rd / 2]
-  pdl_begin();
+__device__ __forceinline__ void turn_rows(const RopeCall& C, const Rope& P, const AttnDims& A,
+                                          const KvBatch& B, int U, int TY, long long row0,
+                                          int rows, int kv0, const int32_t* table, float2* cs_tab,
+                                          int32_t* status) {
   const int half = P.rd >> 1, tid = threadIdx.x;
-  long long row0 = (long long)blockIdx.x * RB;
-  int rows = 0, kv0 = 0;
-  const int32_t* table = nullptr;
-  if (APPEND) {
-    int r = blockIdx.y;
-    if (packed) {
-      // the request that holds this block among all requests' blocks of RB rows
-      __shared__ int found[2], sums[kRopeThreads / 32];
-      const int lane = tid & 31, w = tid >> 5, bx = blockIdx.x;
-      if (tid == 0) found[0] = -1;
-      int at = 0;
-      for (int r0 = 0; r0 < B.R && at <= bx; r0 += kRopeThreads) {
-        const int len = r0 + tid < B.R ? B.row_len[r0 + tid] : 0;
-        // (a length out of bounds has one block, which reports it)
-        const int n = len < 0 || len > B.max_rows ? 1 : (len + RB - 1) / RB;
-        int x = n;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int y = __shfl_up_sync(~0u, x, d);
-          if (lane >= d) x += y;
-        }
-        if (lane == 31) sums[w] = x;
-        __syncthreads();
-        int before = at, all = 0;
-        for (int k = 0; k < kRopeThreads / 32; ++k) {
-          if (k < w) before += sums[k];
-          all += sums[k];
-        }
-        const int first = before + x - n;
-        if (first <= bx && bx < first + n) found[0] = r0 + tid, found[1] = bx - first;
-        at += all;
-        __syncthreads();
-      }
-      if (found[0] < 0) return;
-      r = found[0];
-      row0 = (long long)found[1] * RB;
-    }
-    const int start = B.row_start[r], len = B.row_len[r], kv = B.kv_len[r];
-    if (!kv_request_ok(B, A.ps, start, len, kv)) {
-      if (row0 == 0 && tid == 0) report(status, GDN_DEV_BAD_ROWS);
-      return;
-    }
-    if (row0 >= len) return;
-    rows = min(RB, len - (int)row0);
-    kv0 = kv - len + (int)row0;
-    table = B.table + (size_t)r * B.max_pages;
-    row0 += start;
-  } else {
-    rows = (int)min((long long)RB, C.num_rows - row0);
-  }
   const int D = C.D, Hk = C.Hq + C.Hkv, H = Hk + (APPEND ? C.Hkv : 0);
   const int n_rot = P.rd / (2 * VEC), total = rows * TY * U;
 
@@ -203,6 +154,85 @@ rope_kernel(RopeCall C, Rope P, AttnDims A, KvBatch B, int U, int TY, int RB, in
   }
 }
 
+// Among all requests' blocks of RB rows, a CTA has the one at its own index, then
+// (`turn`) those that lie a grid's length further on: the request that holds it (-1:
+// past the last one), which of its blocks that is, and whether there is a next
+// one. A request that is out of bounds has one block, which reports it, whatever
+// its length says. A thread counts the requests of its part of the map.
+struct Found {
+  int req, block, more;
+};
+__device__ __forceinline__ void find_request(const AttnDims& A, const KvBatch& B, int RB,
+                                             int turn, Found* found) {
+  __shared__ long long sums[kRopeThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int each = (B.R + kRopeThreads - 1) / kRopeThreads;
+  const long long place = blockIdx.x + (long long)turn * gridDim.x;
+  auto blocks = [&](int x) {
+    if (x >= B.R) return 0;
+    const int start = B.row_start[x], len = B.row_len[x], kv = B.kv_len[x];
+    // (D and with it RB are powers of two here)
+    return kv_request_ok(B, A.ps, start, len, kv) ? (len + RB - 1) >> (31 - __clz(RB)) : 1;
+  };
+  long long n = 0;
+#pragma unroll 1
+  for (int i = 0; i < each; ++i) n += blocks(tid * each + i);
+  long long first = n;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long y = __shfl_up_sync(~0u, first, d);
+    if (lane >= d) first += y;
+  }
+  if (turn) __syncthreads();  // (the CTA is done with the turn before)
+  if (lane == 31) sums[w] = first;
+  if (tid == 0) found->req = -1;
+  __syncthreads();
+  first -= n;
+  long long all = 0;
+  for (int k = 0; k < kRopeThreads / 32; ++k) {
+    if (k < w) first += sums[k];
+    all += sums[k];
+  }
+  if (first <= place && place < first + n) {
+    int x = tid * each;
+    for (int i = 1, m; i < each && first + (m = blocks(x)) <= place; ++i, ++x) first += m;
+    *found = Found{x, (int)(place - first), place + gridDim.x < all};
+  }
+  __syncthreads();
+}
+
+template <class T, int VEC, bool INTER, bool APPEND>
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
+rope_kernel(RopeCall C, Rope P, AttnDims A, KvBatch B, int U, int TY, int RB, int packed,
+            int32_t* status) {
+  extern __shared__ float2 cs_tab[];  // [RB][rd / 2]
+  pdl_begin();
+  if constexpr (!APPEND) {
+    const long long row0 = (long long)blockIdx.x * RB;
+    turn_rows<T, VEC, INTER, false>(C, P, A, B, U, TY, row0,
+                                    (int)min((long long)RB, C.num_rows - row0), 0, nullptr, cs_tab,
+                                    status);
+  } else {
+    __shared__ Found found;
+    // (packed: one place a block, unless rows belong to several requests)
+    for (int turn = 0;; ++turn) {
+      if (packed) find_request(A, B, RB, turn, &found);
+      const int r = packed ? found.req : blockIdx.y, block = packed ? found.block : blockIdx.x;
+      if (r < 0) return;
+      const int start = B.row_start[r], len = B.row_len[r], kv = B.kv_len[r];
+      const long long at = (long long)block * RB;
+      if (!kv_request_ok(B, A.ps, start, len, kv)) {
+        if (block == 0 && threadIdx.x == 0) report(status, GDN_DEV_BAD_ROWS);
+      } else if (at < len) {
+        turn_rows<T, VEC, INTER, true>(C, P, A, B, U, TY, start + at, (int)min((long long)RB, len - at),
+                                       kv - len + (int)at, B.table + (size_t)r * B.max_pages,
+                                       cs_tab, status);
+      }
+      if (!packed || !found.more) return;
+    }
+  }
+}
+
 namespace {
 
 template <class T, int VEC, bool APPEND>
@@ -224,7 +254,8 @@ cudaError_t go(const RopeCall& C, const Rope& P, const AttnDims& A, const KvBatc
   if (APPEND) {
     // a block per request and RB rows of the longest; where most of those
     // would be empty (a few prompts among short requests), every block looks
-    // its request up instead, about a microsecond each
+    // its request up instead, about a microsecond each. (`all` is enough where no
+    // two requests share rows; where they do, blocks take several turns.)
     const long long each = (B.max_rows + RB - 1) / RB, all = (long long)B.num_rows / RB + B.R;
     packed = each * B.R > 2 * all && B.R <= 4096;
     grid = packed ? dim3((unsigned)all) : dim3((unsigned)each, B.R);

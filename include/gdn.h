@@ -547,7 +547,9 @@ gdn_status gdn_rope(const gdn_attn_dims* dims, const gdn_rope_params* rope, int3
  * kv_len[r] - row_len[r] + t; k is rotated as by gdn_rope and v copied. With q
  * (else NULL, as q_out) the query rows are rotated to q_out in the same
  * launch. rope NULL: nothing is rotated (q must be NULL). The groups of the
- * batch are not read: no page that is written may be shared.
+ * batch are not read: no page that is written may be shared. Rows may belong to
+ * several requests, each of which gets them in its own pages (q_out may then
+ * not be q).
  * D in {64, 128, 256}, page_size a power of two in [16, 256], io dtype bf16 or
  * fp16. Device errors, request skipped: GDN_DEV_BAD_ROWS (row range, kv_len <
  * row_len, kv_len > max_pages * page_size or >= 2^31 - 256); GDN_DEV_BAD_PAGE:
