@@ -12,6 +12,8 @@
 // TB/s, 0.98 of the copy rate; 8192 rows of 40 heads x 128, fp32: 52 us, 0.96;
 // 30 k rows of 32 heads x 80, three axes: 53 us, 0.91. (One row a block with
 // its loads behind the cosines, 106 registers: 297, 53 and 233 us.)
+#include <algorithm>
+
 #include "attn.cuh"
 #include "kernels.h"
 
@@ -172,7 +174,7 @@ __device__ __forceinline__ void find_request(const AttnDims& A, const KvBatch& B
     if (x >= B.R) return 0;
     const int start = B.row_start[x], len = B.row_len[x], kv = B.kv_len[x];
     // (D and with it RB are powers of two here)
-    return kv_request_ok(B, A.ps, start, len, kv) ? (len + RB - 1) >> (31 - __clz(RB)) : 1;
+    return kv_request_ok(B, A.ps, start, len, kv) ? (int)(((unsigned)len + RB - 1) >> (31 - __clz(RB))) : 1;
   };
   long long n = 0;
 #pragma unroll 1
@@ -256,11 +258,14 @@ cudaError_t go(const RopeCall& C, const Rope& P, const AttnDims& A, const KvBatc
     // would be empty (a few prompts among short requests), every block looks
     // its request up instead, about a microsecond each. (`all` is enough where no
     // two requests share rows; where they do, blocks take several turns.)
-    const long long each = (B.max_rows + RB - 1) / RB, all = (long long)B.num_rows / RB + B.R;
+    // (sums in 64 bits: max_rows may be any bound, of which no request in bounds
+    // has more than num_rows)
+    const long long each = ((long long)std::min(B.max_rows, B.num_rows) + RB - 1) / RB;
+    const long long all = std::min((long long)B.num_rows / RB + B.R, 0x7FFFFFFFLL);
     packed = each * B.R > 2 * all && B.R <= 4096;
     grid = packed ? dim3((unsigned)all) : dim3((unsigned)each, B.R);
   } else {
-    grid = dim3((C.num_rows + RB - 1) / RB);
+    grid = dim3((unsigned)(((long long)C.num_rows + RB - 1) / RB));
   }
   if (C.interleaved)
     return launch_pdl(rope_kernel<T, VEC, true, APPEND>, grid, dim3(kRopeThreads), smem, s, C, P,

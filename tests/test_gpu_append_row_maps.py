@@ -111,3 +111,12 @@ def test_many_requests(R):
         kv[r] = -1
     good = [r for r in good if r not in bad]
     assert append(start, rows, kv, int(rows.sum()), 400, good, Hkv=2, Hq=4, width=7) == BAD_ROWS
+
+
+@pytest.mark.parametrize("R", [3, 40])
+def test_a_bound_on_the_rows_at_the_end_of_32_bits(R):
+    """max_rows is an upper bound: any is allowed."""
+    start, rows, kv = packed([17] + [1] * (R - 1))
+    for top in ((1 << 31) - 1, (1 << 31) - 8, 17):
+        assert append(start, rows, kv, int(rows.sum()), top, range(R), Hq=1, Hkv=1, D=64, width=2,
+                      with_q=False) == 0
