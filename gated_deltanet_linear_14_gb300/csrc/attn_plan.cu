@@ -107,19 +107,41 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, AttnStamp stamp, char* pla
     start = B.row_start[r], len = B.row_len[r], kv = B.kv_len[r];
     return kv_request_ok(B, A.ps, start, len, kv);
   };
-  auto joins = [&](int r, int& start, int& len, int& kv) {
-    return valid(r, start, len, kv) && len > 0 && len <= kJoinRows / A.G;
-  };
 
+  unsigned long long rows_here = 0, rows_all;
   for (int r = tid; r < B.R; r += kPlanThreads) {
     int start, len, kv;
-    if (!valid(r, start, len, kv)) report(status, GDN_DEV_BAD_ROWS);
+    if (valid(r, start, len, kv)) rows_here += len;
+    else report(status, GDN_DEV_BAD_ROWS);
     req_k0[r] = 0;
     req_list[r] = -1;
   }
   for (int i = tid; i < L.max_list; i += kPlanThreads) list[i].row = -1;
   if (tid == 0) saved_s = 0, longest_s = 0;
-  __syncthreads();
+  block_scan(rows_here, rows_all, scan64);
+  // More rows than there are: some belong to several requests. Those requests are
+  // left out (k0 = -1), so that the others' items fit the plan's bounds.
+  const bool clash = rows_all > (unsigned long long)B.num_rows;
+  if (clash) {
+    for (int r = tid; r < B.R; r += kPlanThreads) {
+      int start, len, kv, start2, len2, kv2;
+      if (!valid(r, start, len, kv) || len == 0) continue;
+      for (int x = 0; x < B.R; ++x) {
+        if (x == r || !valid(x, start2, len2, kv2) || len2 == 0) continue;
+        if (start2 >= start + len || start >= start2 + len2) continue;
+        req_k0[r] = -1;
+        report(status, GDN_DEV_BAD_ROWS);
+        break;
+      }
+    }
+    __syncthreads();
+  }
+  auto taken = [&](int r, int& start, int& len, int& kv) {
+    return valid(r, start, len, kv) && !(clash && req_k0[r] < 0);
+  };
+  auto joins = [&](int r, int& start, int& len, int& kv) {
+    return taken(r, start, len, kv) && len > 0 && len <= kJoinRows / A.G;
+  };
   // groups: the keys that every joining member's rows all see, in whole pages
   for (int g = warp; g < NG; g += kPlanThreads / 32) {
     const int a = B.group_start[g], n = B.group_len[g];
@@ -207,18 +229,13 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, AttnStamp stamp, char* pla
       pairs = (long long)g_rows[e] * A.G;
     } else if (e < L.ents) {
       int start, len, kv;
-      if (valid(e - NG, start, len, kv)) pairs = (long long)len * A.G;
+      if (taken(e - NG, start, len, kv)) pairs = (long long)len * A.G;
     }
     const int n = (int)((pairs + kAttnM - 1) / kAttnM);
     int total;
     const int off = n_items + block_scan(n, total, scan32);
-    if (e < L.ents) first_item[e] = min(off, L.max_items);
-    n_items += total;
-  }
-  // more items than the row counts allow: rows that belong to several requests
-  if (n_items > L.max_items) {
-    if (tid == 0) report(status, GDN_DEV_BAD_ROWS);
-    n_items = L.max_items;
+    if (e < L.ents) first_item[e] = off;
+    n_items += total;  // (at most max_items: the rows of all requests are at most num_rows)
   }
   if (tid == 0) first_item[L.ents] = n_items;
   __syncthreads();

@@ -509,7 +509,8 @@ typedef struct {
  * same for the requests group_start[g] .. + group_len[g] - 1. Results do not
  * depend on the groups (up to the order of additions); keys that are declared
  * shared are read once for the group instead of once per request. Groups do
- * not overlap. (Requests with more than 64 (row, query head) pairs per
+ * not overlap. The rows of a request are its own, but for gdn_kv_append.
+ * (Requests with more than 64 (row, query head) pairs per
  * key/value head read the shared keys by themselves, as do all where sharing
  * would save too little to repay the joining of the parts.) */
 typedef struct {
@@ -572,7 +573,10 @@ size_t gdn_attn_workspace_bytes(const gdn_attn_dims* dims, const gdn_kv_batch* b
  * the step; it does not hold page indexes, rows or cache contents. One launch
  * on `stream`. Device error: GDN_DEV_BAD_ROWS (as for gdn_kv_append, request
  * skipped; or a request in two groups that both share: its results are
- * undefined). */
+ * undefined; or the valid requests have more rows than num_rows: those that
+ * share rows with another are skipped, the others complete. Rows of several
+ * requests that do not add up to more are not looked for; they get one of the
+ * requests' results, or a mixture). */
 gdn_status gdn_attn_plan(const gdn_attn_dims* dims, const gdn_kv_batch* batch, void* plan,
                          size_t plan_bytes, int32_t* status, gdn_stream_t stream);
 
