@@ -344,12 +344,20 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
     words[1] = words[2] = words[3] = words[4] = 0;
     mbar_fence_init();
   }
-  if (warp == 5) tmem_alloc(smem_u32((const void*)words), C::TM_COLS);
+  // (tensor memory only after the previous grid, which may need all of it; what
+  // the walk begins with is on its way to the L1 meanwhile)
+  pdl_begin();
+  if (warp == 5) {
+    tmem_alloc(smem_u32((const void*)words), C::TM_COLS);
+  } else if (warp == 4) {
+    touch(reinterpret_cast<const char*>(P.start + blockIdx.x) + 4 * lane);
+    touch(P.head);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = words[0];
-  pdl_begin();
+  Walk W(P, A);
 
   // All lanes of a warp wait, and go on together. A wait that gives up ends
   // its role; words[1] then ends the others.
@@ -358,7 +366,6 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
     return bar_wait_long(bar, parity, words + 1, status);
   };
 
-  Walk W(P, A);
   if (!P.good()) {
     if (blockIdx.x == 0 && tid == 0) report(status, GDN_DEV_STALE_STEP);
     __syncthreads();

@@ -550,10 +550,8 @@ attn_join_kernel(AttnDims A, AttnPlan P, const float* __restrict__ po,
       m2 = (lr.group_m + hg) % kAttnM;
     }
   }
-  // (the first block always waits: the grid must not end before the attention
-  // kernel has)
   if (blockIdx.x != 0 && !__any_sync(~0u, m1 < m_end)) return;
-  pdl_begin();
+  pdl_wait_only();
   const int n1 = s1.c1 - s1.c0 + 1, n = n1 + pieces;
   auto part = [&](int p) {
     if (p < n1)

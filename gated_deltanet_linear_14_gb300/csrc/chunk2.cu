@@ -78,15 +78,12 @@ __device__ __forceinline__ void bulk_store_commit_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
-// Wait for the previous grid without letting the next one start early: the
-// chain that follows holds a whole SM per CTA, and started early it would
-// take SMs from this grid's later waves.
-__device__ __forceinline__ void pdl_wait_only() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 __global__ void __launch_bounds__(kChunkThreads, 2)
 chunk_prep_kernel(const __grid_constant__ CUtensorMap tm_qkv, Geom G, Batch B, Params P,
                   const bf16* __restrict__ a_in, const bf16* __restrict__ b_in, char* ws,
                   int ws_chunks, int32_t* status) {
+  // (the chain that follows holds a whole SM per CTA, and started early it would
+  // take SMs from this grid's later waves)
   pdl_wait_only();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);

@@ -394,10 +394,20 @@ __device__ __forceinline__ void gate_log_c(int gate_mode, float eA, float dtb, f
 // the next grid be scheduled. Launched with launch_pdl, a kernel's blocks can
 // be resident while the previous grid finishes, which hides the launch
 // latency between back-to-back kernels.
+//
+// What a kernel holds before it waits must not be what the previous grid still
+// has to get: that grid may have let this one start before it allocated its
+// tensor memory, and an allocation waits without a bound. So tensor memory is
+// allocated after the wait, in every kernel. (attn_join_kernel reads its plan
+// before it waits and lets blocks without work go without; attn_plan.cu says
+// why it may.)
 __device__ __forceinline__ void pdl_begin() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+
+// Wait for the previous grid without letting the next one start early.
+__device__ __forceinline__ void pdl_wait_only() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <class... KArgs, class... Args>
 inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
