@@ -492,7 +492,8 @@ typedef struct {
 
 /* Rotary positions: pair j of a head's first rotary_dim elements turns by the
  * angle positions[axis[j]][row] * inv_freq[j]. The angle is formed and reduced
- * to a turn with 48 bits, so far positions lose nothing against near ones. */
+ * to a turn before it is rounded to fp32 (within 2^-25 of a turn for |inv_freq|
+ * <= 1), so far positions, up to int32's ends, lose nothing against near ones. */
 typedef struct {
   int32_t rotary_dim;        /* even, <= head_dim; the other elements pass through */
   int32_t num_axes;          /* position axes: 1 for text, 3 for (time, height, width) */
@@ -509,10 +510,10 @@ typedef struct {
  * same for the requests group_start[g] .. + group_len[g] - 1. Results do not
  * depend on the groups (up to the order of additions); keys that are declared
  * shared are read once for the group instead of once per request. Groups do
- * not overlap. The rows of a request are its own, but for gdn_kv_append.
- * (Requests with more than 64 (row, query head) pairs per
+ * not overlap. (Requests with more than 64 (row, query head) pairs per
  * key/value head read the shared keys by themselves, as do all where sharing
- * would save too little to repay the joining of the parts.) */
+ * would save too little to repay the joining of the parts.)
+ * A row belongs to one request, except for gdn_kv_append. */
 typedef struct {
   int32_t num_requests;        /* R                                            */
   int32_t num_rows;            /* rows in the packed q/k/v/o buffers           */
