@@ -315,20 +315,25 @@ def make_attn_dims(Hq, Hkv, D, page_size, io=GDN_BF16, scale=0.0) -> AttnDims:
 
 
 def make_rope(rotary_dim, inv_freq, positions, axis=None, interleaved=False) -> RopeParams:
-    """positions: device int32 [rows] or [axes][rows]; axis: device int32 [rotary_dim / 2]."""
+    """positions: device int32 [rows] or [axes][rows]; axis: device int32 [rotary_dim / 2]. The
+    structure keeps its tensors."""
     axes = 1 if positions is None or positions.dim() == 1 else positions.shape[0]
-    return RopeParams(int(rotary_dim), int(axes), int(interleaved), _ptr(inv_freq), _ptr(axis),
+    rope = RopeParams(int(rotary_dim), int(axes), int(interleaved), _ptr(inv_freq), _ptr(axis),
                       _ptr(positions))
+    rope.tensors = (inv_freq, axis, positions)
+    return rope
 
 
 def make_kv_batch(num_requests, num_rows, max_rows, num_pages, row_start, row_len, kv_len,
                   page_table, group_start=None, group_len=None, group_pages=None) -> KvBatch:
-    """Row map over a paged cache from device int32 tensors; page_table [requests][pages]."""
-    return KvBatch(int(num_requests), int(num_rows), int(max_rows), int(num_pages),
-                   0 if page_table is None else int(page_table.shape[1]),
-                   0 if group_start is None else int(group_start.numel()), _ptr(row_start),
-                   _ptr(row_len), _ptr(kv_len), _ptr(page_table), _ptr(group_start),
-                   _ptr(group_len), _ptr(group_pages))
+    """Row map over a paged cache from device int32 tensors; page_table [requests][pages]. The
+    structure keeps its tensors."""
+    tensors = (row_start, row_len, kv_len, page_table, group_start, group_len, group_pages)
+    batch = KvBatch(int(num_requests), int(num_rows), int(max_rows), int(num_pages),
+                    0 if page_table is None else int(page_table.shape[1]),
+                    0 if group_start is None else int(group_start.numel()), *map(_ptr, tensors))
+    batch.tensors = tensors
+    return batch
 
 
 def _rows(t):
