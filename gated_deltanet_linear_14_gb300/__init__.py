@@ -336,31 +336,59 @@ def make_kv_batch(num_requests, num_rows, max_rows, num_pages, row_start, row_le
     return batch
 
 
-def _rows(t):
+_types = None  # dtype code -> torch dtype
+
+
+def _type(code):
+    global _types
+    if _types is None:
+        import torch
+        _types = {GDN_F32: torch.float32, GDN_BF16: torch.bfloat16, GDN_F16: torch.float16}
+    return _types.get(code)  # None: the call itself refuses the code
+
+
+def _refuse(what):
+    raise GdnError(CODES["GDN_ERR_INVALID_ARG"], what)
+
+
+def _rows(t, rows, heads, dim, dtype):
     """(address, elements between rows) of a [rows][heads][dim] tensor whose heads are
-    contiguous within a row, e.g. a slice of a projection's output."""
+    contiguous within a row, e.g. a slice of a projection's output. It may have more rows and
+    heads than the call takes."""
     if t is None:
         return None, 0
-    rows, heads, dim = t.shape
+    n, h, d = t.shape
+    if n < rows or h < heads or d != dim or (dtype is not None and t.dtype is not dtype):
+        _refuse(f"row tensor: {t.dtype} {tuple(t.shape)} for {rows} rows, {heads} heads x {dim}")
+    if t.is_contiguous():
+        return t.data_ptr(), h * d
     between, head, one = t.stride()
-    if one != 1 or (heads > 1 and head != dim):
-        raise GdnError(CODES["GDN_ERR_INVALID_ARG"], "row tensor: heads not contiguous")
-    return t.data_ptr(), (between if rows > 1 else heads * dim)
+    if one != 1 or (h > 1 and head != d):
+        _refuse("row tensor: heads not contiguous")
+    return t.data_ptr(), (between if n > 1 else h * d)
 
 
 def gdn_rope(dims, rope, q, q_out, k=None, k_out=None, inverse=False, stream=None):
     rows = (q if q is not None else k).shape[0]
+    if q is not None and k is not None and k.shape[0] != rows:
+        _refuse(f"gdn_rope: q has {rows} rows, k {k.shape[0]}")
+    hq, hk, dim, dtype = dims.num_q_heads, dims.num_kv_heads, dims.head_dim, _type(dims.io_dtype)
     # (a structure passed where a pointer is declared goes by reference)
-    code = (_lib or load_library()).gdn_rope(dims, rope, rows, *_rows(q), *_rows(q_out), *_rows(k),
-                                             *_rows(k_out), int(inverse), _stream(stream))
+    code = (_lib or load_library()).gdn_rope(
+        dims, rope, rows, *_rows(q, rows, hq, dim, dtype), *_rows(q_out, rows, hq, dim, dtype),
+        *_rows(k, rows, hk, dim, dtype), *_rows(k_out, rows, hk, dim, dtype), int(inverse),
+        _stream(stream))
     if code:
         raise GdnError(code, "gdn_rope")
 
 
 def gdn_kv_append(dims, batch, rope, q, k, v, q_out, k_cache, v_cache, status, stream=None):
-    code = (_lib or load_library()).gdn_kv_append(dims, batch, rope, *_rows(q), *_rows(k),
-                                                  *_rows(v), *_rows(q_out), _ptr(k_cache),
-                                                  _ptr(v_cache), _ptr(status), _stream(stream))
+    rows = batch.num_rows
+    hq, hk, dim, dtype = dims.num_q_heads, dims.num_kv_heads, dims.head_dim, _type(dims.io_dtype)
+    code = (_lib or load_library()).gdn_kv_append(
+        dims, batch, rope, *_rows(q, rows, hq, dim, dtype), *_rows(k, rows, hk, dim, dtype),
+        *_rows(v, rows, hk, dim, dtype), *_rows(q_out, rows, hq, dim, dtype), _ptr(k_cache),
+        _ptr(v_cache), _ptr(status), _stream(stream))
     if code:
         raise GdnError(code, "gdn_kv_append")
 
@@ -381,7 +409,8 @@ def gdn_attn_plan(dims, batch, plan, plan_bytes, status, stream=None):
 
 def gdn_attn(dims, batch, plan, q, k_cache, v_cache, o, lse, workspace, workspace_bytes, status,
              stream=None):
-    code = (_lib or load_library()).gdn_attn(dims, batch, _ptr(plan), *_rows(q), _ptr(k_cache),
+    q_rows = _rows(q, batch.num_rows, dims.num_q_heads, dims.head_dim, _type(dims.io_dtype))
+    code = (_lib or load_library()).gdn_attn(dims, batch, _ptr(plan), *q_rows, _ptr(k_cache),
                                              _ptr(v_cache), _ptr(o), _ptr(lse), _ptr(workspace),
                                              int(workspace_bytes), _ptr(status), _stream(stream))
     if code:

@@ -43,3 +43,87 @@ def test_structures_keep_their_tensors():
     made(gdn.make_rope, 64, lambda: torch.ones(32), lambda: i32(3, 5), axis=lambda: i32(32))
     made(gdn.make_kv_batch, 4, 4, 1, 9, *[lambda: i32(4)] * 3, lambda: i32(4, 2),
          group_start=lambda: i32(1), group_len=lambda: i32(1), group_pages=lambda: i32(1))
+
+
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def rows(n, heads, dim=64, dtype=BF):
+    return torch.zeros(n, heads, dim, dtype=dtype)
+
+
+def code_of(call, *args, **kw):
+    with pytest.raises(gdn.GdnError) as e:
+        call(*args, stream=0, **kw)
+    return e.value.code
+
+
+def rope_code(q, q_out, k=None, k_out=None, dims=None, positions=None):
+    dims = dims or gdn.make_attn_dims(4, 2, 64, 16)
+    positions = i32((q if q is not None else k).shape[0]) if positions is None else positions
+    return code_of(gdn.gdn_rope, dims, gdn.make_rope(64, torch.ones(32), positions), q, q_out, k,
+                   k_out)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="host memory is passed on to the launch")
+def test_rope_rows_that_fit_reach_the_launch():
+    assert rope_code(rows(5, 4), rows(5, 4), rows(5, 2), rows(5, 2)) != INVALID
+    assert rope_code(rows(5, 4), rows(9, 4)) != INVALID                 # an output with more rows
+    assert rope_code(rows(5, 6)[:, :4], rows(5, 4)) != INVALID          # a slice of the heads
+    assert rope_code(rows(1, 6), rows(1, 4)) != INVALID                 # more heads than are turned
+
+
+def test_rope_rows_that_do_not_fit_are_refused():
+    q, k = rows(5, 4), rows(5, 2)
+    assert rope_code(q, rows(4, 4)) == INVALID                          # fewer rows out than in
+    assert rope_code(q, q, rows(4, 2), k) == INVALID                    # k shorter than q
+    assert rope_code(q, q, rows(6, 2), rows(6, 2)) == INVALID           # and longer
+    assert rope_code(q, q, k, rows(4, 2)) == INVALID
+    assert rope_code(rows(5, 3), q) == INVALID                          # fewer heads
+    assert rope_code(q, rows(5, 3)) == INVALID
+    assert rope_code(rows(5, 4, 32), q) == INVALID                      # another width
+    assert rope_code(rows(5, 4, dtype=F32), q) == INVALID               # another type
+    assert rope_code(q, rows(5, 4, dtype=HF)) == INVALID
+    assert rope_code(rows(5, 4, 128)[..., ::2], q) == INVALID           # elements apart
+    assert rope_code(rows(4, 5).transpose(0, 1), q) == INVALID          # heads not side by side
+
+
+def append_args(**kw):
+    a = dict(dims=gdn.make_attn_dims(4, 2, 64, 16),
+             batch=gdn.make_kv_batch(2, 5, 4, 3, i32(2), i32(2), i32(2), i32(2, 2)),
+             rope=gdn.make_rope(64, torch.ones(32), i32(5)), q=rows(5, 4), k=rows(5, 2),
+             v=rows(5, 2), q_out=rows(5, 4), k_cache=torch.zeros(3, 2, 16, 64, dtype=BF),
+             v_cache=torch.zeros(3, 2, 16, 64, dtype=BF), status=i32(1))
+    a.update(kw)
+    return a
+
+
+def attn_args(**kw):
+    a = append_args()
+    for name in ("rope", "q_out", "k", "v"):
+        del a[name]
+    n = [size(a["dims"], a["batch"]) for size in
+         (gdn.gdn_attn_plan_bytes, gdn.gdn_attn_workspace_bytes)]
+    a.update(plan=torch.zeros(n[0], dtype=torch.uint8), o=rows(5, 4), lse=torch.zeros(5, 4),
+             workspace=torch.zeros(n[1], dtype=torch.uint8), workspace_bytes=n[1])
+    a.update(kw)
+    return a
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="host memory is passed on to the launch")
+def test_calls_that_fit_reach_the_launch():
+    assert code_of(gdn.gdn_kv_append, **append_args()) != INVALID
+    assert code_of(gdn.gdn_kv_append, **append_args(k=rows(8, 2), q_out=rows(6, 4))) != INVALID
+    assert code_of(gdn.gdn_attn, **attn_args()) != INVALID
+
+
+@pytest.mark.parametrize("name,heads", [("q", 4), ("k", 2), ("v", 2), ("q_out", 4)])
+def test_append_rows_that_do_not_fit_are_refused(name, heads):
+    for t in (rows(4, heads), rows(5, heads - 1), rows(5, heads, 128), rows(5, heads, dtype=HF),
+              rows(heads, 5).transpose(0, 1)):
+        assert code_of(gdn.gdn_kv_append, **append_args(**{name: t})) == INVALID, t.shape
+
+
+def test_attn_query_rows_that_do_not_fit_are_refused():
+    for t in (rows(4, 4), rows(5, 3), rows(5, 4, 128), rows(5, 4, dtype=HF)):
+        assert code_of(gdn.gdn_attn, **attn_args(q=t)) == INVALID, t.shape
