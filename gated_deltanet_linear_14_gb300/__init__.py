@@ -91,6 +91,7 @@ class AttnDims(ctypes.Structure):
 
 
 class RopeParams(ctypes.Structure):
+    columns = None  # of the positions, where make_rope saw them
     _fields_ = [("rotary_dim", ctypes.c_int32), ("num_axes", ctypes.c_int32),
                 ("interleaved", ctypes.c_int32), ("inv_freq", ctypes.c_void_p),
                 ("axis", ctypes.c_void_p), ("positions", ctypes.c_void_p)]
@@ -314,13 +315,33 @@ def make_attn_dims(Hq, Hkv, D, page_size, io=GDN_BF16, scale=0.0) -> AttnDims:
     return AttnDims(Hq, Hkv, D, page_size, io, float(scale))
 
 
+def _int32(t, least, what):
+    """Address of a device int32 tensor of at least `least` contiguous elements (or None, or an
+    int address)."""
+    if t is None or isinstance(t, int):
+        return t
+    import torch
+    if t.dtype is not torch.int32 or t.numel() < least or not t.is_contiguous():
+        _refuse(f"{what}: {t.dtype} {tuple(t.shape)} strides {t.stride()} where {least} int32 "
+                "values side by side are read")
+    return t.data_ptr()
+
+
 def make_rope(rotary_dim, inv_freq, positions, axis=None, interleaved=False) -> RopeParams:
-    """positions: device int32 [rows] or [axes][rows]; axis: device int32 [rotary_dim / 2]. The
-    structure keeps its tensors."""
+    """positions: device int32 [rows] or [axes][rows]; axis: device int32 [rotary_dim / 2];
+    inv_freq: device float32 [rotary_dim / 2]. The structure keeps its tensors."""
+    rotary_dim = int(rotary_dim)
     axes = 1 if positions is None or positions.dim() == 1 else positions.shape[0]
-    rope = RopeParams(int(rotary_dim), int(axes), int(interleaved), _ptr(inv_freq), _ptr(axis),
-                      _ptr(positions))
+    if inv_freq is not None and not isinstance(inv_freq, int):
+        import torch
+        if (inv_freq.dtype is not torch.float32 or inv_freq.numel() < rotary_dim // 2
+                or not inv_freq.is_contiguous()):
+            _refuse(f"inv_freq: {inv_freq.dtype} {tuple(inv_freq.shape)} where "
+                    f"{rotary_dim // 2} float32 values side by side are read")
+    rope = RopeParams(rotary_dim, int(axes), int(interleaved), _ptr(inv_freq),
+                      _int32(axis, rotary_dim // 2, "axis"), _int32(positions, 0, "positions"))
     rope.tensors = (inv_freq, axis, positions)
+    rope.columns = None if positions is None else int(positions.shape[-1])
     return rope
 
 
@@ -328,11 +349,15 @@ def make_kv_batch(num_requests, num_rows, max_rows, num_pages, row_start, row_le
                   page_table, group_start=None, group_len=None, group_pages=None) -> KvBatch:
     """Row map over a paged cache from device int32 tensors; page_table [requests][pages]. The
     structure keeps its tensors."""
-    tensors = (row_start, row_len, kv_len, page_table, group_start, group_len, group_pages)
-    batch = KvBatch(int(num_requests), int(num_rows), int(max_rows), int(num_pages),
-                    0 if page_table is None else int(page_table.shape[1]),
-                    0 if group_start is None else int(group_start.numel()), *map(_ptr, tensors))
-    batch.tensors = tensors
+    R, width = int(num_requests), 0 if page_table is None else int(page_table.shape[1])
+    groups = 0 if group_start is None else int(group_start.numel())
+    batch = KvBatch(R, int(num_rows), int(max_rows), int(num_pages), width, groups,
+                    _int32(row_start, R, "row_start"), _int32(row_len, R, "row_len"),
+                    _int32(kv_len, R, "kv_len"), _int32(page_table, R * width, "page_table"),
+                    _int32(group_start, groups, "group_start"),
+                    _int32(group_len, groups, "group_len"),
+                    _int32(group_pages, groups, "group_pages"))
+    batch.tensors = (row_start, row_len, kv_len, page_table, group_start, group_len, group_pages)
     return batch
 
 
@@ -368,10 +393,17 @@ def _rows(t, rows, heads, dim, dtype):
     return t.data_ptr(), (between if n > 1 else h * d)
 
 
+def _positions(rope, rows):
+    n = rope.columns
+    if n is not None and n != rows and (n < rows or rope.num_axes > 1) and rope.rotary_dim:
+        _refuse(f"positions: {n} on each axis for {rows} rows")
+
+
 def gdn_rope(dims, rope, q, q_out, k=None, k_out=None, inverse=False, stream=None):
     rows = (q if q is not None else k).shape[0]
     if q is not None and k is not None and k.shape[0] != rows:
         _refuse(f"gdn_rope: q has {rows} rows, k {k.shape[0]}")
+    _positions(rope, rows)
     hq, hk, dim, dtype = dims.num_q_heads, dims.num_kv_heads, dims.head_dim, _type(dims.io_dtype)
     # (a structure passed where a pointer is declared goes by reference)
     code = (_lib or load_library()).gdn_rope(
@@ -384,6 +416,8 @@ def gdn_rope(dims, rope, q, q_out, k=None, k_out=None, inverse=False, stream=Non
 
 def gdn_kv_append(dims, batch, rope, q, k, v, q_out, k_cache, v_cache, status, stream=None):
     rows = batch.num_rows
+    if rope is not None:
+        _positions(rope, rows)
     hq, hk, dim, dtype = dims.num_q_heads, dims.num_kv_heads, dims.head_dim, _type(dims.io_dtype)
     code = (_lib or load_library()).gdn_kv_append(
         dims, batch, rope, *_rows(q, rows, hq, dim, dtype), *_rows(k, rows, hk, dim, dtype),

@@ -127,3 +127,63 @@ def test_append_rows_that_do_not_fit_are_refused(name, heads):
 def test_attn_query_rows_that_do_not_fit_are_refused():
     for t in (rows(4, 4), rows(5, 3), rows(5, 4, 128), rows(5, 4, dtype=HF)):
         assert code_of(gdn.gdn_attn, **attn_args(q=t)) == INVALID, t.shape
+
+
+def refused(make, *args, **kw):
+    with pytest.raises(gdn.GdnError) as e:
+        make(*args, **kw)
+    return e.value.code == INVALID
+
+
+def test_index_tensors_that_are_not_int32_are_refused():
+    """torch counts in int64 unless told otherwise; read as int32 every other number is 0."""
+    freq = torch.ones(32)
+    assert refused(gdn.make_rope, 64, freq, torch.arange(5))
+    assert refused(gdn.make_rope, 64, freq, i32(5), axis=torch.zeros(32, dtype=torch.int64))
+    assert refused(gdn.make_rope, 64, freq.double(), i32(5))
+    assert refused(gdn.make_rope, 64, freq.bfloat16(), i32(5))
+    good = [i32(2), i32(2), i32(2), i32(2, 3), i32(1), i32(1), i32(1)]
+    gdn.make_kv_batch(2, 5, 4, 9, *good)
+    for i, t in enumerate(good):
+        bad = list(good)
+        bad[i] = t.long()
+        assert refused(gdn.make_kv_batch, 2, 5, 4, 9, *bad), i
+
+
+def test_index_tensors_that_are_short_or_strided_are_refused():
+    freq = torch.ones(32)
+    assert refused(gdn.make_rope, 64, torch.ones(31), i32(5))
+    assert refused(gdn.make_rope, 64, torch.ones(64)[::2], i32(5))
+    assert refused(gdn.make_rope, 64, freq, i32(5), axis=i32(31))
+    assert refused(gdn.make_rope, 64, freq, i32(3, 8)[:, :5])      # three axes cut from longer ones
+    assert refused(gdn.make_rope, 64, freq, i32(5, 3).t())
+    good = [i32(4), i32(4), i32(4), i32(4, 3), i32(2), i32(2), i32(2)]
+    gdn.make_kv_batch(4, 5, 4, 9, *good)
+    for i, t in enumerate(good):
+        if i != 4:                                                 # (the groups are as many as it holds)
+            bad = list(good)
+            bad[i] = t[:-1]
+            assert refused(gdn.make_kv_batch, 4, 5, 4, 9, *bad), i
+        bad = list(good)
+        bad[i] = torch.stack([t, t], -1)[..., 0] if t.dim() == 1 else i32(4, 8)[:, :3]
+        assert refused(gdn.make_kv_batch, 4, 5, 4, 9, *bad), i
+    assert refused(gdn.make_kv_batch, 4, 5, 4, 9, *good[:3], i32(3, 4).t())
+
+
+def test_positions_for_other_rows_are_refused():
+    q = rows(5, 4)
+    assert rope_code(q, q, positions=i32(4)) == INVALID
+    assert rope_code(q, q, positions=i32(3, 6)) == INVALID         # each axis would start elsewhere
+    assert rope_code(q, q, positions=i32(3, 4)) == INVALID
+    for n in (4, 3):
+        short = gdn.make_rope(64, torch.ones(32), i32(n))
+        assert code_of(gdn.gdn_kv_append, **append_args(rope=short)) == INVALID
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="host memory is passed on to the launch")
+def test_positions_with_room_reach_the_launch():
+    q = rows(5, 4)
+    assert rope_code(q, q, positions=i32(9)) != INVALID            # one axis: the first ones
+    assert rope_code(q, q, positions=i32(3, 5)) != INVALID
+    none = gdn.make_rope(0, None, None)
+    assert code_of(gdn.gdn_rope, gdn.make_attn_dims(4, 2, 64, 16), none, q, q) != INVALID
