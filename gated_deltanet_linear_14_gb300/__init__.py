@@ -393,6 +393,20 @@ def _rows(t, rows, heads, dim, dtype):
     return t.data_ptr(), (between if n > 1 else h * d)
 
 
+def _dense(t, count, dtype, what):
+    """Address of a tensor of at least `count` contiguous elements (or None, or an int address)."""
+    if t is None or isinstance(t, int):
+        return t
+    if (t.dtype is not dtype and dtype is not None) or t.numel() < count or not t.is_contiguous():
+        _refuse(f"{what}: {t.dtype} {tuple(t.shape)} strides {t.stride()} where {count} elements of "
+                f"{dtype} side by side are used")
+    return t.data_ptr()
+
+
+def _cache_elements(dims, batch):
+    return batch.num_pages * dims.num_kv_heads * dims.page_size * dims.head_dim
+
+
 def _positions(rope, rows):
     n = rope.columns
     if n is not None and n != rows and (n < rows or rope.num_axes > 1) and rope.rotary_dim:
@@ -415,14 +429,15 @@ def gdn_rope(dims, rope, q, q_out, k=None, k_out=None, inverse=False, stream=Non
 
 
 def gdn_kv_append(dims, batch, rope, q, k, v, q_out, k_cache, v_cache, status, stream=None):
-    rows = batch.num_rows
+    rows, n = batch.num_rows, _cache_elements(dims, batch)
     if rope is not None:
         _positions(rope, rows)
     hq, hk, dim, dtype = dims.num_q_heads, dims.num_kv_heads, dims.head_dim, _type(dims.io_dtype)
     code = (_lib or load_library()).gdn_kv_append(
         dims, batch, rope, *_rows(q, rows, hq, dim, dtype), *_rows(k, rows, hk, dim, dtype),
-        *_rows(v, rows, hk, dim, dtype), *_rows(q_out, rows, hq, dim, dtype), _ptr(k_cache),
-        _ptr(v_cache), _ptr(status), _stream(stream))
+        *_rows(v, rows, hk, dim, dtype), *_rows(q_out, rows, hq, dim, dtype),
+        _dense(k_cache, n, dtype, "k_cache"), _dense(v_cache, n, dtype, "v_cache"), _ptr(status),
+        _stream(stream))
     if code:
         raise GdnError(code, "gdn_kv_append")
 
@@ -443,10 +458,13 @@ def gdn_attn_plan(dims, batch, plan, plan_bytes, status, stream=None):
 
 def gdn_attn(dims, batch, plan, q, k_cache, v_cache, o, lse, workspace, workspace_bytes, status,
              stream=None):
-    q_rows = _rows(q, batch.num_rows, dims.num_q_heads, dims.head_dim, _type(dims.io_dtype))
-    code = (_lib or load_library()).gdn_attn(dims, batch, _ptr(plan), *q_rows, _ptr(k_cache),
-                                             _ptr(v_cache), _ptr(o), _ptr(lse), _ptr(workspace),
-                                             int(workspace_bytes), _ptr(status), _stream(stream))
+    rows, n, lse_type = batch.num_rows, _cache_elements(dims, batch), _type(GDN_F32)
+    hq, dim, dtype = dims.num_q_heads, dims.head_dim, _type(dims.io_dtype)
+    code = (_lib or load_library()).gdn_attn(
+        dims, batch, _ptr(plan), *_rows(q, rows, hq, dim, dtype),
+        _dense(k_cache, n, dtype, "k_cache"), _dense(v_cache, n, dtype, "v_cache"),
+        _dense(o, rows * hq * dim, dtype, "o"), _dense(lse, rows * hq, lse_type, "lse"),
+        _ptr(workspace), int(workspace_bytes), _ptr(status), _stream(stream))
     if code:
         raise GdnError(code, "gdn_attn")
 

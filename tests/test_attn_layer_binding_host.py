@@ -187,3 +187,32 @@ def test_positions_with_room_reach_the_launch():
     assert rope_code(q, q, positions=i32(3, 5)) != INVALID
     none = gdn.make_rope(0, None, None)
     assert code_of(gdn.gdn_rope, gdn.make_attn_dims(4, 2, 64, 16), none, q, q) != INVALID
+
+
+def not_fitting(t, other):
+    """Tensors that hold other elements than a dense t does: too few, strided, of another type."""
+    wide = torch.zeros(*t.shape[:-1], 2 * t.shape[-1], dtype=t.dtype)
+    return [t[:-1], wide[..., ::2], wide[..., :t.shape[-1]], t.to(other),
+            torch.zeros_like(t).transpose(0, 1)]
+
+
+@pytest.mark.parametrize("name", ["k_cache", "v_cache"])
+def test_caches_that_are_not_dense_are_refused(name):
+    for t in not_fitting(torch.zeros(3, 2, 16, 64, dtype=BF), HF):
+        assert code_of(gdn.gdn_kv_append, **append_args(**{name: t})) == INVALID, t.shape
+        assert code_of(gdn.gdn_attn, **attn_args(**{name: t})) == INVALID, t.shape
+
+
+def test_outputs_that_are_not_dense_are_refused():
+    for t in not_fitting(rows(5, 4), HF):
+        assert code_of(gdn.gdn_attn, **attn_args(o=t)) == INVALID, t.shape
+    for t in not_fitting(torch.zeros(5, 4), torch.float64):
+        assert code_of(gdn.gdn_attn, **attn_args(lse=t)) == INVALID, t.shape
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="host memory is passed on to the launch")
+def test_outputs_and_caches_of_other_shapes_reach_the_launch():
+    assert code_of(gdn.gdn_attn, **attn_args(o=torch.zeros(5, 256, dtype=BF), lse=None)) != INVALID
+    assert code_of(gdn.gdn_attn, **attn_args(o=rows(9, 4))) != INVALID
+    big = torch.zeros(8, 2, 16, 64, dtype=BF)
+    assert code_of(gdn.gdn_attn, **attn_args(k_cache=big, v_cache=big)) != INVALID
