@@ -15,17 +15,31 @@
 
 namespace gdn {
 
-// One thread waits on an mbarrier that nothing arrives at; the bounded wait
-// gives up after limit_ns and the kernel reports GDN_DEV_TIMEOUT, the path
-// every kernel takes when one of its own copies or MMAs does not complete.
+// Waits on mbarriers that nothing arrives at, as every kernel waits for its own
+// copies and MMAs: one thread (umma::mbar_wait) and a whole warp
+// (umma::mbar_wait_warp) each give up after limit_ns, and a further wait of
+// that warp, which may take much longer, ends at once by the word that the first
+// one left. The kernel reports GDN_DEV_TIMEOUT if all three gave up.
+constexpr int64_t kCheckMaxNs = 10000000000LL;
 __global__ void wait_check_kernel(uint64_t limit_ns, int32_t* status) {
   __shared__ __align__(8) uint64_t bar;
+  __shared__ uint32_t dead;
+  __shared__ int32_t thread, warp, again;
+  const uint32_t b = umma::smem_u32(&bar);
   if (threadIdx.x == 0) {
-    const uint32_t b = umma::smem_u32(&bar);
     umma::mbar_init(b, 1);
     umma::mbar_fence_init();
-    if (!umma::mbar_wait(b, 0, limit_ns)) report(status, GDN_DEV_TIMEOUT);
+    dead = 0, thread = warp = again = 0;
   }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    if (!umma::mbar_wait(b, 0, limit_ns)) thread = GDN_DEV_TIMEOUT;
+  } else if (threadIdx.x >= 32) {
+    umma::mbar_wait_warp(b, 0, &dead, &warp, limit_ns);
+    if (dead) umma::mbar_wait_warp(b, 0, &dead, &again, kCheckMaxNs);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && thread && warp && again) report(status, GDN_DEV_TIMEOUT);
 }
 
 // SMs of the current device (looked up once per device; declared in kernels.h).
@@ -649,8 +663,8 @@ gdn_status gdn_chunk_prefill_noalloc(const gdn_dims* dims, const gdn_batch* batc
 }
 
 gdn_status gdn_check_bounded_wait(int64_t limit_ns, int32_t* status, gdn_stream_t stream) {
-  if (!status || limit_ns <= 0 || limit_ns > 10000000000LL) return GDN_ERR_INVALID_ARG;
-  gdn::wait_check_kernel<<<1, 32, 0, (cudaStream_t)stream>>>((uint64_t)limit_ns, status);
+  if (!status || limit_ns <= 0 || limit_ns > gdn::kCheckMaxNs) return GDN_ERR_INVALID_ARG;
+  gdn::wait_check_kernel<<<1, 64, 0, (cudaStream_t)stream>>>((uint64_t)limit_ns, status);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 

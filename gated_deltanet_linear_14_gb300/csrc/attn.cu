@@ -179,35 +179,6 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(~0u, x, 0); }
 
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// The slow end of a wait by a whole warp, bounded as umma::mbar_wait is; `dead`
-// (shared) says that another role gave up.
-__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* dead,
-                                           int32_t* status) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 0; i < kWaitPolls; ++i) {
-    if (__all_sync(~0u, bar_try(bar, parity))) return true;
-    if ((i & 63) == 63) {
-      const uint64_t now = global_ns();
-      if (t0 == 0) t0 = now;
-      if (__any_sync(~0u, *dead || now - t0 > kWaitNs)) break;
-    }
-  }
-  *dead = 1;
-  report(status, GDN_DEV_TIMEOUT);
-  return false;
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
@@ -377,8 +348,8 @@ attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUte
   // All lanes of a warp wait, and go on together. A wait that gives up ends
   // its role; words[1] then ends the others.
   auto wait = [&](uint32_t bar, uint32_t parity) {
-    if (__all_sync(~0u, bar_try(bar, parity))) return true;
-    return bar_wait_long(bar, parity, words + 1, status);
+    if (__all_sync(~0u, mbar_try(bar, parity))) return true;
+    return mbar_wait_warp(bar, parity, words + 1, status);
   };
 
   if (!P.good()) {

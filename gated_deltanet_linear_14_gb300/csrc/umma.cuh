@@ -15,6 +15,8 @@
 
 #include <stdint.h>
 
+#include "common.cuh"
+
 namespace gdn {
 namespace umma {
 
@@ -51,6 +53,19 @@ __device__ __forceinline__ uint64_t global_ns() {
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint32_t kWaitPolls = 1u << 26;
 
+// Whether the phase with the given parity is complete (after a short wait of the
+// hardware's own).
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Wait for the phase with the given parity to complete; gives up after
 // limit_ns of global time and returns false (the caller reports and
 // unwinds).
@@ -58,18 +73,30 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
                                           uint64_t limit_ns = kWaitNs) {
   uint64_t t0 = 0;
   for (uint32_t i = 0; i < kWaitPolls; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return true;
+    if (mbar_try(bar, parity)) return true;
     const uint64_t now = global_ns();
     if (i == 0) t0 = now;
     else if (now - t0 > limit_ns) return false;
   }
+  return false;
+}
+
+// The slow end of a wait by a whole warp, bounded in the same way. `dead` (shared
+// by the roles of a CTA) says that another role gave up, which ends this wait too.
+static __device__ __noinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity,
+                                                   volatile uint32_t* dead, int32_t* status,
+                                                   uint64_t limit_ns = kWaitNs) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+    if (__all_sync(~0u, mbar_try(bar, parity))) return true;
+    if ((i & 63) == 63) {
+      const uint64_t now = global_ns();
+      if (t0 == 0) t0 = now;
+      if (__any_sync(~0u, *dead || now - t0 > limit_ns)) break;
+    }
+  }
+  *dead = 1;
+  report(status, GDN_DEV_TIMEOUT);
   return false;
 }
 

@@ -455,12 +455,13 @@ gdn_status gdn_prefill(const gdn_dims* dims, const gdn_batch* batch,
 
 /* Failure-detection check of the bounded on-chip waits. Every wait a
  * kernel makes on its own bulk copies or MMAs (gdn_decode,
- * gdn_chunk_prefill) gives up after one second of global time: the kernel
- * then writes GDN_DEV_TIMEOUT to *status, lets its copies in flight land,
- * frees its tensor memory and returns, so the context stays usable. This
- * call runs that path on demand: one block waits on an mbarrier that
- * nothing arrives at, gives up after limit_ns of global time
- * (0 < limit_ns <= 10^10) and writes GDN_DEV_TIMEOUT to *status.
+ * gdn_chunk_prefill, gdn_attn) gives up after one second of global time: the
+ * kernel then writes GDN_DEV_TIMEOUT to *status, lets its copies in flight
+ * land, frees its tensor memory and returns, so the context stays usable. This
+ * call runs that path on demand: a thread and a warp of one block wait, each in
+ * its kind of wait, on an mbarrier that nothing arrives at, give up after
+ * limit_ns of global time (0 < limit_ns <= 10^10), the warp's next wait ends
+ * with them, and GDN_DEV_TIMEOUT is written to *status.
  *   status  device int32 (first error wins, as for every entry point)
  * Returns GDN_ERR_INVALID_ARG for a NULL status or a limit out of range. */
 gdn_status gdn_check_bounded_wait(int64_t limit_ns, int32_t* status,
