@@ -613,7 +613,9 @@ gdn_status gdn_attn(const gdn_attn_dims* dims, const gdn_kv_batch* batch, const 
 /* Text for a status code (host, static storage). */
 const char* gdn_strerror(int32_t status);
 
-/* ABI version of this header: (major << 16) | minor. */
+/* ABI version of this header: (major << 16) | minor. 2.2 added GDN_F16, the
+ * attention-layer structures and gdn_rope, gdn_kv_append, gdn_attn_plan,
+ * gdn_attn and their sizes. */
 int32_t gdn_abi_version(void);
 
 #ifdef __cplusplus

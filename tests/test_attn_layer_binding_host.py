@@ -216,3 +216,7 @@ def test_outputs_and_caches_of_other_shapes_reach_the_launch():
     assert code_of(gdn.gdn_attn, **attn_args(o=rows(9, 4))) != INVALID
     big = torch.zeros(8, 2, 16, 64, dtype=BF)
     assert code_of(gdn.gdn_attn, **attn_args(k_cache=big, v_cache=big)) != INVALID
+
+
+def test_abi_version_tells_the_attention_layer_calls():
+    assert gdn.gdn_abi_version() >= (2 << 16 | 2)
