@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -361,36 +362,42 @@ def make_kv_batch(num_requests, num_rows, max_rows, num_pages, row_start, row_le
     return batch
 
 
-_types = None  # dtype code -> torch dtype
+class _Types(dict):
+    """dtype code -> torch dtype; None for other codes, which the calls themselves refuse."""
 
-
-def _type(code):
-    global _types
-    if _types is None:
+    def __missing__(self, code):
         import torch
-        _types = {GDN_F32: torch.float32, GDN_BF16: torch.bfloat16, GDN_F16: torch.float16}
-    return _types.get(code)  # None: the call itself refuses the code
+        self.update({GDN_F32: torch.float32, GDN_BF16: torch.bfloat16, GDN_F16: torch.float16})
+        return self.get(code)
+
+
+_types = _Types()
+# Several fields of a structure in one go (a field by itself costs half as much as all)
+_attn_dims = struct.Struct("=5i").unpack_from   # (Hq, Hkv, D, page size, io dtype)
+_kv_counts = struct.Struct("=4i").unpack_from   # (requests, rows, max rows, pages)
 
 
 def _refuse(what):
     raise GdnError(CODES["GDN_ERR_INVALID_ARG"], what)
 
 
-def _rows(t, rows, heads, dim, dtype):
-    """(address, elements between rows) of a [rows][heads][dim] tensor whose heads are
-    contiguous within a row, e.g. a slice of a projection's output. It may have more rows and
-    heads than the call takes."""
-    if t is None:
-        return None, 0
+def _rows(t, heads, dim, dtype):
+    """(rows, address, elements between rows) of a [rows][heads][dim] tensor whose heads are
+    contiguous within a row, e.g. a slice of a projection's output. It may have more heads than
+    the call takes."""
     n, h, d = t.shape
-    if n < rows or h < heads or d != dim or (dtype is not None and t.dtype is not dtype):
-        _refuse(f"row tensor: {t.dtype} {tuple(t.shape)} for {rows} rows, {heads} heads x {dim}")
+    if h < heads or d != dim or (t.dtype is not dtype and dtype is not None):
+        _refuse(f"row tensor: {t.dtype} {tuple(t.shape)} for {heads} heads x {dim} of {dtype}")
     if t.is_contiguous():
-        return t.data_ptr(), h * d
+        return n, t.data_ptr(), h * d
     between, head, one = t.stride()
     if one != 1 or (h > 1 and head != d):
         _refuse("row tensor: heads not contiguous")
-    return t.data_ptr(), (between if n > 1 else h * d)
+    return n, t.data_ptr(), (between if n > 1 else h * d)
+
+
+def _too_few(what, n, rows):
+    _refuse(f"{what}: {n} rows where {rows} are used")
 
 
 def _dense(t, count, dtype, what):
@@ -403,41 +410,68 @@ def _dense(t, count, dtype, what):
     return t.data_ptr()
 
 
-def _cache_elements(dims, batch):
-    return batch.num_pages * dims.num_kv_heads * dims.page_size * dims.head_dim
-
-
 def _positions(rope, rows):
+    """rope.columns differs from the call's rows: more are all right on a single axis."""
     n = rope.columns
-    if n is not None and n != rows and (n < rows or rope.num_axes > 1) and rope.rotary_dim:
+    if n is not None and (n < rows or rope.num_axes > 1) and rope.rotary_dim:
         _refuse(f"positions: {n} on each axis for {rows} rows")
 
 
 def gdn_rope(dims, rope, q, q_out, k=None, k_out=None, inverse=False, stream=None):
-    rows = (q if q is not None else k).shape[0]
-    if q is not None and k is not None and k.shape[0] != rows:
-        _refuse(f"gdn_rope: q has {rows} rows, k {k.shape[0]}")
-    _positions(rope, rows)
-    hq, hk, dim, dtype = dims.num_q_heads, dims.num_kv_heads, dims.head_dim, _type(dims.io_dtype)
+    hq, hk, dim, _, io = _attn_dims(dims)
+    dtype = _types[io]
+    q_at = q_row = qo_at = qo_row = k_at = k_row = ko_at = ko_row = 0
+    if q is not None:
+        rows, q_at, q_row = _rows(q, hq, dim, dtype)
+    if k is not None:
+        n, k_at, k_row = _rows(k, hk, dim, dtype)
+        if q is not None and n != rows:
+            _refuse(f"gdn_rope: q has {rows} rows, k {n}")
+        rows = n
+    if q_out is not None:
+        n, qo_at, qo_row = _rows(q_out, hq, dim, dtype)
+        if n < rows:
+            _too_few("q_out", n, rows)
+    if k_out is not None:
+        n, ko_at, ko_row = _rows(k_out, hk, dim, dtype)
+        if n < rows:
+            _too_few("k_out", n, rows)
+    if rope.columns != rows:
+        _positions(rope, rows)
     # (a structure passed where a pointer is declared goes by reference)
-    code = (_lib or load_library()).gdn_rope(
-        dims, rope, rows, *_rows(q, rows, hq, dim, dtype), *_rows(q_out, rows, hq, dim, dtype),
-        *_rows(k, rows, hk, dim, dtype), *_rows(k_out, rows, hk, dim, dtype), int(inverse),
-        _stream(stream))
+    code = (_lib or load_library()).gdn_rope(dims, rope, rows, q_at, q_row, qo_at, qo_row, k_at,
+                                             k_row, ko_at, ko_row, int(inverse), _stream(stream))
     if code:
         raise GdnError(code, "gdn_rope")
 
 
 def gdn_kv_append(dims, batch, rope, q, k, v, q_out, k_cache, v_cache, status, stream=None):
-    rows, n = batch.num_rows, _cache_elements(dims, batch)
-    if rope is not None:
+    hq, hk, dim, ps, io = _attn_dims(dims)
+    _, rows, _, pages = _kv_counts(batch)
+    dtype, n_cache = _types[io], pages * hk * ps * dim
+    q_at = q_row = qo_at = qo_row = k_at = k_row = v_at = v_row = 0
+    if k is not None:
+        n, k_at, k_row = _rows(k, hk, dim, dtype)
+        if n < rows:
+            _too_few("k", n, rows)
+    if v is not None:
+        n, v_at, v_row = _rows(v, hk, dim, dtype)
+        if n < rows:
+            _too_few("v", n, rows)
+    if q is not None:
+        n, q_at, q_row = _rows(q, hq, dim, dtype)
+        if n < rows:
+            _too_few("q", n, rows)
+    if q_out is not None:
+        n, qo_at, qo_row = _rows(q_out, hq, dim, dtype)
+        if n < rows:
+            _too_few("q_out", n, rows)
+    if rope is not None and rope.columns != rows:
         _positions(rope, rows)
-    hq, hk, dim, dtype = dims.num_q_heads, dims.num_kv_heads, dims.head_dim, _type(dims.io_dtype)
     code = (_lib or load_library()).gdn_kv_append(
-        dims, batch, rope, *_rows(q, rows, hq, dim, dtype), *_rows(k, rows, hk, dim, dtype),
-        *_rows(v, rows, hk, dim, dtype), *_rows(q_out, rows, hq, dim, dtype),
-        _dense(k_cache, n, dtype, "k_cache"), _dense(v_cache, n, dtype, "v_cache"), _ptr(status),
-        _stream(stream))
+        dims, batch, rope, q_at, q_row, k_at, k_row, v_at, v_row, qo_at, qo_row,
+        _dense(k_cache, n_cache, dtype, "k_cache"), _dense(v_cache, n_cache, dtype, "v_cache"),
+        _ptr(status), _stream(stream))
     if code:
         raise GdnError(code, "gdn_kv_append")
 
@@ -458,13 +492,18 @@ def gdn_attn_plan(dims, batch, plan, plan_bytes, status, stream=None):
 
 def gdn_attn(dims, batch, plan, q, k_cache, v_cache, o, lse, workspace, workspace_bytes, status,
              stream=None):
-    rows, n, lse_type = batch.num_rows, _cache_elements(dims, batch), _type(GDN_F32)
-    hq, dim, dtype = dims.num_q_heads, dims.head_dim, _type(dims.io_dtype)
+    hq, hk, dim, ps, io = _attn_dims(dims)
+    _, rows, _, pages = _kv_counts(batch)
+    dtype, n_cache, q_at, q_row = _types[io], pages * hk * ps * dim, 0, 0
+    if q is not None:
+        n, q_at, q_row = _rows(q, hq, dim, dtype)
+        if n < rows:
+            _too_few("q", n, rows)
     code = (_lib or load_library()).gdn_attn(
-        dims, batch, _ptr(plan), *_rows(q, rows, hq, dim, dtype),
-        _dense(k_cache, n, dtype, "k_cache"), _dense(v_cache, n, dtype, "v_cache"),
-        _dense(o, rows * hq * dim, dtype, "o"), _dense(lse, rows * hq, lse_type, "lse"),
-        _ptr(workspace), int(workspace_bytes), _ptr(status), _stream(stream))
+        dims, batch, _ptr(plan), q_at, q_row, _dense(k_cache, n_cache, dtype, "k_cache"),
+        _dense(v_cache, n_cache, dtype, "v_cache"), _dense(o, rows * hq * dim, dtype, "o"),
+        _dense(lse, rows * hq, _types[GDN_F32], "lse"), _ptr(workspace), int(workspace_bytes),
+        _ptr(status), _stream(stream))
     if code:
         raise GdnError(code, "gdn_attn")
 
