@@ -74,6 +74,13 @@ __device__ __forceinline__ T block_scan(T v, T& total, T* sm) {
   return excl;
 }
 
+// The lanes' sum, of values below 2^51 each (in parts of 24 and 27 bits).
+__device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
+  const unsigned lo = __reduce_add_sync(~0u, (unsigned)v & 0xFFFFFF);
+  const unsigned hi = __reduce_add_sync(~0u, (unsigned)(v >> 24));
+  return ((unsigned long long)hi << 24) + lo;
+}
+
 __global__ void __launch_bounds__(kPlanThreads)
 attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, AttnStamp stamp, char* plan,
                  int32_t* status) {
@@ -108,7 +115,7 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, AttnStamp stamp, char* pla
     return kv_request_ok(B, A.ps, start, len, kv);
   };
 
-  unsigned long long rows_here = 0, rows_all;
+  unsigned long long rows_here = 0;
   for (int r = tid; r < B.R; r += kPlanThreads) {
     int start, len, kv;
     if (valid(r, start, len, kv)) rows_here += len;
@@ -118,7 +125,10 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, AttnStamp stamp, char* pla
   }
   for (int i = tid; i < L.max_list; i += kPlanThreads) list[i].row = -1;
   if (tid == 0) saved_s = 0, longest_s = 0;
-  block_scan(rows_here, rows_all, scan64);
+  rows_here = warp_sum(rows_here);
+  if (lane == 0) scan64[warp] = rows_here;
+  __syncthreads();
+  const unsigned long long rows_all = warp_sum(scan64[lane]);
   // More rows than there are: some belong to several requests. Those requests are
   // left out (k0 = -1), so that the others' items fit the plan's bounds.
   const bool clash = rows_all > (unsigned long long)B.num_rows;
