@@ -421,6 +421,8 @@ def gdn_rope(dims, rope, q, q_out, k=None, k_out=None, inverse=False, stream=Non
     hq, hk, dim, _, io = _attn_dims(dims)
     dtype = _types[io]
     q_at = q_row = qo_at = qo_row = k_at = k_row = ko_at = ko_row = 0
+    if q is None and k is None:
+        _refuse("gdn_rope: neither q nor k")
     if q is not None:
         rows, q_at, q_row = _rows(q, hq, dim, dtype)
     if k is not None:

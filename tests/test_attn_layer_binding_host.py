@@ -86,6 +86,9 @@ def test_rope_rows_that_do_not_fit_are_refused():
     assert rope_code(q, rows(5, 4, dtype=HF)) == INVALID
     assert rope_code(rows(5, 4, 128)[..., ::2], q) == INVALID           # elements apart
     assert rope_code(rows(4, 5).transpose(0, 1), q) == INVALID          # heads not side by side
+    assert rope_code(None, q, k, k) == INVALID                          # an output without its input
+    assert code_of(gdn.gdn_rope, gdn.make_attn_dims(4, 2, 64, 16),
+                   gdn.make_rope(64, torch.ones(32), i32(5)), None, None) == INVALID
 
 
 def append_args(**kw):

@@ -90,6 +90,24 @@ def test_rows_of_several_requests(D, Hq, Hkv):
     assert append(start, rows, kv, 200, 400, range(9), Hq=Hq, Hkv=Hkv, D=D) == 0
 
 
+@pytest.mark.parametrize("where", ["first", "last", "spread"])
+def test_rows_of_several_among_many_requests(where):
+    """Twenty of 300 requests on the same 300 rows: several times as many blocks as rows."""
+    rows = np.ones(300, int)
+    long = {"first": np.arange(20), "last": np.arange(280, 300),
+            "spread": np.arange(20) * 14 + 3}[where]
+    rows[long] = 300
+    start = np.full(300, 300)
+    start[long] = 0
+    short = np.setdiff1d(np.arange(300), long)
+    start[short] = 300 + np.arange(280)
+    kv = rows + np.arange(300) % 7
+    assert append(start, rows, kv, 580, 300, range(300), Hq=4, Hkv=2) == 0
+    kv[short[5]], kv[long[3]] = 0, 299  # and two bad ones among them
+    good = [r for r in range(300) if r not in (short[5], long[3])]
+    assert append(start, rows, kv, 580, 300, good, Hq=4, Hkv=2, width=6) == BAD_ROWS
+
+
 def test_no_rows_and_a_bad_length_is_reported():
     """A request without rows whose length is past its table, beside long and short ones."""
     start, rows, kv = packed([200] + [1] * 30 + [0])
