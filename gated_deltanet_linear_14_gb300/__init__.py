@@ -12,7 +12,8 @@ Entry points (same names as the C ABI): ``gdn_conv``, ``gdn_seq``,
 ``gdn_slot_layout``, ``gdn_check_bounded_wait``, ``gdn_strerror``,
 ``gdn_abi_version``; for the attention layers between GDN layers ``gdn_rope``,
 ``gdn_kv_append``, ``gdn_attn_plan``, ``gdn_attn``, ``gdn_attn_plan_bytes``,
-``gdn_attn_workspace_bytes``.
+``gdn_attn_workspace_bytes``; norms of queries and keys and an 8-bit cache for them
+``gdn_norm_rope``, ``gdn_kv8_append``, ``gdn_kv8_read``.
 """
 from __future__ import annotations
 
@@ -108,6 +109,18 @@ class KvBatch(ctypes.Structure):
                 ("group_pages", ctypes.c_void_p)]
 
 
+class HeadNorm(ctypes.Structure):
+    width = None  # of the narrower weight, where make_head_norm saw one
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("offset", ctypes.c_float)]
+
+
+class Kv8Codes(ctypes.Structure):
+    shape = None  # (pages, key heads, page size, head dim), where make_kv8_cache saw tensors
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p)]
+
+
 _lock = threading.Lock()
 _lib = None
 _raw_stream = None  # -> handle of the current stream
@@ -129,6 +142,7 @@ def load_library(path: str = LIB_PATH):
         D, B, PR = ctypes.POINTER(Dims), ctypes.POINTER(Batch), ctypes.POINTER(Params)
         AD, KB, RP = (ctypes.POINTER(AttnDims), ctypes.POINTER(KvBatch),
                       ctypes.POINTER(RopeParams))
+        HN, KC = ctypes.POINTER(HeadNorm), ctypes.POINTER(Kv8Codes)
         L = ctypes.c_int64
         sig = {
             "gdn_page_layout": ([D, ctypes.POINTER(PageLayout)], I),
@@ -152,6 +166,9 @@ def load_library(path: str = LIB_PATH):
             "gdn_attn_workspace_bytes": ([AD, KB], S),
             "gdn_attn_plan": ([AD, KB, P, S, P, P], I),
             "gdn_attn": ([AD, KB, P, P, L, P, P, P, P, P, S, P, P], I),
+            "gdn_norm_rope": ([AD, HN, RP, I, P, L, P, L, P, L, P, L, P], I),
+            "gdn_kv8_append": ([AD, KB, HN, RP, P, L, P, L, P, L, P, L, KC, P, P], I),
+            "gdn_kv8_read": ([AD, KB, KC, P, L, P, L, P, P], I),
             "gdn_strerror": ([I], ctypes.c_char_p),
             "gdn_abi_version": ([], I),
         }
@@ -508,6 +525,144 @@ def gdn_attn(dims, batch, plan, q, k_cache, v_cache, o, lse, workspace, workspac
         _ptr(status), _stream(stream))
     if code:
         raise GdnError(code, "gdn_attn")
+
+
+def make_head_norm(q_weight=None, k_weight=None, eps=1e-6, offset=0.0) -> HeadNorm:
+    """RMS norm of each head: x / sqrt(mean x^2 + eps) * (offset + weight); weights: device
+    float32 [D] or None. The structure keeps its tensors."""
+    width = None
+    for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is None or isinstance(w, int):
+            continue
+        import torch
+        if w.dtype is not torch.float32 or not w.is_contiguous():
+            _refuse(f"{what}: {w.dtype} strides {w.stride()} where float32 values side by side "
+                    "are read")
+        width = w.numel() if width is None else min(width, w.numel())
+    norm = HeadNorm(_ptr(q_weight), _ptr(k_weight), float(eps), float(offset))
+    norm.tensors, norm.width = (q_weight, k_weight), width
+    return norm
+
+
+def make_kv8_cache(k, v, k_exp, v_exp) -> Kv8Codes:
+    """A cache of 8-bit codes: k, v float8_e4m3fn or uint8 [pages][Hkv][page size][D], k_exp,
+    v_exp int8 [pages][Hkv][page size / 16]; device, contiguous (k or v may be None where only
+    the other is read). The structure keeps its tensors."""
+    shape = None
+    for codes, exps, what in ((k, k_exp, "k"), (v, v_exp, "v")):
+        if codes is None or isinstance(codes, int):
+            continue
+        import torch
+        if (codes.dtype not in (torch.float8_e4m3fn, torch.uint8) or codes.dim() != 4
+                or not codes.is_contiguous()):
+            _refuse(f"{what}: {codes.dtype} {tuple(codes.shape)} strides {codes.stride()} where "
+                    "dense codes [pages][heads][page size][D] are used")
+        pages, heads, ps, _ = codes.shape
+        if (exps is None or isinstance(exps, int) or exps.dtype is not torch.int8
+                or tuple(exps.shape) != (pages, heads, ps // 16) or not exps.is_contiguous()):
+            _refuse(f"{what}_exp: int8 [{pages}][{heads}][{ps // 16}], dense, goes with {what}")
+        if shape is not None and tuple(codes.shape) != shape:
+            _refuse(f"k {shape} and v {tuple(codes.shape)} differ")
+        shape = tuple(codes.shape)
+    cache = Kv8Codes(_ptr(k), _ptr(v), _ptr(k_exp), _ptr(v_exp))
+    cache.tensors, cache.shape = (k, v, k_exp, v_exp), shape
+    return cache
+
+
+def _kv8_fits(cache, hk, ps, dim, pages):
+    if cache is None:
+        _refuse("no cache")
+    shape = cache.shape
+    if shape is not None and (shape[0] < pages or shape[1:] != (hk, ps, dim)):
+        _refuse(f"cache {shape} where [{pages}][{hk}][{ps}][{dim}] is used")
+
+
+def _norm_fits(norm, dim):
+    if norm is not None and norm.width is not None and norm.width < dim:
+        _refuse(f"norm weights of {norm.width} elements for heads of {dim}")
+
+
+def gdn_norm_rope(dims, norm, rope, q, q_out, k=None, k_out=None, stream=None):
+    hq, hk, dim, _, io = _attn_dims(dims)
+    dtype = _types[io]
+    q_at = q_row = qo_at = qo_row = k_at = k_row = ko_at = ko_row = 0
+    if q is None and k is None:
+        _refuse("gdn_norm_rope: neither q nor k")
+    _norm_fits(norm, dim)
+    if q is not None:
+        rows, q_at, q_row = _rows(q, hq, dim, dtype)
+    if k is not None:
+        n, k_at, k_row = _rows(k, hk, dim, dtype)
+        if q is not None and n != rows:
+            _refuse(f"gdn_norm_rope: q has {rows} rows, k {n}")
+        rows = n
+    if q_out is not None:
+        n, qo_at, qo_row = _rows(q_out, hq, dim, dtype)
+        if n < rows:
+            _too_few("q_out", n, rows)
+    if k_out is not None:
+        n, ko_at, ko_row = _rows(k_out, hk, dim, dtype)
+        if n < rows:
+            _too_few("k_out", n, rows)
+    if rope is not None and rope.columns != rows:
+        _positions(rope, rows)
+    code = (_lib or load_library()).gdn_norm_rope(dims, norm, rope, rows, q_at, q_row, qo_at,
+                                                  qo_row, k_at, k_row, ko_at, ko_row,
+                                                  _stream(stream))
+    if code:
+        raise GdnError(code, "gdn_norm_rope")
+
+
+def gdn_kv8_append(dims, batch, norm, rope, q, k, v, q_out, cache, status, stream=None):
+    hq, hk, dim, ps, io = _attn_dims(dims)
+    _, rows, _, pages = _kv_counts(batch)
+    dtype = _types[io]
+    q_at = q_row = qo_at = qo_row = k_at = k_row = v_at = v_row = 0
+    _kv8_fits(cache, hk, ps, dim, pages)
+    _norm_fits(norm, dim)
+    if k is not None:
+        n, k_at, k_row = _rows(k, hk, dim, dtype)
+        if n < rows:
+            _too_few("k", n, rows)
+    if v is not None:
+        n, v_at, v_row = _rows(v, hk, dim, dtype)
+        if n < rows:
+            _too_few("v", n, rows)
+    if q is not None:
+        n, q_at, q_row = _rows(q, hq, dim, dtype)
+        if n < rows:
+            _too_few("q", n, rows)
+    if q_out is not None:
+        n, qo_at, qo_row = _rows(q_out, hq, dim, dtype)
+        if n < rows:
+            _too_few("q_out", n, rows)
+    if rope is not None and rope.columns != rows:
+        _positions(rope, rows)
+    code = (_lib or load_library()).gdn_kv8_append(
+        dims, batch, norm, rope, q_at, q_row, k_at, k_row, v_at, v_row, qo_at, qo_row, cache,
+        _ptr(status), _stream(stream))
+    if code:
+        raise GdnError(code, "gdn_kv8_append")
+
+
+def gdn_kv8_read(dims, batch, cache, k_out, v_out, status, stream=None):
+    hq, hk, dim, ps, io = _attn_dims(dims)
+    _, rows, _, pages = _kv_counts(batch)
+    dtype = _types[io]
+    k_at = k_row = v_at = v_row = 0
+    _kv8_fits(cache, hk, ps, dim, pages)
+    if k_out is not None:
+        n, k_at, k_row = _rows(k_out, hk, dim, dtype)
+        if n < rows:
+            _too_few("k_out", n, rows)
+    if v_out is not None:
+        n, v_at, v_row = _rows(v_out, hk, dim, dtype)
+        if n < rows:
+            _too_few("v_out", n, rows)
+    code = (_lib or load_library()).gdn_kv8_read(dims, batch, cache, k_at, k_row, v_at, v_row,
+                                                 _ptr(status), _stream(stream))
+    if code:
+        raise GdnError(code, "gdn_kv8_read")
 
 
 def gdn_check_bounded_wait(limit_ns, status, stream=None):

@@ -1,0 +1,144 @@
+// C ABI of the norms of queries and keys and of the 8-bit key/value cache:
+// host-side validation and launches. A negative return means nothing was launched
+// and nothing written.
+#include "attn_checks.h"
+#include "gdn.h"
+#include "kernels.h"
+#include "kv8.cuh"
+
+using namespace gdn;
+
+namespace {
+
+gdn_status check_norm(const gdn_head_norm* n) {
+  if (!n || !std::isfinite(n->eps) || n->eps < 0.0f || !std::isfinite(n->offset))
+    return GDN_ERR_INVALID_ARG;
+  return GDN_OK;
+}
+
+HeadNorm norm_args(const gdn_head_norm* n) {
+  return n ? HeadNorm{n->q_weight, n->k_weight, n->eps, n->offset, 1}
+           : HeadNorm{nullptr, nullptr, 0.0f, 0.0f, 0};
+}
+
+// The cache, k and v of it as asked for.
+gdn_status check_cache(const gdn_kv8_cache* c, bool k, bool v) {
+  if (!c || (k && (!c->k || !c->k_exp)) || (v && (!c->v || !c->v_exp))) return GDN_ERR_INVALID_ARG;
+  const uintptr_t at = (k ? (uintptr_t)c->k : 0) | (v ? (uintptr_t)c->v : 0);
+  return at & 15 ? GDN_ERR_UNSUPPORTED : GDN_OK;
+}
+
+Kv8Cache cache_args(const gdn_kv8_cache* c) {
+  return Kv8Cache{(uint8_t*)c->k, (uint8_t*)c->v, c->k_exp, c->v_exp};
+}
+
+// What the 8-bit cache calls take of the dims.
+gdn_status check_kv8_dims(const gdn_attn_dims* d) {
+  if (!d) return GDN_ERR_INVALID_ARG;
+  gdn_attn_dims x = *d;
+  if (x.io_dtype == GDN_F32) x.io_dtype = GDN_BF16;
+  return check_cache_dims(&x);
+}
+
+gdn_status launched(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH; }
+
+}  // namespace
+
+extern "C" {
+
+gdn_status gdn_norm_rope(const gdn_attn_dims* dims, const gdn_head_norm* norm,
+                         const gdn_rope_params* rope, int32_t num_rows, const void* q,
+                         int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k,
+                         int64_t k_stride, void* k_out, int64_t k_out_stride,
+                         gdn_stream_t stream) {
+  gdn_status e = check_attn_dims(dims);
+  if (e != GDN_OK || (e = check_norm(norm)) != GDN_OK) return e;
+  if (rope && (e = check_rope(rope, dims)) != GDN_OK) return e;
+  if (num_rows < 0) return GDN_ERR_INVALID_ARG;
+  if (dims->head_dim % 2 != 0 || dims->head_dim > kMaxRopeDim) return GDN_ERR_UNSUPPORTED;
+  if (num_rows == 0) return GDN_OK;
+  if ((!q != !q_out) || (!k != !k_out) || (!q && !k)) return GDN_ERR_INVALID_ARG;
+  const int D = dims->head_dim;
+  if ((q && (!stride_ok(q_stride, dims->num_q_heads, D) ||
+             !stride_ok(q_out_stride, dims->num_q_heads, D) ||
+             (q == q_out && q_stride != q_out_stride))) ||
+      (k && (!stride_ok(k_stride, dims->num_kv_heads, D) ||
+             !stride_ok(k_out_stride, dims->num_kv_heads, D) ||
+             (k == k_out && k_stride != k_out_stride))))
+    return GDN_ERR_INVALID_ARG;
+  RopeCall C{};
+  C.q = q, C.q_out = q_out, C.qs = q_stride, C.qos = q_out_stride;
+  C.k = k, C.k_out = k_out, C.ks = k_stride, C.kos = k_out_stride;
+  C.Hq = q ? dims->num_q_heads : 0;
+  C.Hkv = k ? dims->num_kv_heads : 0;
+  C.D = D;
+  C.num_rows = num_rows;
+  C.io = dims->io_dtype;
+  C.interleaved = rope ? rope->interleaved : 0;
+  const Rope P = rope_args(rope, num_rows, false);
+  C.vec = access_width(C, P.rd);
+  return launched(launch_norm_rope(C, P, norm_args(norm), (cudaStream_t)stream));
+}
+
+gdn_status gdn_kv8_append(const gdn_attn_dims* dims, const gdn_kv_batch* batch,
+                          const gdn_head_norm* norm, const gdn_rope_params* rope, const void* q,
+                          int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, void* q_out, int64_t q_out_stride,
+                          const gdn_kv8_cache* cache, int32_t* status, gdn_stream_t stream) {
+  gdn_status e = check_cache_dims(dims);
+  if (e != GDN_OK || (e = check_kv_batch(batch, false)) != GDN_OK) return e;
+  if (norm && (e = check_norm(norm)) != GDN_OK) return e;
+  if (rope && (e = check_rope(rope, dims)) != GDN_OK) return e;
+  if (rope && rope->rotary_dim % 16 != 0) return GDN_ERR_UNSUPPORTED;
+  if ((!norm && !rope && q) || (!q != !q_out)) return GDN_ERR_INVALID_ARG;
+  if (batch->num_requests == 0 || batch->max_rows == 0 || batch->num_rows == 0) return GDN_OK;
+  if (!k || !v || !status) return GDN_ERR_INVALID_ARG;
+  if ((e = check_cache(cache, true, true)) != GDN_OK) return e;
+  const int D = dims->head_dim;
+  if ((q && (!stride_ok(q_stride, dims->num_q_heads, D) ||
+             !stride_ok(q_out_stride, dims->num_q_heads, D) ||
+             (q == q_out && q_stride != q_out_stride))) ||
+      !stride_ok(k_stride, dims->num_kv_heads, D) || !stride_ok(v_stride, dims->num_kv_heads, D))
+    return GDN_ERR_INVALID_ARG;
+  RopeCall C{};
+  C.q = q, C.q_out = q_out, C.qs = q_stride, C.qos = q_out_stride;
+  C.k = k, C.ks = k_stride;
+  C.v = v, C.vs = v_stride;
+  C.Hq = q ? dims->num_q_heads : 0;
+  C.Hkv = dims->num_kv_heads;
+  C.D = D;
+  C.num_rows = batch->num_rows;
+  C.io = dims->io_dtype;
+  C.interleaved = rope ? rope->interleaved : 0;
+  const Rope P = rope_args(rope, batch->num_rows, false);
+  C.vec = access_width(C, P.rd);
+  return launched(launch_kv8_append(C, P, norm_args(norm), attn_dims(dims), kv_batch(batch),
+                                    cache_args(cache), status, (cudaStream_t)stream));
+}
+
+gdn_status gdn_kv8_read(const gdn_attn_dims* dims, const gdn_kv_batch* batch,
+                        const gdn_kv8_cache* cache, void* k_out, int64_t k_out_stride,
+                        void* v_out, int64_t v_out_stride, int32_t* status,
+                        gdn_stream_t stream) {
+  gdn_status e = check_kv8_dims(dims);
+  if (e != GDN_OK || (e = check_kv_batch(batch, false)) != GDN_OK) return e;
+  if (!k_out && !v_out) return GDN_ERR_INVALID_ARG;
+  if (batch->num_requests == 0 || batch->max_rows == 0 || batch->num_rows == 0) return GDN_OK;
+  if (!status) return GDN_ERR_INVALID_ARG;
+  if ((e = check_cache(cache, k_out, v_out)) != GDN_OK) return e;
+  const int D = dims->head_dim;
+  if ((k_out && !stride_ok(k_out_stride, dims->num_kv_heads, D)) ||
+      (v_out && !stride_ok(v_out_stride, dims->num_kv_heads, D)))
+    return GDN_ERR_INVALID_ARG;
+  RopeCall C{};
+  C.k_out = k_out, C.kos = k_out_stride;
+  C.v_out = v_out, C.vs = v_out_stride;
+  C.io = dims->io_dtype;
+  const uintptr_t at = (uintptr_t)k_out | (uintptr_t)v_out;
+  const int64_t strides = (k_out ? k_out_stride : 0) | (v_out ? v_out_stride : 0);
+  C.vec = (at & 15) == 0 && strides % (C.io == GDN_F32 ? 4 : 8) == 0 ? 8 : 1;
+  return launched(launch_kv8_read(C, attn_dims(dims), kv_batch(batch), cache_args(cache), status,
+                                  (cudaStream_t)stream));
+}
+
+}  // extern "C"

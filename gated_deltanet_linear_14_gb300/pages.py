@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (GDN_BF16, AttnDims, Dims, gdn_page_layout, gdn_slot_layout)
+from . import (GDN_BF16, AttnDims, Dims, gdn_page_layout, gdn_slot_layout, make_kv8_cache)
 
 _TORCH = {0: torch.float32, 1: torch.bfloat16, 2: torch.float16}
 
@@ -114,3 +114,26 @@ class KvCache:
         shape = (self.num_pages, dims.num_kv_heads, dims.page_size, dims.head_dim)
         self.k, self.v = (torch.empty(shape, dtype=torch_dtype(dims.io_dtype), device=device)
                           for _ in range(2))
+
+
+class Kv8Cache:
+    """A paged key/value cache in 8 bits: ``k`` and ``v`` codes, float8_e4m3fn
+    [num_pages][Hkv][page_size][D], ``k_exp`` and ``v_exp``, int8 [num_pages][Hkv][page_size / 16]
+    (a block of 16 tokens and head stands for code * 2^exp), and ``codes``, the structure that
+    the calls take. Slots that hold no token are never used, so the memory need not be cleared."""
+
+    def __init__(self, dims: AttnDims, num_pages: int, device="cuda"):
+        self.dims = dims
+        self.num_pages = int(num_pages)
+        shape = (self.num_pages, dims.num_kv_heads, dims.page_size, dims.head_dim)
+        self.k, self.v = (torch.empty(shape, dtype=torch.float8_e4m3fn, device=device)
+                          for _ in range(2))
+        self.k_exp, self.v_exp = (torch.empty(shape[:2] + (dims.page_size // 16,),
+                                              dtype=torch.int8, device=device) for _ in range(2))
+        self.codes = make_kv8_cache(self.k, self.v, self.k_exp, self.v_exp)
+
+    @staticmethod
+    def values(codes, exps):
+        """What codes and exponents (of these or fewer pages) stand for, in fp32."""
+        unit = torch.exp2(exps.float().clamp(-60, 60)).repeat_interleave(16, 2)
+        return codes.float() * unit[..., None]

@@ -17,7 +17,9 @@
  *
  * and, for the softmax-attention layers that hybrid stacks put between GDN
  * layers, rotary positions (gdn_rope), a paged key/value cache
- * (gdn_kv_append) and the attention over it (gdn_attn_plan, gdn_attn).
+ * (gdn_kv_append) and the attention over it (gdn_attn_plan, gdn_attn); the
+ * norms of queries and keys with the rotation (gdn_norm_rope), and the same
+ * cache in 8 bits (gdn_kv8_append, gdn_kv8_read).
  *
  * Sources (the method is described, not printed, on these pages):
  *   - r9700-stack v0.2.4 release notes, "What it does": one state page per
@@ -610,12 +612,91 @@ gdn_status gdn_attn(const gdn_attn_dims* dims, const gdn_kv_batch* batch, const 
                     void* o, float* lse, void* workspace, size_t workspace_bytes,
                     int32_t* status, gdn_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Norms of queries and keys, and a key/value cache held in 8 bits.
+ *
+ *   codes:   k, v [num_pages][Hkv][page_size][D], one byte each: 8-bit floating
+ *            point of 4 exponent and 3 mantissa bits (e4m3: largest value 448,
+ *            least 2^-9, codes 0x7F and 0xFF NaN, no infinity);
+ *   scales:  k_exp, v_exp [num_pages][Hkv][page_size / 16], int8: the block of 16
+ *            tokens b of a page and head stands for code * 2^exp. Exponents lie in
+ *            [-60, 60]; others count as the nearest of these.
+ * Half the bytes of a 16-bit cache. A power of two loses nothing against other
+ * scales (codes are floating point), and makes raising it exact for all codes but
+ * those that fall below 2^-6 2^exp.
+ * ------------------------------------------------------------------------- */
+
+#define GDN_KV8_BLOCK 16   /* tokens of a block with one scale */
+
+typedef struct {
+  void* k;                 /* device, 16-byte aligned codes                  */
+  void* v;
+  int8_t* k_exp;           /* device                                         */
+  int8_t* v_exp;
+} gdn_kv8_cache;
+
+/* RMS norm of each head's D elements: y = x / sqrt(mean x^2 + eps) * (offset + w). */
+typedef struct {
+  const float* q_weight;   /* device [D], or NULL: no weight (and no offset)  */
+  const float* k_weight;   /* device [D], or NULL                            */
+  float eps;               /* >= 0, finite                                   */
+  float offset;            /* 0, or 1 for weights that are kept around zero  */
+} gdn_head_norm;
+
+/* Norm query and key rows head by head, then rotate them as gdn_rope does
+ * (rope NULL: they are normed only), in one pass: fp32 throughout, rounded once.
+ * Arguments, types, alignments, in-place outputs and limits as gdn_rope; the mean
+ * of squares is formed in fp32 (of rows scaled down where the squares leave its
+ * range). A row that holds an infinite or NaN value gives NaN there and what the
+ * formula gives elsewhere (0 beside an infinite one, NaN beside a NaN). One launch
+ * on `stream`. */
+gdn_status gdn_norm_rope(const gdn_attn_dims* dims, const gdn_head_norm* norm,
+                         const gdn_rope_params* rope, int32_t num_rows, const void* q,
+                         int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k,
+                         int64_t k_stride, void* k_out, int64_t k_out_stride,
+                         gdn_stream_t stream);
+
+/* Append a step's rows to an 8-bit cache: row t of request r becomes token
+ * kv_len[r] - row_len[r] + t. k is normed (norm NULL: not) and rotated (rope NULL:
+ * not) and v is taken as it is; both are quantised from fp32, with one rounding.
+ * With q (else NULL, as q_out; needs norm or rope) the query rows are normed and
+ * rotated to q_out in the io dtype in the same launch.
+ *   exp   of a block: the least with max |x| <= 448 * 2^exp over the block's new
+ *         values (-60 for zeros). Where the request has older tokens in the block
+ *         (its first new token is not the block's first) the exponent never falls,
+ *         and if it rises, their codes are rounded anew to it.
+ *   code  x 2^-exp to nearest even. Infinite and NaN values become NaN and do not
+ *         count for exp; finite ones beyond 448 * 2^60 become that.
+ * Slots behind the request's last token keep what they hold. Batch, rows and
+ * device errors as gdn_kv_append (rows may belong to several requests; no page
+ * that is written may be shared), and a block whose page index is out of range is
+ * not written. D in {64, 128, 256}, page_size a power of two in [16, 256],
+ * rotary_dim a multiple of 16, io dtype bf16 or fp16. */
+gdn_status gdn_kv8_append(const gdn_attn_dims* dims, const gdn_kv_batch* batch,
+                          const gdn_head_norm* norm, const gdn_rope_params* rope, const void* q,
+                          int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, void* q_out, int64_t q_out_stride,
+                          const gdn_kv8_cache* cache, int32_t* status, gdn_stream_t stream);
+
+/* Read tokens of an 8-bit cache back as rows [num_rows][Hkv][D] of the io dtype
+ * (fp32, bf16 or fp16): row t of request r is token kv_len[r] - row_len[r] + t, so
+ * the batch of an append reads back what it wrote, and row_len = kv_len a whole
+ * history. k_out or v_out may be NULL. Values are exact in fp32 and bf16; in fp16
+ * they are rounded, and those beyond 65504 become it. Rows of no request are not
+ * written; device errors as gdn_kv_append (a row whose page index is out of range
+ * is not written). D in {64, 128, 256}, page_size as gdn_kv8_append. One launch. */
+gdn_status gdn_kv8_read(const gdn_attn_dims* dims, const gdn_kv_batch* batch,
+                        const gdn_kv8_cache* cache, void* k_out, int64_t k_out_stride,
+                        void* v_out, int64_t v_out_stride, int32_t* status,
+                        gdn_stream_t stream);
+
 /* Text for a status code (host, static storage). */
 const char* gdn_strerror(int32_t status);
 
 /* ABI version of this header: (major << 16) | minor. 2.2 added GDN_F16, the
  * attention-layer structures and gdn_rope, gdn_kv_append, gdn_attn_plan,
- * gdn_attn and their sizes. */
+ * gdn_attn and their sizes; 2.3 gdn_norm_rope, gdn_kv8_append, gdn_kv8_read
+ * and their structures. */
 int32_t gdn_abi_version(void);
 
 #ifdef __cplusplus

@@ -1,0 +1,316 @@
+"""The append to an 8-bit cache and reading it back, against 64-bit forms.
+
+A stored value is its value rounded once to the grid of its block: half a grid step, and before it
+what fp32 does to a key (2^-18 of its pair, see test_gpu_norm_rope.py). Values (v) see no arithmetic and
+are exact. A block's exponent is the least that holds its largest value; a key's block may come out
+one higher or lower only where its largest value is within 2^-18 of the limit."""
+import pytest
+import torch
+
+import gated_deltanet_linear_14_gb300 as gdn
+from gated_deltanet_linear_14_gb300.pages import Kv8Cache
+from tests.kv8_util import (BF, BLOCK, CODE, F32, HF, Blocks, Paged, grid_step, i32, least_exponent,
+                            normed, partners, rotated)
+
+pytestmark = pytest.mark.gpu
+
+
+def rows_for(P, t, seed=0, spread=1.0):
+    d, hq, hkv = P.dims.head_dim, P.dims.num_q_heads, P.dims.num_kv_heads
+    dtype = {v: k for k, v in CODE.items()}[P.dims.io_dtype]
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(t, hq + 2 * hkv, d, generator=g, device="cuda")
+    x = (x * torch.exp(spread * torch.randn(t, 1, 1, generator=g, device="cuda"))).to(dtype)
+    return x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("hq,hkv,d,rd,ps,axes,inter,norm_on,lens,befores", [
+    (4, 2, 128, 128, 16, 1, False, True, [1], [0]),
+    (4, 2, 128, 128, 64, 1, True, True, [1, 40, 3, 16], [7, 0, 30, 16]),
+    (16, 2, 256, 64, 32, 3, False, True, [5, 130, 1], [11, 16, 31]),
+    (2, 1, 64, 64, 256, 1, False, False, [33, 2, 300], [15, 250, 5]),
+    (8, 8, 64, 32, 16, 1, True, True, [17], [47]),
+    (6, 3, 256, 0, 128, 1, False, True, [20, 20], [1, 2])])
+def test_append_and_read(dtype, hq, hkv, d, rd, ps, axes, inter, norm_on, lens, befores):
+    R, most = len(lens), max(a + b for a, b in zip(lens, befores))
+    P = Paged(R, most, hq, hkv, d, ps, dtype, seed=d)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    qw, kw = (1 + 0.3 * torch.randn(d, generator=g, device="cuda") for _ in range(2))
+    inv = (1e4 ** -(torch.arange(max(rd // 2, 1), device="cuda").double() / max(rd // 2, 1))).float()
+    axis = (torch.arange(max(rd // 2, 1), device="cuda") % axes).int()
+    norm = gdn.make_head_norm(qw, kw, eps=1e-6, offset=0.5) if norm_on else None
+    kb, vb = ([Blocks(hkv, d) for _ in range(R)] for _ in range(2))
+    # what stands before, then the step itself
+    for turn, (n, at) in enumerate(((befores, [0] * R), (lens, befores))):
+        t = sum(n)
+        if t == 0:
+            continue
+        q, k, v = rows_for(P, t, seed=turn, spread=1.5 if turn else 0.5)
+        pos = torch.randint(0, 100000, (axes, t), generator=g, device="cuda", dtype=torch.int32)
+        rope = gdn.make_rope(rd, inv, pos, axis=axis, interleaved=inter)
+        start = [sum(n[:r]) for r in range(R)]
+        kv = [a + b for a, b in zip(n, at)]
+        batch = P.batch(start, n, kv, rows=t)
+        q_out = torch.full((t, hq, d), 7.0, device="cuda", dtype=dtype)
+        with_q = norm is not None or rd > 0
+        gdn.gdn_kv8_append(P.dims, batch, norm, rope, q if with_q else None, k, v,
+                           q_out if with_q else None, P.cache.codes, P.status)
+        gdn.raise_on_status(P.status)
+        y = normed(k, kw, 1e-6, 0.5) if norm_on else k.double()
+        turned = rotated(y, rd, inv, pos, axis, inter)
+        room = partners(y, rd, inter) * 2.0 ** -18 if norm_on or rd else 0 * y
+        if with_q:
+            yq = normed(q, qw, 1e-6, 0.5) if norm_on else q.double()
+            want = rotated(yq, rd, inv, pos, axis, inter)
+            half = torch.finfo(dtype).eps / 2
+            assert ((q_out.double() - want).abs() <= want.abs() * half * (1 + 2.0 ** -10)
+                    + partners(yq, rd, inter) * 2.0 ** -18 + 1e-7).all()
+        k_back, v_back = (torch.full((t, hkv, d), 7.0, device="cuda", dtype=dtype) for _ in range(2))
+        gdn.gdn_kv8_read(P.dims, batch, P.cache.codes, k_back, v_back, P.status)
+        for r in range(R):
+            a, b = start[r], start[r] + n[r]
+            if not n[r]:
+                continue
+            vb[r].append(v[a:b].double(), at[r])
+            x, e = P.tokens(r, kv[r], P.cache.v, P.cache.v_exp)
+            assert torch.equal(e, vb[r].e) and torch.equal(x, vb[r].x)
+            assert torch.equal(v_back[a:b].double(), x[at[r]:])
+            x, e = P.tokens(r, kv[r], P.cache.k, P.cache.k_exp)
+            assert torch.equal(k_back[a:b].double(), x[at[r]:])
+            kb[r].append(turned[a:b], at[r])
+            new, first = turned[a:b], at[r] // BLOCK
+            # exponents: equal, but for largest values next to a limit
+            off = e != kb[r].e
+            near = torch.zeros_like(off)
+            for bl in range(first, len(e)):
+                part = new[max(bl * BLOCK, at[r]) - at[r]:bl * BLOCK + BLOCK - at[r]]
+                top = part.abs().amax(-1).amax(0)
+                near[bl] = (least_exponent(top * (1 - 2.0 ** -18))
+                            != least_exponent(top * (1 + 2.0 ** -18)))
+            assert not (off & ~near).any()
+            unit = torch.exp2(e.double()).repeat_interleave(BLOCK, 0)[:kv[r], :, None]
+            miss = (x[at[r]:] - new).abs() - room[a:b]
+            assert (miss <= grid_step(new / unit[at[r]:]) / 2 * unit[at[r]:] * (1 + 1e-9)).all()
+            # older tokens: their stored values, rounded anew where the exponent grew
+            if at[r] and not off.any():
+                assert ((x[:at[r]] - kb[r].x[:at[r]]).abs()
+                        <= grid_step(kb[r].x[:at[r]] / unit[:at[r]]) * unit[:at[r]]).all()
+                same = torch.equal(x[:at[r] // BLOCK * BLOCK], kb[r].x[:at[r] // BLOCK * BLOCK]) \
+                    if not (norm_on or rd) else True
+                assert same
+            kb[r].x, kb[r].e = x.clone(), e.clone()   # go on from what is stored
+
+
+def test_tokens_one_by_one_as_all_at_once():
+    """Raising a block's power of two is exact but for values that fall below 2^-6 of it: those are
+    rounded twice, by at most half a step of 2^-9 each time."""
+    T, d = 70, 128
+    P, O = Paged(1, T, 2, 1, d, 32), Paged(1, T, 2, 1, d, 32)
+    _, k, v = rows_for(P, T, spread=2.0)
+    gdn.gdn_kv8_append(P.dims, P.batch([0], [T], [T]), None, None, None, k, v, None,
+                       P.cache.codes, P.status)
+    for t in range(T):
+        gdn.gdn_kv8_append(O.dims, O.batch([0], [1], [t + 1]), None, None, None, k[t:t + 1],
+                           v[t:t + 1], None, O.cache.codes, O.status)
+    gdn.raise_on_status(P.status)
+    gdn.raise_on_status(O.status)
+    for name in "kv":
+        (x, e), (y, f) = (S.tokens(0, T, getattr(S.cache, name), getattr(S.cache, name + "_exp"))
+                          for S in (P, O))
+        assert torch.equal(e, f)
+        unit = torch.exp2(e.double()).repeat_interleave(BLOCK, 0)[:T, :, None]
+        assert ((x - y).abs() <= 2.0 ** -9 * unit).all()
+        big = x.abs() >= 2.0 ** -6 * unit
+        assert torch.equal(x[big], y[big])
+
+
+def test_a_block_begun_anew_forgets_its_scale():
+    P = Paged(1, 32, 2, 1, 64, 16)
+    _, k, v = rows_for(P, 16)
+    for size in (1e6, 1e-6):
+        batch = P.batch([0], [16], [16])
+        gdn.gdn_kv8_append(P.dims, batch, None, None, None, (k * size).to(BF), (v * size).to(BF),
+                           None, P.cache.codes, P.status)
+        x, e = P.tokens(0, 16, P.cache.v, P.cache.v_exp)
+        want = (v * size).to(BF).double()
+        assert torch.equal(e, least_exponent(want.abs().amax(-1).amax(0))[None])
+        assert ((x - want).abs() <= want.abs().amax() * 2.0 ** -4).all()
+
+
+def test_infinite_nan_zero_and_far_values():
+    P = Paged(1, 64, 2, 1, 64, 64)
+    x = torch.ones(64, 1, 64, device="cuda", dtype=BF)
+    x[3, 0, 5], x[4, 0, 6], x[5, 0, 7] = float("inf"), float("-inf"), float("nan")
+    x[16:32] = 0.0
+    x[32:48] *= 1e30       # beyond 448 2^60
+    x[48:] *= 1e-30        # below 2^-69
+    gdn.gdn_kv8_append(P.dims, P.batch([0], [64], [64]), None, None, None, x, -x, None,
+                       P.cache.codes, P.status)
+    gdn.raise_on_status(P.status)
+    y, e = P.tokens(0, 64, P.cache.k, P.cache.k_exp)
+    assert e[:, 0].tolist() == [-8, -60, 60, -60]
+    bad = torch.zeros_like(y, dtype=torch.bool)
+    bad[3, 0, 5] = bad[4, 0, 6] = bad[5, 0, 7] = True
+    assert torch.equal(y.isnan(), bad) and (y[:16][~bad[:16]] == 1).all()
+    assert (y[16:32] == 0).all() and (y[32:48] == 448 * 2.0 ** 60).all() and (y[48:] == 0).all()
+    back = torch.empty(64, 1, 64, device="cuda", dtype=F32)
+    dims = gdn.make_attn_dims(2, 1, 64, 64, io=gdn.GDN_F32)
+    gdn.gdn_kv8_read(dims, P.batch([0], [64], [64]), P.cache.codes, None, back, P.status)
+    assert torch.equal(back.isnan(), bad) and torch.equal(back.double()[~bad], -y[~bad])
+    # fp16 holds no more than 65504
+    h, dims = torch.empty(64, 1, 64, device="cuda", dtype=HF), gdn.make_attn_dims(2, 1, 64, 64, io=gdn.GDN_F16)
+    gdn.gdn_kv8_read(dims, P.batch([0], [64], [64]), P.cache.codes, h, None, P.status)
+    assert torch.equal(h.isnan(), bad) and (h[32:48] == 65504).all()
+    # an infinite key in the norm: itself NaN, 0 beside it
+    gdn.gdn_kv8_append(P.dims, P.batch([0], [16], [16]), gdn.make_head_norm(eps=1e-6), None, None,
+                       x[:16], x[:16], None, P.cache.codes, P.status)
+    y, _ = P.tokens(0, 16, P.cache.k, P.cache.k_exp)
+    assert y[3, 0, 5].isnan() and (y[3, 0, 6:] == 0).all() and y[5].isnan().all()
+
+
+def test_read_whole_histories_into_strided_rows_of_every_type():
+    lens, d, hkv = [100, 1, 0, 37], 128, 3
+    P = Paged(4, 100, 3, hkv, d, 32)
+    _, k, v = rows_for(P, sum(lens))
+    start = [0, 100, 101, 101]
+    batch = P.batch(start, lens, lens)
+    gdn.gdn_kv8_append(P.dims, batch, None, None, None, k, v, None, P.cache.codes, P.status)
+    for dtype in (BF, HF, F32):
+        dims = gdn.make_attn_dims(3, hkv, d, 32, io=CODE[dtype])
+        for pad, shift in ((0, 0), (8, 0), (3, 1)):
+            gap = hkv * d + pad
+            store = torch.full((2, 140 * gap), 7.0, device="cuda", dtype=dtype)
+            outs = [torch.as_strided(s, (140, hkv, d), (gap, d, 1), s.storage_offset() + shift)
+                    for s in store[:, :].unbind(0)] if shift == 0 else \
+                   [torch.as_strided(s, (139, hkv, d), (gap, d, 1), s.storage_offset() + shift)
+                    for s in store.unbind(0)]
+            gdn.gdn_kv8_read(dims, batch, P.cache.codes, outs[0], outs[1], P.status)
+            gdn.raise_on_status(P.status)
+            for r in range(4):
+                if not lens[r]:
+                    continue
+                for out, name in zip(outs, "kv"):
+                    x, _ = P.tokens(r, lens[r], getattr(P.cache, name), getattr(P.cache, name + "_exp"))
+                    assert torch.equal(out[start[r]:start[r] + lens[r]], x.to(dtype))
+            assert (outs[0][138] == 7).all()   # rows of no request
+
+
+def test_slots_and_pages_of_others_keep_what_they_hold():
+    P = Paged(2, 40, 2, 1, 64, 16)
+    _, k, v = rows_for(P, 5)
+    before = P.cache.k.view(torch.uint8).clone(), P.cache.k_exp.clone()
+    gdn.gdn_kv8_append(P.dims, P.batch([0, 5], [5, 0], [25, 3]), None, None, None, k, v, None,
+                       P.cache.codes, P.status)
+    gdn.raise_on_status(P.status)
+    page = int(P.table[0, 1])   # tokens 20..24 are slots 4..8 of its second page
+    codes, exps = P.cache.k.view(torch.uint8).clone(), P.cache.k_exp.clone()
+    assert (codes[page, :, 9:] == before[0][page, :, 9:]).all()
+    codes[page], exps[page] = before[0][page], before[1][page]
+    assert torch.equal(codes, before[0]) and torch.equal(exps, before[1])
+
+
+def test_bad_requests_and_pages_are_skipped_and_reported():
+    P = Paged(4, 48, 2, 1, 64, 16, spare=0)
+    _, k, v = rows_for(P, 20)
+    P.table[1, 0] = 99
+    P.table[3, 1] = -1
+    # request 0: rows outside; 1: a bad first page; 2: longer than the table; 3: a bad second page
+    batch = P.batch([18, 0, 0, 0], [5, 5, 5, 20], [5, 5, 50, 20], rows=20)
+    back = torch.full((20, 1, 64), 7.0, device="cuda", dtype=BF)
+    gdn.gdn_kv8_append(P.dims, batch, None, None, None, k, v, None, P.cache.codes, P.status)
+    assert P.status.item() in (gdn.CODES["GDN_DEV_BAD_ROWS"], gdn.CODES["GDN_DEV_BAD_PAGE"])
+    P.status.zero_()
+    gdn.gdn_kv8_read(P.dims, batch, P.cache.codes, None, back, P.status)
+    assert P.status.item() in (gdn.CODES["GDN_DEV_BAD_ROWS"], gdn.CODES["GDN_DEV_BAD_PAGE"])
+    assert (back[16:] == 7).all() and not (back[:16] == 7).all(-1).any()
+    codes = P.cache.k.view(torch.uint8)
+    page = int(P.table[3, 0])
+    assert (codes[page] != 0x7F).all()
+    codes[page] = 0x7F
+    assert (codes == 0x7F).all()
+
+
+def test_several_requests_continue_with_the_same_rows():
+    """More rows than there are: every request gets them in its own pages, however the grid is made."""
+    R, T = 300, 40
+    P = Paged(R, T, 2, 1, 64, 16)
+    _, k, v = rows_for(P, T)
+    for lens in ([T] * R, [1] * (R - 1) + [T]):
+        batch = P.batch([0] * R, lens, lens, rows=T)
+        gdn.gdn_kv8_append(P.dims, batch, None, None, None, k, v, None, P.cache.codes, P.status)
+        gdn.raise_on_status(P.status)
+        for r in (0, 1, R // 2, R - 2, R - 1):
+            want = Blocks(1, 64)
+            want.append(v[:lens[r]].double(), 0)
+            x, _ = P.tokens(r, lens[r], P.cache.v, P.cache.v_exp)
+            assert torch.equal(x, want.x)
+
+
+@pytest.mark.parametrize("R,long", [(200, 3000), (1, 5000), (5000, 1)])
+def test_many_requests_beside_a_long_one(R, long):
+    lens = [1] * R
+    lens[R // 2] = long
+    P = Paged(R, long, 2, 1, 64, 256, spare=0) if R * long < 4e6 else None
+    start = [sum(lens[:r]) for r in range(R)] if R < 1000 else list(range(R))
+    _, k, v = rows_for(P, sum(lens))
+    batch = P.batch(start, lens, lens)
+    gdn.gdn_kv8_append(P.dims, batch, None, None, None, k, v, None, P.cache.codes, P.status)
+    back = torch.empty(sum(lens), 1, 64, device="cuda", dtype=BF)
+    gdn.gdn_kv8_read(P.dims, batch, P.cache.codes, None, back, P.status)
+    gdn.raise_on_status(P.status)
+    for r in (0, R // 2, R - 1):
+        want = Blocks(1, 64)
+        want.append(v[start[r]:start[r] + lens[r]].double(), 0)
+        assert torch.equal(back[start[r]:start[r] + lens[r]].double(), want.x)
+
+
+def test_pages_beyond_4_gib():
+    hkv, d, ps, pages = 8, 128, 256, 17000     # 4.46e9 bytes of keys
+    dims = gdn.make_attn_dims(8, hkv, d, ps)
+    cache = Kv8Cache(dims, pages)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x = torch.randn(300, hkv, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(0)).to(BF)
+    batch = gdn.make_kv_batch(1, 300, 300, pages, i32([0]), i32([300]), i32([300]),
+                              i32([pages - 1, 16500]).view(1, 2))
+    gdn.gdn_kv8_append(dims, batch, None, None, None, x, x, None, cache.codes, status)
+    back = torch.empty_like(x), torch.empty_like(x)
+    gdn.gdn_kv8_read(dims, batch, cache.codes, *back, status)
+    gdn.raise_on_status(status)
+    want = Blocks(hkv, d)
+    want.append(x.double(), 0)
+    assert torch.equal(back[0].double(), want.x) and torch.equal(back[1].double(), want.x)
+
+
+def test_captured_and_replayed_on_two_streams():
+    """Two captured steps on caches of their own, replayed at once."""
+    made = []
+    for seed in range(2):
+        P = Paged(8, 64, 4, 2, 128, 16, seed=seed)
+        _, k, v = rows_for(P, 8 * 20, seed=seed)
+        batch = P.batch(range(0, 160, 20), [20] * 8, [33] * 8)
+        back = torch.empty(160, 2, 128, device="cuda", dtype=BF)
+
+        def step(P=P, k=k, v=v, batch=batch, back=back):
+            gdn.gdn_kv8_append(P.dims, batch, None, None, None, k, v, None, P.cache.codes, P.status)
+            gdn.gdn_kv8_read(P.dims, batch, P.cache.codes, None, back, P.status)
+
+        P.cache.v_exp.fill_(-60)
+        P.cache.k_exp.fill_(-60)
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        k.copy_(k.flip(0)), v.copy_(v.flip(0))
+        made.append((P, v, back, graph, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _, _, _, graph, stream in made:
+        with torch.cuda.stream(stream):
+            graph.replay()
+    torch.cuda.synchronize()
+    for P, v, back, _, _ in made:
+        gdn.raise_on_status(P.status)
+        # (the first block of a request keeps the larger of its exponents)
+        assert ((back - v).abs().double() <= v.abs().amax().double() * 2.0 ** -4).all()
+        x, _ = P.tokens(3, 33, P.cache.v, P.cache.v_exp)
+        assert torch.equal(back[60:80].double(), x[13:])
