@@ -460,7 +460,8 @@ def run(s):
                                s["v"], s["q_out"], s["cache"], s["status"])
         gdn.gdn_kv8_read(s["dims"], s["back_batch"], s["cache"], s["k_back"], s["v_back"],
                          s["status"])
-        return (s["q_out"],) * (op == "append") + (s["k_back"], s["v_back"])
+        back = s["k_back"], s["v_back"]
+        return (s["q_out"],) + back if op == "append" else back
     if op == "norm":
         return (_normed_rotated(s, s["q"], s["qw"]).to(s["q"].dtype),
                 _normed_rotated(s, s["k"], s["kw"]).to(s["k"].dtype))
