@@ -13,7 +13,8 @@ Entry points (same names as the C ABI): ``gdn_conv``, ``gdn_seq``,
 ``gdn_abi_version``; for the attention layers between GDN layers ``gdn_rope``,
 ``gdn_kv_append``, ``gdn_attn_plan``, ``gdn_attn``, ``gdn_attn_plan_bytes``,
 ``gdn_attn_workspace_bytes``; norms of queries and keys and an 8-bit cache for them
-``gdn_norm_rope``, ``gdn_kv8_append``, ``gdn_kv8_read``.
+``gdn_norm_rope``, ``gdn_kv8_append``, ``gdn_kv8_read``, ``gdn_kv8_attn_plan``,
+``gdn_kv8_attn``, ``gdn_kv8_attn_plan_bytes``, ``gdn_kv8_attn_workspace_bytes``.
 """
 from __future__ import annotations
 
@@ -169,6 +170,10 @@ def load_library(path: str = LIB_PATH):
             "gdn_norm_rope": ([AD, HN, RP, I, P, L, P, L, P, L, P, L, P], I),
             "gdn_kv8_append": ([AD, KB, HN, RP, P, L, P, L, P, L, P, L, KC, P, P], I),
             "gdn_kv8_read": ([AD, KB, KC, P, L, P, L, P, P], I),
+            "gdn_kv8_attn_plan_bytes": ([AD, KB], S),
+            "gdn_kv8_attn_workspace_bytes": ([AD, KB], S),
+            "gdn_kv8_attn_plan": ([AD, KB, P, S, P, P], I),
+            "gdn_kv8_attn": ([AD, KB, P, P, L, KC, P, P, P, S, P, P], I),
             "gdn_strerror": ([I], ctypes.c_char_p),
             "gdn_abi_version": ([], I),
         }
@@ -663,6 +668,39 @@ def gdn_kv8_read(dims, batch, cache, k_out, v_out, status, stream=None):
                                                  _ptr(status), _stream(stream))
     if code:
         raise GdnError(code, "gdn_kv8_read")
+
+
+def gdn_kv8_attn_plan_bytes(dims, batch) -> int:
+    return int(load_library().gdn_kv8_attn_plan_bytes(ctypes.byref(dims), ctypes.byref(batch)))
+
+
+def gdn_kv8_attn_workspace_bytes(dims, batch) -> int:
+    return int(load_library().gdn_kv8_attn_workspace_bytes(ctypes.byref(dims),
+                                                           ctypes.byref(batch)))
+
+
+def gdn_kv8_attn_plan(dims, batch, plan, plan_bytes, status, stream=None):
+    _check(load_library().gdn_kv8_attn_plan(ctypes.byref(dims), ctypes.byref(batch), _ptr(plan),
+                                            int(plan_bytes), _ptr(status), _stream(stream)),
+           "gdn_kv8_attn_plan")
+
+
+def gdn_kv8_attn(dims, batch, plan, q, cache, o, lse, workspace, workspace_bytes, status,
+                 stream=None):
+    hq, hk, dim, ps, io = _attn_dims(dims)
+    _, rows, _, pages = _kv_counts(batch)
+    dtype, q_at, q_row = _types[io], 0, 0
+    _kv8_fits(cache, hk, ps, dim, pages)
+    if q is not None:
+        n, q_at, q_row = _rows(q, hq, dim, dtype)
+        if n < rows:
+            _too_few("q", n, rows)
+    code = (_lib or load_library()).gdn_kv8_attn(
+        dims, batch, _ptr(plan), q_at, q_row, cache, _dense(o, rows * hq * dim, dtype, "o"),
+        _dense(lse, rows * hq, _types[GDN_F32], "lse"), _ptr(workspace), int(workspace_bytes),
+        _ptr(status), _stream(stream))
+    if code:
+        raise GdnError(code, "gdn_kv8_attn")
 
 
 def gdn_check_bounded_wait(limit_ns, status, stream=None):

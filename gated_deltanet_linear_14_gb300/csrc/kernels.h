@@ -16,6 +16,11 @@ int device_sms();
 gdn_status encode_cache_tmap(void* tmap, const void* cache, int D, int tokens, int pages,
                              int box_tokens);
 
+// The same of a cache of 8-bit codes: boxes of min(D, 128) codes x box_tokens, swizzled over
+// the box's row (64 or 128 bytes). Implemented in api.cu.
+gdn_status encode_kv8_tmap(void* tmap, const void* codes, int D, int tokens, int pages,
+                           int box_tokens);
+
 cudaError_t launch_conv(const Geom& G, const Batch& B, const Params& P, int io_bf16, int y_f32,
                         const void* x, const void* w, void* y, void* pages, int32_t* status,
                         cudaStream_t stream);

@@ -1,7 +1,10 @@
 // C ABI of the norms of queries and keys and of the 8-bit key/value cache:
 // host-side validation and launches. A negative return means nothing was launched
 // and nothing written.
+#include <cuda.h>
+
 #include "attn_checks.h"
+#include "attn_plan.cuh"
 #include "gdn.h"
 #include "kernels.h"
 #include "kv8.cuh"
@@ -138,6 +141,51 @@ gdn_status gdn_kv8_read(const gdn_attn_dims* dims, const gdn_kv_batch* batch,
   const int64_t strides = (k_out ? k_out_stride : 0) | (v_out ? v_out_stride : 0);
   C.vec = (at & 15) == 0 && strides % (C.io == GDN_F32 ? 4 : 8) == 0 ? 8 : 1;
   return launched(launch_kv8_read(C, attn_dims(dims), kv_batch(batch), cache_args(cache), status,
+                                  (cudaStream_t)stream));
+}
+
+size_t gdn_kv8_attn_plan_bytes(const gdn_attn_dims* dims, const gdn_kv_batch* batch) {
+  if (check_attn(dims) != GDN_OK || check_kv_batch(batch, true) != GDN_OK) return 0;
+  return attn_layout(attn_dims(dims), kv_batch(batch)).bytes;
+}
+
+size_t gdn_kv8_attn_workspace_bytes(const gdn_attn_dims* dims, const gdn_kv_batch* batch) {
+  if (check_attn(dims) != GDN_OK || check_kv_batch(batch, true) != GDN_OK) return 0;
+  return attn_layout(attn_dims(dims), kv_batch(batch)).ws_bytes;
+}
+
+gdn_status gdn_kv8_attn_plan(const gdn_attn_dims* dims, const gdn_kv_batch* batch, void* plan,
+                             size_t plan_bytes, int32_t* status, gdn_stream_t stream) {
+  gdn_status e = check_attn(dims);
+  if (e != GDN_OK || (e = check_kv_batch(batch, true)) != GDN_OK) return e;
+  if (!plan || !status || ((uintptr_t)plan & 15) != 0) return GDN_ERR_INVALID_ARG;
+  if (plan_bytes < gdn_kv8_attn_plan_bytes(dims, batch)) return GDN_ERR_WORKSPACE;
+  return launched(launch_attn_plan(attn_dims(dims), kv_batch(batch), plan, status,
+                                   (cudaStream_t)stream));
+}
+
+gdn_status gdn_kv8_attn(const gdn_attn_dims* dims, const gdn_kv_batch* batch, const void* plan,
+                        const void* q, int64_t q_stride, const gdn_kv8_cache* cache, void* o,
+                        float* lse, void* workspace, size_t workspace_bytes, int32_t* status,
+                        gdn_stream_t stream) {
+  gdn_status e = check_attn(dims);
+  if (e != GDN_OK || (e = check_kv_batch(batch, true)) != GDN_OK) return e;
+  if (batch->num_requests == 0 || batch->max_rows == 0 || batch->num_rows == 0) return GDN_OK;
+  if (!plan || !q || !o || !workspace || !status) return GDN_ERR_INVALID_ARG;
+  if ((e = check_cache(cache, true, true)) != GDN_OK) return e;
+  if ((((uintptr_t)plan | (uintptr_t)workspace) & 15) != 0) return GDN_ERR_INVALID_ARG;
+  if (!stride_ok(q_stride, dims->num_q_heads, dims->head_dim)) return GDN_ERR_INVALID_ARG;
+  if ((((uintptr_t)q | (uintptr_t)o) & 15) != 0 || q_stride % 8 != 0) return GDN_ERR_UNSUPPORTED;
+  if (workspace_bytes < gdn_kv8_attn_workspace_bytes(dims, batch)) return GDN_ERR_WORKSPACE;
+  if (batch->num_pages == 0) return GDN_ERR_INVALID_ARG;
+  const AttnDims A = attn_dims(dims);
+  const int box = A.ps < kAttnKeys ? A.ps : kAttnKeys;
+  CUtensorMap tk, tv;
+  if ((e = encode_kv8_tmap(&tk, cache->k, A.D, A.Hkv * A.ps, batch->num_pages, box)) != GDN_OK ||
+      (e = encode_kv8_tmap(&tv, cache->v, A.D, A.Hkv * A.ps, batch->num_pages, box)) != GDN_OK)
+    return e;
+  return launched(launch_kv8_attn(&tk, &tv, A, kv_batch(batch), dims->io_dtype, plan, q, q_stride,
+                                  cache_args(cache), o, lse, workspace, status,
                                   (cudaStream_t)stream));
 }
 

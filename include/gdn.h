@@ -19,7 +19,7 @@
  * layers, rotary positions (gdn_rope), a paged key/value cache
  * (gdn_kv_append) and the attention over it (gdn_attn_plan, gdn_attn); the
  * norms of queries and keys with the rotation (gdn_norm_rope), and the same
- * cache in 8 bits (gdn_kv8_append, gdn_kv8_read).
+ * cache in 8 bits (gdn_kv8_append, gdn_kv8_read, gdn_kv8_attn).
  *
  * Sources (the method is described, not printed, on these pages):
  *   - r9700-stack v0.2.4 release notes, "What it does": one state page per
@@ -690,13 +690,31 @@ gdn_status gdn_kv8_read(const gdn_attn_dims* dims, const gdn_kv_batch* batch,
                         void* v_out, int64_t v_out_stride, int32_t* status,
                         gdn_stream_t stream);
 
+/* The plan, the workspace and the attention over an 8-bit cache: as gdn_attn_plan
+ * and gdn_attn (types, limits, groups, errors, what a row sees) with k and v as the
+ * codes stand for. The plan is this call's own. q is bf16 or fp16, as is o.
+ * Both products run on the 8-bit tensor cores, exact in the codes: q is cut into
+ * parts that together hold it (2 parts in bf16, 3 in fp16: within 2^-18 of the
+ * row's largest element), and so are the probabilities (within 2^-7 of each in
+ * bf16, 2^-10 in fp16, down to 2^-24 of the largest and beyond). Scores, softmax
+ * statistics and sums are fp32. A NaN code reaches only the rows that see it; an
+ * infinite or NaN query row is NaN throughout. */
+size_t gdn_kv8_attn_plan_bytes(const gdn_attn_dims* dims, const gdn_kv_batch* batch);
+size_t gdn_kv8_attn_workspace_bytes(const gdn_attn_dims* dims, const gdn_kv_batch* batch);
+gdn_status gdn_kv8_attn_plan(const gdn_attn_dims* dims, const gdn_kv_batch* batch, void* plan,
+                             size_t plan_bytes, int32_t* status, gdn_stream_t stream);
+gdn_status gdn_kv8_attn(const gdn_attn_dims* dims, const gdn_kv_batch* batch, const void* plan,
+                        const void* q, int64_t q_stride, const gdn_kv8_cache* cache, void* o,
+                        float* lse, void* workspace, size_t workspace_bytes, int32_t* status,
+                        gdn_stream_t stream);
+
 /* Text for a status code (host, static storage). */
 const char* gdn_strerror(int32_t status);
 
 /* ABI version of this header: (major << 16) | minor. 2.2 added GDN_F16, the
  * attention-layer structures and gdn_rope, gdn_kv_append, gdn_attn_plan,
- * gdn_attn and their sizes; 2.3 gdn_norm_rope, gdn_kv8_append, gdn_kv8_read
- * and their structures. */
+ * gdn_attn and their sizes; 2.3 gdn_norm_rope, gdn_kv8_append, gdn_kv8_read,
+ * gdn_kv8_attn, its plan and sizes, and their structures. */
 int32_t gdn_abi_version(void);
 
 #ifdef __cplusplus
