@@ -55,9 +55,16 @@ cudaError_t launch_kv8_append(const RopeCall& C, const Rope& P, const HeadNorm& 
 cudaError_t launch_kv8_read(const RopeCall& C, const AttnDims& A, const KvBatch& B,
                             const Kv8Cache& K, int32_t* status, cudaStream_t s);
 
+// The columns that kv8_decode.cu takes for a step of so few (row, query head) pairs per
+// key/value head and request, 0: kv8_attn.cu takes the step.
+int kv8_few_pairs(const AttnDims& A, const KvBatch& B);
 // tk, tv: CUtensorMaps of the codes ([pages][Hkv * page_size][D], boxes of min(D, 128)
 // codes x min(page_size, 64) tokens, swizzled over a box's row). The plan is
 // attn_plan.cu's.
+cudaError_t launch_kv8_few(const void* tk, const void* tv, const AttnDims& A, const KvBatch& B,
+                           int io, const void* plan, const void* q, long long qs,
+                           const Kv8Cache& K, void* o, float* lse, void* ws, int32_t* status,
+                           cudaStream_t s);
 cudaError_t launch_kv8_attn(const void* tk, const void* tv, const AttnDims& A, const KvBatch& B,
                             int io, const void* plan, const void* q, long long qs,
                             const Kv8Cache& K, void* o, float* lse, void* ws, int32_t* status,

@@ -94,7 +94,10 @@ def queries(P, t, dtype, seed=0, spread=0.0):
     (4, 2, 128, 64, [1, 1, 1], [63, 64, 65]), (4, 2, 64, 32, [1, 2, 3, 0, 5], [1, 17, 300, 4, 5]),
     (16, 2, 256, 64, [1, 8, 1], [1000, 130, 8]), (32, 8, 128, 16, [1] * 9, list(range(1, 1800, 200))),
     (8, 1, 128, 128, [40, 3], [40, 700]), (6, 2, 64, 256, [200, 1], [513, 129]),
-    (5, 5, 256, 16, [70], [257]), (128, 1, 64, 16, [2, 1], [33, 31]), (12, 3, 128, 32, [129], [129])])
+    (5, 5, 256, 16, [70], [257]), (128, 1, 64, 16, [2, 1], [33, 31]), (12, 3, 128, 32, [129], [129]),
+    (32, 8, 128, 256, [1, 1, 1], [20000, 777, 12345]), (8, 2, 64, 128, [8, 5, 8], [9000, 130, 8]),
+    (16, 2, 256, 128, [2, 4], [7000, 3001]), (16, 4, 128, 16, [8, 1, 3], [5000, 4097, 3]),
+    (3, 3, 256, 32, [32, 11], [4000, 32]), (16, 1, 64, 64, [1, 1], [40000, 64])])
 def test_against_64_bits(dtype, hq, hkv, d, ps, lens, kv):
     P = Paged(len(lens), max(kv), hq, hkv, d, ps, dtype, seed=d + ps)
     fill(P, seed=1)
@@ -187,7 +190,7 @@ def test_small_probabilities_that_make_up_a_part_together(dtype):
         check(P, q, o, lse, [0], [1], [n])
 
 
-@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("rows", [1, 8, 16, 40])
 def test_nan_codes_reach_only_the_rows_that_see_them(rows):
     """NaN in slots past the end, in a value and in a key inside the rows' own tile."""
     kv, d = 200, 128
