@@ -92,7 +92,6 @@ gdn_status gdn_kv8_append(const gdn_attn_dims* dims, const gdn_kv_batch* batch,
   if (e != GDN_OK || (e = check_kv_batch(batch, false)) != GDN_OK) return e;
   if (norm && (e = check_norm(norm)) != GDN_OK) return e;
   if (rope && (e = check_rope(rope, dims)) != GDN_OK) return e;
-  if (rope && rope->rotary_dim % 16 != 0) return GDN_ERR_UNSUPPORTED;
   if ((!norm && !rope && q) || (!q != !q_out)) return GDN_ERR_INVALID_ARG;
   if (batch->num_requests == 0 || batch->max_rows == 0 || batch->num_rows == 0) return GDN_OK;
   if (!k || !v || !status) return GDN_ERR_INVALID_ARG;
@@ -114,7 +113,7 @@ gdn_status gdn_kv8_append(const gdn_attn_dims* dims, const gdn_kv_batch* batch,
   C.io = dims->io_dtype;
   C.interleaved = rope ? rope->interleaved : 0;
   const Rope P = rope_args(rope, batch->num_rows, false);
-  C.vec = access_width(C, P.rd);
+  if (access_width(C, P.rd) != 8) return GDN_ERR_UNSUPPORTED;
   return launched(launch_kv8_append(C, P, norm_args(norm), attn_dims(dims), kv_batch(batch),
                                     cache_args(cache), status, (cudaStream_t)stream));
 }

@@ -1,12 +1,12 @@
 // The 8-bit key/value cache: quantising a step's rows as they are appended, with
 // the keys' norm and rotation on the way, and reading tokens back (sm_103a).
 //
-// Append. A block of 16 tokens and head is a warp's task: its new rows lie in
-// registers in the io type, half as many as their fp32 values would take, and
-// are normed and turned twice, for the largest value and for the codes. Blocks of
-// threads take the token blocks of the step one by one ("places"), all heads of
-// one, so that its cosines are formed once. Bound by memory: bytes of the rows,
-// the rotated queries and the codes. Reading back is a copy.
+// Append. Blocks of threads take the step's blocks of 16 tokens one by one
+// ("places"), some of them the queries of a place, some its keys, some its values. For
+// the queries a thread has 16 elements of one row and goes through the heads, what the
+// row's heads share (weights, cosines) in its registers. Of the keys and values a warp
+// has a head's block in registers, as it came. Bound by memory: bytes of the rows, the
+// rotated queries and the codes. Reading back is a copy.
 #include <algorithm>
 
 #include "angles.cuh"
@@ -15,7 +15,7 @@
 
 namespace gdn {
 
-constexpr int kKv8Threads = 128, kKv8Warps = kKv8Threads / 32;
+constexpr int kKv8Threads = 128;
 constexpr int kPackedMost = 4096;  // requests whose places a block adds up in shared memory
 
 // The places of all requests side by side: place x belongs to the request r with
@@ -52,7 +52,7 @@ __device__ __forceinline__ void add_places(int R, F count, long long* sum, long 
 template <class Count, class F>
 __device__ __forceinline__ void each_place(const KvBatch& B, bool packed, long long* sum,
                                            Count count, F f) {
-  __shared__ long long sm[kKv8Warps];
+  __shared__ long long sm[kKv8Threads / 32];
   if (!packed) {
     const int r = blockIdx.y;
     const long long n = count(r);
@@ -77,27 +77,30 @@ __device__ __forceinline__ void each_place(const KvBatch& B, bool packed, long l
 
 // ------------------------------------------------------------------ append
 
+enum { ROLE_Q = 0, ROLE_K = 1, ROLE_V = 2 };
+
 template <class T, int D, bool INTER>
 __global__ void __launch_bounds__(kKv8Threads, 4)
 kv8_append_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Rope R,
                   const __grid_constant__ HeadNorm N, const __grid_constant__ AttnDims A,
                   const __grid_constant__ KvBatch B, const __grid_constant__ Kv8Cache K,
-                  int packed, int32_t* status) {
-  // A row has U lanes of 16 elements, pairs together (see rope.cu); RPT rows a turn.
-  constexpr int U = D / 16, RPT = 32 / U, TURNS = kKv8Block / RPT;
+                  int packed, int zq, int zk, int32_t* status) {
+  constexpr int U = D / 16;  // lanes of a row, 16 elements each, pairs together (see rope.cu)
   typedef Vec<T, 8> Oct;
   extern __shared__ float4 kv8_smem[];
-  float* w_tab = reinterpret_cast<float*>(kv8_smem);             // [2][D]
-  float2* cs_tab = reinterpret_cast<float2*>(w_tab + 2 * D);     // [16][rd / 2]
-  long long* sum = reinterpret_cast<long long*>(cs_tab + 8 * R.rd);
+  float* w_tab = reinterpret_cast<float*>(kv8_smem);         // [D]
+  float *c_tab = w_tab + D, *s_tab = c_tab + 8 * R.rd;       // [16][rd / 2] each
+  long long* sum = reinterpret_cast<long long*>(s_tab + 8 * R.rd);
+  __shared__ uint32_t top_tab[kKv8Threads / 32];
   pdl_begin();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, half = R.rd >> 1;
-  const int u = lane % U, rr = lane / U, n_rot = R.rd / 16;
-  const bool rot = u < n_rot, wide = C.vec == 8;
+  const int z = blockIdx.z, role = z < zq ? ROLE_Q : z < zq + zk ? ROLE_K : ROLE_V;
+  const int part = role == ROLE_Q ? z : role == ROLE_K ? z - zq : z - zq - zk;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, half = R.rd >> 1, u = tid % U;
+  const bool rot = role != ROLE_V && u < R.rd / 16;
   const int ea = INTER || !rot ? 16 * u : 8 * u, eb = INTER || !rot ? 16 * u + 8 : half + 8 * u;
-  for (int x = tid; x < 2 * D; x += kKv8Threads)
-    w_tab[x] = x < D ? norm_weight(N.qw, x, N.offset) : norm_weight(N.kw, x - D, N.offset);
-  __syncthreads();
+  if (role != ROLE_V)
+    for (int x = tid; x < D; x += kKv8Threads)
+      w_tab[x] = norm_weight(role == ROLE_Q ? N.qw : N.kw, x, N.offset);
 
   auto count = [&](int r) -> long long {
     const int start = B.row_start[r], len = B.row_len[r], kv = B.kv_len[r];
@@ -107,164 +110,178 @@ kv8_append_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Ro
   each_place(B, packed, sum, count, [&](int r, long long place) {
     const int start = B.row_start[r], len = B.row_len[r], kv = B.kv_len[r];
     if (!kv_request_ok(B, A.ps, start, len, kv)) {
-      if (tid == 0 && blockIdx.z == 0) report(status, GDN_DEV_BAD_ROWS);
+      if (tid == 0 && z == 0) report(status, GDN_DEV_BAD_ROWS);
       return;
     }
     const int begin = kv - len;  // the first new token
     const int t0 = ((begin >> 4) + (int)place) << 4;
     const int lo = max(begin - t0, 0), hi = min(kv - t0, kKv8Block);  // new ones of the block
     const long long row0 = (long long)start + t0 - begin;              // of the block's token 0
-    int page = B.table[(size_t)r * B.max_pages + (t0 >> A.ps_log2)];
-    if (page < 0 || page >= B.num_pages) {
-      if (tid == 0 && blockIdx.z == 0) report(status, GDN_DEV_BAD_PAGE);
-      page = -1;
-    }
-    for (int x = tid; x < kKv8Block * half; x += kKv8Threads) {
-      const int i = x / half, j = x - i * half;
-      if (i < lo || i >= hi) continue;
-      int ax = R.axis ? R.axis[j] : 0;
-      if (ax < 0 || ax >= R.axes) ax = 0;
-      cs_tab[x] = cos_sin(R.pos[(size_t)ax * R.num_rows + row0 + i], R.inv_freq[j]);
-    }
-    __syncthreads();
+    const int page = B.table[(size_t)r * B.max_pages + (t0 >> A.ps_log2)];
+    const bool good = page >= 0 && page < B.num_pages;
+    if (!good && tid == 0 && z == 0) report(status, GDN_DEV_BAD_PAGE);
+    // (called when a thread's first rows are on their way)
+    auto angles = [&] {
+      for (int x = tid; x < kKv8Block * half; x += kKv8Threads) {
+        const int i = x / half, j = x - i * half;
+        if (i < lo || i >= hi) continue;
+        int ax = R.axis ? R.axis[j] : 0;
+        if (ax < 0 || ax >= R.axes) ax = 0;
+        const float2 cs = cos_sin(R.pos[(size_t)ax * R.num_rows + row0 + i], R.inv_freq[j]);
+        c_tab[x] = cs.x, s_tab[x] = cs.y;
+      }
+      __syncthreads();
+    };
 
-    const int first_turn = lo / RPT, last_turn = (hi - 1) / RPT;
-    for (int task = blockIdx.z * kKv8Warps + warp; task < C.Hq + 2 * C.Hkv;
-         task += gridDim.z * kKv8Warps) {
-      const bool is_q = task >= 2 * C.Hkv, is_k = task < C.Hkv;
-      const int h = is_q ? task - 2 * C.Hkv : is_k ? task : task - C.Hkv;
-      if (!is_q && page < 0) continue;
-      const long long step = is_q ? C.qs : is_k ? C.ks : C.vs;
-      const T* src = (const T*)(is_q ? C.q : is_k ? C.k : C.v) + row0 * step + h * D;
-      Oct a[TURNS], b[TURNS];
-      auto here = [&](int n) { return n * RPT + rr >= lo && n * RPT + rr < hi; };
-      const bool norm = N.on && (is_q || is_k), turned = rot && (is_q || is_k);
-      const int fa = turned ? ea : 16 * u, fb = turned ? eb : 16 * u + 8;
-#pragma unroll
-      for (int n = 0; n < TURNS; ++n) {
-        if (!here(n)) {
-          a[n].u = b[n].u = make_uint4(0, 0, 0, 0);
-          continue;
-        }
-        const T* p = src + (n * RPT + rr) * step;
-        if (wide) {
-          a[n].load(p + fa), b[n].load(p + fb);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) a[n].e[e] = p[fa + e], b[n].e[e] = p[fb + e];
-        }
-      }
-      // an older exponent is on its way meanwhile
-      const size_t head = (size_t)page * A.Hkv + h;
-      const size_t eat = head * (A.ps >> 4) + ((t0 & (A.ps - 1)) >> 4);
-      int8_t* exps = is_k ? K.k_exp : K.v_exp;
-      const int before = !is_q && lo > 0 ? kv8_clamp(exps[eat]) : -kKv8MaxExp;
-      float inv[TURNS];
-#pragma unroll
-      for (int n = 0; n < TURNS; ++n) {
-        inv[n] = 1.0f;
-        if (!norm || n < first_turn || n > last_turn) continue;
-        auto squares = [&](float scale) {
-          float s = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float x = elem_to_f(a[n].e[e]) * scale, y = elem_to_f(b[n].e[e]) * scale;
-            s += x * x + y * y;
-          }
-          return lanes_sum(s, U);
+    if (role == ROLE_Q) {
+      // Rows beside one another and heads beside those: as many rows at once as there
+      // are, up to a thread per unit; a thread keeps what its row's heads share.
+      int rows = 1;
+      while (rows < hi - lo && 2 * rows * U <= kKv8Threads) rows *= 2;
+      const int TY = kKv8Threads / (rows * U), step = TY * zq, ty = tid / (U * rows) + TY * part;
+      for (int i0 = lo; i0 < hi; i0 += rows) {
+        const int i = i0 + tid / U % rows;
+        const bool on_row = i < hi;
+        const T* src = (const T*)C.q + (row0 + i) * C.qs;
+        T* dst = (T*)C.q_out + (row0 + i) * C.qos;
+        constexpr int AHEAD = 1;  // heads that a lane has in flight
+        Oct a[AHEAD], b[AHEAD];
+        auto fetch = [&](int h, int n) {
+          if (!on_row || h >= C.Hq) return;
+          a[n].load(src + h * D + ea), b[n].load(src + h * D + eb);
         };
-        inv[n] = inv_rms(squares, D, N.eps);
+#pragma unroll
+        for (int n = 0; n < AHEAD; ++n) fetch(n * step + ty, n);
+        if (i0 == lo) angles();
+        UnitTurn<8, INTER> turn;
+        if (on_row)
+          turn.set(w_tab, ea, eb, rot ? c_tab + i * half + 8 * u : nullptr,
+                   s_tab + i * half + 8 * u);
+        for (int h0 = 0; h0 < C.Hq; h0 += AHEAD * step) {
+#pragma unroll
+          for (int n = 0; n < AHEAD; ++n) {
+            const int h = h0 + n * step + ty;
+            const bool on = on_row && h < C.Hq;
+            float inv = 1.0f;
+            if (N.on)
+              inv = inv_rms([&](float scale) {
+                const float s = unit_squares(a[n], b[n], scale);
+                return lanes_sum(on ? s : 0.0f, U);
+              }, D, N.eps);
+            if (!on) continue;
+            turn.apply(a[n], b[n], inv);
+            a[n].store(dst + h * D + ea), b[n].store(dst + h * D + eb);
+            fetch(h + AHEAD * step, n);
+          }
+        }
       }
-      // (formed anew in each pass: kept from one to the next, the fp32 values spill)
-      auto forget = [&] {
+      return;
+    }
+    if (!good) return;
+
+    // One warp, or two where D = 256, has the block's rows of a head, RPT a turn, all in
+    // flight at once, then their fp32 values up to the codes.
+    constexpr int RPT = 32 / U, SHARE = D == 256 ? 2 : 1, TURNS = kKv8Block / RPT / SHARE;
+    constexpr int HEADS = kKv8Threads / 32 / SHARE;  // of the block at once
+    const int r0 = warp % SHARE * (kKv8Block / SHARE) + lane / U, slot0 = t0 & (A.ps - 1);
+    const long long stride = role == ROLE_K ? C.ks : C.vs;
+    const T* base = (const T*)(role == ROLE_K ? C.k : C.v) + row0 * stride;
+    auto here = [&](int n) { return n * RPT + r0 >= lo && n * RPT + r0 < hi; };
+    for (int h0 = part * HEADS; h0 < C.Hkv; h0 += zk * HEADS) {
+      const int h = h0 + warp / SHARE;
+      const bool on = h < C.Hkv;
+      Oct a[TURNS], b[TURNS];
+#pragma unroll
+      for (int n = 0; n < TURNS; ++n) {
+        a[n].u = b[n].u = make_uint4(0, 0, 0, 0);
+        if (!on || !here(n)) continue;
+        const T* p = base + (n * RPT + r0) * stride + h * D;
+        a[n].load(p + ea), b[n].load(p + eb);
+      }
+      if (role == ROLE_K && h0 == part * HEADS) angles();
+      const size_t head = (size_t)page * A.Hkv + h;
+      int8_t* exp = (role == ROLE_K ? K.k_exp : K.v_exp) + head * (A.ps >> 4) + (slot0 >> 4);
+      uint8_t* codes = (role == ROLE_K ? K.k : K.v) + (head * A.ps + slot0) * D;
+      const int before = on && lo > 0 ? kv8_clamp(*exp) : -kKv8MaxExp;
+      float x[TURNS][16];
+#pragma unroll
+      for (int n = 0; n < TURNS; ++n) {
+        if (role == ROLE_K) {
+          float inv = 1.0f;
+          if (N.on)
+            inv = inv_rms([&](float scale) {
+              return lanes_sum(unit_squares(a[n], b[n], scale), U);
+            }, D, N.eps);
+          if (!here(n)) inv = 0.0f;
+          UnitTurn<8, INTER> turn;
+          const int at = min(n * RPT + r0, kKv8Block - 1) * half + 8 * u;
+          turn.set(w_tab, ea, eb, rot ? c_tab + at : nullptr, s_tab + at);
+          turn.values(a[n], b[n], inv, x[n]);
+          if (!here(n)) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[n][e] = 0.0f;
+          }
+        } else {
+          unpack(a[n], x[n]);
+          unpack(b[n], x[n] + 8);
+        }
+      }
+      // the largest size; an infinite value makes way for NaN, which counts for none and
+      // which the codes have
+      auto largest = [&] {
+        float most = 0.0f;
 #pragma unroll
         for (int n = 0; n < TURNS; ++n)
-          asm volatile("" : "+r"(a[n].u.x), "+r"(a[n].u.y), "+r"(a[n].u.z), "+r"(a[n].u.w),
-                            "+r"(b[n].u.x), "+r"(b[n].u.y), "+r"(b[n].u.z), "+r"(b[n].u.w));
+#pragma unroll
+          for (int e = 0; e < 16; e += 2)
+            most = fmaxf(fmaxf(most, fabsf(x[n][e])), fabsf(x[n][e + 1]));
+        return __reduce_max_sync(~0u, __float_as_uint(most));
       };
-      forget();
-      // the 16 values of a turn, normed and rotated
-      auto values = [&](int n, float* x) {
-        float* y = x + 8;
+      uint32_t top = largest();
+      if (top == 0x7F800000) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = elem_to_f(a[n].e[e]), y[e] = elem_to_f(b[n].e[e]);
-        if (norm) {
-          const float* w = w_tab + (is_q ? 0 : D);
+        for (int n = 0; n < TURNS; ++n)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= inv[n] * w[fa + e], y[e] *= inv[n] * w[fb + e];
-        }
-        if (turned) {
-          const float2* cs = cs_tab + (n * RPT + rr) * half + 8 * u;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if constexpr (INTER) turn(x[2 * e], x[2 * e + 1], cs[e]);
-            else turn(x[e], y[e], cs[e]);
-          }
-        }
-      };
-      if (is_q) {
-        T* dst = (T*)C.q_out + row0 * C.qos + h * D;
-#pragma unroll
-        for (int n = 0; n < TURNS; ++n) {
-          if (!here(n)) continue;
-          float x[16];
-          values(n, x);
-          Oct oa, ob;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) elem_from_f(x[e], oa.e[e]), elem_from_f(x[8 + e], ob.e[e]);
-          T* p = dst + (n * RPT + rr) * C.qos;
-          if (wide) {
-            oa.store(p + fa), ob.store(p + fb);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) p[fa + e] = oa.e[e], p[fb + e] = ob.e[e];
-          }
-        }
-        continue;
+          for (int e = 0; e < 16; ++e) x[n][e] = __fmaf_rn(x[n][e], 0.0f, x[n][e]);
+        top = largest();
       }
-      uint32_t top = 0;
+      if (SHARE > 1) {
+        if (lane == 0) top_tab[warp] = top;
+        __syncthreads();
+        top = max(top_tab[warp & ~1], top_tab[warp | 1]);
+        __syncthreads();
+      }
+      if (!on) continue;
+      const int e8 = max(kv8_exponent(top), before);
+      const float2 ss = make_float2(pow2(-e8), pow2(-e8));
 #pragma unroll
       for (int n = 0; n < TURNS; ++n) {
         if (!here(n)) continue;
-        float x[16];
-        values(n, x);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const uint32_t m = __float_as_uint(x[e]) & 0x7FFFFFFF;
-          if (m < 0x7F800000) top = max(top, m);
+        for (int e = 0; e < 16; e += 2) {
+          const float2 y = __fmul2_rn(make_float2(x[n][e], x[n][e + 1]), ss);
+          x[n][e] = y.x, x[n][e + 1] = y.y;
         }
+        uint8_t* p = codes + (n * RPT + r0) * D;
+        *reinterpret_cast<uint2*>(p + ea) = make_uint2(e4m3x4(x[n]), e4m3x4(x[n] + 4));
+        *reinterpret_cast<uint2*>(p + eb) = make_uint2(e4m3x4(x[n] + 8), e4m3x4(x[n] + 12));
       }
-      const int e8 = max(kv8_exponent(__reduce_max_sync(~0u, top)), before);
-      uint8_t* dst = (is_k ? K.k : K.v) + (head * A.ps + (t0 & (A.ps - 1))) * D;
       if (lo > 0 && e8 > before) {  // the older tokens' codes to the new scale
         const float down = pow2(before - e8);
-        for (int i = rr; i < lo; i += RPT) {
-          uint4* p = reinterpret_cast<uint4*>(dst + i * D) + u;
+        for (int i = r0; i < min(lo, (warp % SHARE + 1) * (kKv8Block / SHARE)); i += RPT) {
+          uint4* p = reinterpret_cast<uint4*>(codes + i * D) + u;
           uint4 c = *p;
           uint32_t* w = &c.x;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float2 x = from_e4m3x2((uint16_t)w[k]), y = from_e4m3x2((uint16_t)(w[k] >> 16));
-            w[k] = e4m3x2(x.x * down, x.y * down) | e4m3x2(y.x * down, y.y * down) << 16;
+            const float2 f = from_e4m3x2((uint16_t)w[k]), g = from_e4m3x2((uint16_t)(w[k] >> 16));
+            w[k] = e4m3x2(f.x * down, f.y * down) | e4m3x2(g.x * down, g.y * down) << 16;
           }
           *p = c;
         }
       }
-      if (lane == 0) exps[eat] = (int8_t)e8;
-      forget();
-      const float scale = pow2(-e8);
-#pragma unroll
-      for (int n = 0; n < TURNS; ++n) {
-        if (!here(n)) continue;
-        float x[16];
-        values(n, x);
-        // (an infinite value times 0 is NaN, which the codes have)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = __fmaf_rn(x[e], 0.0f, x[e]) * scale;
-        uint8_t* p = dst + (n * RPT + rr) * D;
-        *reinterpret_cast<uint2*>(p + fa) = make_uint2(e4m3x4(x), e4m3x4(x + 4));
-        *reinterpret_cast<uint2*>(p + fb) = make_uint2(e4m3x4(x + 8), e4m3x4(x + 12));
-      }
+      __syncwarp();
+      if (lane == 0 && warp % SHARE == 0) *exp = (int8_t)e8;
     }
   });
 }
@@ -376,29 +393,32 @@ cudaError_t launch_kv8_append(const RopeCall& C, const Rope& R, const HeadNorm& 
                               const AttnDims& A, const KvBatch& B, const Kv8Cache& K,
                               int32_t* status, cudaStream_t s) {
   const long long rows = std::min(B.max_rows, B.num_rows);
-  const Grid g = grid_for(B, (rows + 2 * kKv8Block - 2) / kKv8Block,
-                          B.num_rows / kKv8Block + 2LL * B.R,
-                          (C.Hq + 2 * C.Hkv + kKv8Warps - 1) / kKv8Warps);
-  const size_t smem = 8 * (size_t)C.D + 64 * (size_t)R.rd + g.sum_bytes;
-  auto run = [&](auto kernel, auto limit) {
-    const cudaError_t e = limit();
-    if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, g.dim, dim3(kKv8Threads), smem, s, C, R, N, A, B, K, g.packed,
-                      status);
-  };
-  // (at most 2 KB of weights, 16 KB of cosines and 32 KB of sums)
-  constexpr int kMost = 8 * 256 + 64 * 256 + 8 * (kPackedMost + 1);
-  auto by_dim = [&](auto t, auto inter) {
+  // blocks of their own for the queries, keys and values of a place, more of them where
+  // the places are few
+  const long long each = (rows + 2 * kKv8Block - 2) / kKv8Block;
+  Grid g = grid_for(B, each, B.num_rows / kKv8Block + 2LL * B.R,
+                    (C.D == 256 ? C.Hkv + 1 : C.Hkv + 3) / (C.D == 256 ? 2 : 4));
+  const int zk = g.dim.z;
+  const int most = (int)std::min<long long>(rows, kKv8Block) * (C.D / 16) * C.Hq / kKv8Threads;
+  const long long blocks = (long long)g.dim.x * g.dim.y;
+  int zq = C.Hq ? 1 : 0;
+  while (zq && 2 * zq <= most && 2 * zq * blocks <= 8LL * device_sms()) zq *= 2;
+  const size_t smem = 4 * (size_t)C.D + 64 * (size_t)R.rd + g.sum_bytes;
+  // (at most 1 KB of weights, 16 KB of cosines and 32 KB of sums)
+  constexpr int kMost = 4 * 256 + 64 * 256 + 8 * (kPackedMost + 1);
+  auto launch = [&](auto t, auto d, auto inter) {
     using T = decltype(t);
+    constexpr int D = decltype(d)::value;
     constexpr bool I = decltype(inter)::value;
-    if (A.D == 64)
-      return run(kv8_append_kernel<T, 64, I>,
-                 [] { return ensure_smem_limit<kv8_append_kernel<T, 64, I>>(kMost); });
-    if (A.D == 128)
-      return run(kv8_append_kernel<T, 128, I>,
-                 [] { return ensure_smem_limit<kv8_append_kernel<T, 128, I>>(kMost); });
-    return run(kv8_append_kernel<T, 256, I>,
-               [] { return ensure_smem_limit<kv8_append_kernel<T, 256, I>>(kMost); });
+    const cudaError_t e = ensure_smem_limit<kv8_append_kernel<T, D, I>>(kMost);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kv8_append_kernel<T, D, I>, dim3(g.dim.x, g.dim.y, zq + 2 * zk),
+                      dim3(kKv8Threads), smem, s, C, R, N, A, B, K, g.packed, zq, zk, status);
+  };
+  auto by_dim = [&](auto t, auto inter) {
+    if (A.D == 64) return launch(t, std::integral_constant<int, 64>(), inter);
+    if (A.D == 128) return launch(t, std::integral_constant<int, 128>(), inter);
+    return launch(t, std::integral_constant<int, 256>(), inter);
   };
   auto by_pairs = [&](auto t) {
     return C.interleaved ? by_dim(t, std::true_type()) : by_dim(t, std::false_type());

@@ -18,7 +18,11 @@ __device__ __forceinline__ float norm_weight(const float* w, int d, float offset
 
 // The sum over aligned groups of P lanes (P a power of two), in all of them.
 __device__ __forceinline__ float lanes_sum(float v, int P) {
-  for (int d = 1; d < P; d <<= 1) v += __shfl_xor_sync(~0u, v, d);
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    if (d >= P) break;
+    v += __shfl_xor_sync(~0u, v, d);
+  }
   return v;
 }
 
@@ -29,10 +33,10 @@ template <class F>
 __device__ __forceinline__ float inv_rms(F squares, int D, float eps) {
   const float ss = squares(1.0f), n = 1.0f / (float)D;
   const bool big = !(ss <= 3.0e38f), small = ss < 1.0e-26f && eps < 1.0e-20f;
-  float inv = 1.0f / sqrtf(ss * n + eps);
+  float inv = rsqrtf(ss * n + eps);  // (within 2^-22)
   if (__any_sync(~0u, big || small)) {
     const float scale = big ? 0x1p-70f : 0x1p70f;
-    const float again = scale / sqrtf(squares(scale) * n + eps * scale * scale);
+    const float again = scale * rsqrtf(squares(scale) * n + eps * scale * scale);
     if (big || small) inv = again;
   }
   return inv;
@@ -44,6 +48,128 @@ __device__ __forceinline__ void turn(float& x, float& y, float2 cs) {
   y = y * cs.x + x * cs.y;
   x = t;
 }
+
+template <class T, int VEC>
+__device__ __forceinline__ void unpack(const Vec<T, VEC>& v, float* x) {
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) x[e] = elem_to_f(v.e[e]);
+}
+
+// The sum of squares of a unit's elements times scale.
+template <class T, int VEC>
+__device__ __forceinline__ float unit_squares(const Vec<T, VEC>& a, const Vec<T, VEC>& b,
+                                              float scale) {
+  float v[2 * VEC];
+  unpack(a, v);
+  unpack(b, v + VEC);
+  float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int e = 0; e < 2 * VEC; e += 2) {
+    const float2 x = __fmul2_rn(make_float2(v[e], v[e + 1]), make_float2(scale, scale));
+    s = __ffma2_rn(x, x, s);
+  }
+  return s.x + s.y;
+}
+
+// VEC values rounded to T, two at a time where T has 16 bits.
+template <class T, int VEC>
+__device__ __forceinline__ void to_vec(const float* x, Vec<T, VEC>& v) {
+  if constexpr (sizeof(T) == 2 && VEC % 2 == 0) {
+    uint32_t w[VEC / 2];
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) w[e / 2] = pack2<T>(x[e], x[e + 1]);
+    if constexpr (VEC == 8) v.u = make_uint4(w[0], w[1], w[2], w[3]);
+    else v.u = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) elem_from_f(x[e], v.e[e]);
+  }
+}
+
+// What a lane does to its unit of a head, 2 VEC elements (v[0 .. VEC - 1] from ea on and
+// the rest from eb on; pairs are (e, VEC + e), interleaved ones (2 e, 2 e + 1)), weight
+// and turn in one: x' = (s x) xc - (s y) ys, y' = (s y) yc + (s x) xs with the row's scale
+// s. The same for all heads of a row that share a weight, so it stays in registers.
+template <int VEC, bool INTER>
+struct UnitTurn {
+  float xc[VEC], ys[VEC], yc[VEC], xs[VEC];
+  bool turns;  // where not, an infinite or NaN element leaves its neighbours alone
+  static __device__ __forceinline__ int x_of(int e) { return INTER && VEC > 1 ? 2 * e : e; }
+  static __device__ __forceinline__ int y_of(int e) { return INTER && VEC > 1 ? 2 * e + 1 : VEC + e; }
+  // c, s: the pairs' cosines and sines; c NULL: they do not turn (and s is not read)
+  __device__ __forceinline__ void set(const float* w, int ea, int eb, const float* c,
+                                      const float* s) {
+    turns = c != nullptr;
+    float ww[2 * VEC], cos[VEC], sin[VEC];
+    side_by_side(w + ea, ww), side_by_side(w + eb, ww + VEC);
+    if (turns) {
+      side_by_side(c, cos), side_by_side(s, sin);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) cos[e] = 1.0f, sin[e] = 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float wx = ww[x_of(e)], wy = ww[y_of(e)];
+      xc[e] = wx * cos[e], ys[e] = wy * sin[e], yc[e] = wy * cos[e], xs[e] = wx * sin[e];
+    }
+  }
+  // (units begin at multiples of VEC elements, as do the tables' rows)
+  static __device__ __forceinline__ void side_by_side(const float* p, float* x) {
+    if constexpr (VEC % 4 == 0) {
+#pragma unroll
+      for (int e = 0; e < VEC; e += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p + e);
+        x[e] = v.x, x[e + 1] = v.y, x[e + 2] = v.z, x[e + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[e] = p[e];
+    }
+  }
+  template <class T>
+  __device__ __forceinline__ void values(const Vec<T, VEC>& a, const Vec<T, VEC>& b, float scale,
+                                         float* v) const {
+    unpack(a, v);
+    unpack(b, v + VEC);
+    if constexpr (VEC % 2 == 0) {  // two pairs at a time
+      const float2 ss = make_float2(scale, scale);
+#pragma unroll
+      for (int e = 0; e < VEC; e += 2) {
+        float &x0 = v[x_of(e)], &x1 = v[x_of(e + 1)], &y0 = v[y_of(e)], &y1 = v[y_of(e + 1)];
+        const float2 x = __fmul2_rn(make_float2(x0, x1), ss), y = __fmul2_rn(make_float2(y0, y1), ss);
+        float2 xx = __fmul2_rn(x, make_float2(xc[e], xc[e + 1]));
+        float2 yy = __fmul2_rn(y, make_float2(yc[e], yc[e + 1]));
+        if (turns) {
+          xx = __ffma2_rn(y, make_float2(-ys[e], -ys[e + 1]), xx);
+          yy = __ffma2_rn(x, make_float2(xs[e], xs[e + 1]), yy);
+        }
+        x0 = xx.x, x1 = xx.y, y0 = yy.x, y1 = yy.y;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        float &x = v[x_of(e)], &y = v[y_of(e)];
+        x *= scale, y *= scale;
+        const float xx = x * xc[e], yy = y * yc[e];
+        if (turns) {
+          const float t = xx - y * ys[e];
+          y = yy + x * xs[e];
+          x = t;
+        } else {
+          x = xx, y = yy;
+        }
+      }
+    }
+  }
+  template <class T>
+  __device__ __forceinline__ void apply(Vec<T, VEC>& a, Vec<T, VEC>& b, float scale) const {
+    float v[2 * VEC];
+    values(a, b, scale, v);
+    to_vec(v, a);
+    to_vec(v + VEC, b);
+  }
+};
 
 cudaError_t launch_norm_rope(const RopeCall& C, const Rope& R, const HeadNorm& N, cudaStream_t s);
 

@@ -6,7 +6,7 @@
 // memory. The lanes of a head hold it in registers between the sum of its squares
 // (shuffles) and the rest, so that it is read once; cosines, sines and weights
 // lie in shared memory, formed once per block for all heads of its rows while the
-// first heads are in flight.
+// first heads are in flight, and go to registers for a thread's heads of a row.
 #include "angles.cuh"
 #include "attn.cuh"
 #include "kernels.h"
@@ -15,8 +15,8 @@
 namespace gdn {
 
 constexpr int kNormThreads = 128;
-constexpr int kNormBlocks = 8;  // per SM: 64 registers a thread
-constexpr int kNormHeads = 2;   // heads that a lane has in flight
+constexpr int kNormBlocks = 5;  // per SM: 102 registers a thread
+constexpr int kNormHeads = 3;   // heads that a lane has in flight
 
 // P lanes a head (a power of two), TY heads side by side, RB rows a block. A
 // lane's unit u: 2 VEC elements as two accesses, pairs together (see rope.cu). BIG:
@@ -26,9 +26,9 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks)
 norm_rope_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Rope R,
                  const __grid_constant__ HeadNorm N, int U, int P, int TY, int RB) {
   extern __shared__ float4 norm_smem[];
-  float2* cs_tab = reinterpret_cast<float2*>(norm_smem);  // [RB][rd / 2], then the weights
+  float* c_tab = reinterpret_cast<float*>(norm_smem);  // [RB][rd / 2], and the sines, then the weights
   const int half = R.rd >> 1, tid = threadIdx.x, D = C.D, H = C.Hq + C.Hkv;
-  float* w_tab = reinterpret_cast<float*>(norm_smem) + ((RB * R.rd + 3) & ~3);  // [2][D]
+  float *s_tab = c_tab + RB * half, *w_tab = c_tab + ((RB * R.rd + 3) & ~3);  // [2][D]
   pdl_begin();
   const int lane_u = tid % P, ty = tid / P % TY, row = tid / (P * TY);
   const long long gr = (long long)blockIdx.x * RB + row;
@@ -44,16 +44,15 @@ norm_rope_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Rop
   auto dst_of = [&](int h) { return h < C.Hq ? qdst + h * D : kdst + (h - C.Hq) * D; };
 
   Vec<T, VEC> a[kNormHeads], b[kNormHeads];
-  auto fetch = [&](int h0) {
-#pragma unroll
-    for (int n = 0; n < kNormHeads; ++n) {
-      const int h = h0 + n * TY + ty;
-      if (!here || h >= H || lane_u >= U) continue;
-      a[n].load(src_of(h) + first(lane_u));
-      b[n].load(src_of(h) + second(lane_u));
-    }
+  auto fetch = [&](int h, int n) {
+    if (!here || h >= H || lane_u >= U) return;
+    a[n].load(src_of(h) + first(lane_u));
+    b[n].load(src_of(h) + second(lane_u));
   };
-  if (!BIG) fetch(0);
+  if (!BIG) {
+#pragma unroll
+    for (int n = 0; n < kNormHeads; ++n) fetch(n * TY + ty, n);
+  }
   for (int x = tid; x < 2 * D; x += kNormThreads)
     w_tab[x] = x < D ? norm_weight(N.qw, x, N.offset) : norm_weight(N.kw, x - D, N.offset);
   const long long row0 = (long long)blockIdx.x * RB;
@@ -62,41 +61,19 @@ norm_rope_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Rop
     if (row0 + xr >= C.num_rows) break;
     int ax = R.axis ? R.axis[j] : 0;
     if (ax < 0 || ax >= R.axes) ax = 0;
-    cs_tab[x] = cos_sin(R.pos[(size_t)ax * R.num_rows + row0 + xr], R.inv_freq[j]);
+    const float2 cs = cos_sin(R.pos[(size_t)ax * R.num_rows + row0 + xr], R.inv_freq[j]);
+    c_tab[x] = cs.x, s_tab[x] = cs.y;
   }
   __syncthreads();
 
-  // one unit of a head: scaled, weighted, turned and stored
-  auto finish = [&](int h, int u, const Vec<T, VEC>& va, const Vec<T, VEC>& vb, float inv) {
-    const float* w = w_tab + (h < C.Hq ? 0 : D);
-    const int ea = first(u), eb = second(u);
-    float x[VEC], y[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      x[e] = elem_to_f(va.e[e]) * inv * w[ea + e];
-      y[e] = elem_to_f(vb.e[e]) * inv * w[eb + e];
-    }
-    if (u < n_rot) {
-      const float2* cs = cs_tab + row * half + VEC * u;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        if constexpr (INTER && VEC > 1) {
-          float* z = 2 * e < VEC ? x : y;
-          const int f = 2 * e < VEC ? 2 * e : 2 * e - VEC;
-          turn(z[f], z[f + 1], cs[e]);
-        } else {
-          turn(x[e], y[e], cs[e]);
-        }
-      }
-    }
-    Vec<T, VEC> oa, ob;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) elem_from_f(x[e], oa.e[e]), elem_from_f(y[e], ob.e[e]);
-    T* dst = dst_of(h);
-    oa.store(dst + ea);
-    ob.store(dst + eb);
+  UnitTurn<VEC, INTER> turn;
+  bool for_k = false;
+  auto turn_for = [&](int h, int u) {
+    for_k = h >= C.Hq;
+    turn.set(w_tab + (for_k ? D : 0), first(u), second(u),
+             u < n_rot ? c_tab + row * half + VEC * u : nullptr, s_tab + row * half + VEC * u);
   };
-
+  if (!BIG && lane_u < U) turn_for(ty, lane_u);
   for (int h0 = 0; h0 < H; h0 += TY * kNormHeads) {
     if constexpr (!BIG) {
 #pragma unroll
@@ -104,18 +81,18 @@ norm_rope_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Rop
         const int h = h0 + n * TY + ty;
         const bool on = here && h < H && lane_u < U;
         auto squares = [&](float scale) {
-          float s = 0.0f;
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float x = elem_to_f(a[n].e[e]) * scale, y = elem_to_f(b[n].e[e]) * scale;
-            s += x * x + y * y;
-          }
+          const float s = unit_squares(a[n], b[n], scale);  // (no branch: heads overlap)
           return lanes_sum(on ? s : 0.0f, P);
         };
         const float inv = inv_rms(squares, D, N.eps);
-        if (on) finish(h, lane_u, a[n], b[n], inv);
+        if (!on) continue;
+        if (h >= C.Hq && !for_k) turn_for(h, lane_u);
+        turn.apply(a[n], b[n], inv);
+        T* dst = dst_of(h);
+        a[n].store(dst + first(lane_u));
+        b[n].store(dst + second(lane_u));
+        fetch(h + TY * kNormHeads, n);
       }
-      if (h0 + TY * kNormHeads < H) fetch(h0 + TY * kNormHeads);
     } else {
       for (int n = 0; n < kNormHeads; ++n) {
         const int h = h0 + n * TY + ty;
@@ -126,11 +103,7 @@ norm_rope_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Rop
             Vec<T, VEC> va, vb;
             va.load(src_of(h) + first(u));
             vb.load(src_of(h) + second(u));
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              const float x = elem_to_f(va.e[e]) * scale, y = elem_to_f(vb.e[e]) * scale;
-              s += x * x + y * y;
-            }
+            s += unit_squares(va, vb, scale);
           }
           return lanes_sum(s, P);
         };
@@ -139,7 +112,10 @@ norm_rope_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Rop
           Vec<T, VEC> va, vb;
           va.load(src_of(h) + first(u));
           vb.load(src_of(h) + second(u));
-          finish(h, u, va, vb, inv);
+          turn_for(h, u);
+          turn.apply(va, vb, inv);
+          va.store(dst_of(h) + first(u));
+          vb.store(dst_of(h) + second(u));
         }
       }
     }
@@ -153,11 +129,13 @@ cudaError_t go(const RopeCall& C, const Rope& R, const HeadNorm& N, cudaStream_t
   const int U = C.D / (2 * VEC), H = C.Hq + C.Hkv;
   int P = 1;
   while (P < U && P < 32) P *= 2;
-  // heads side by side as in rope.cu
+  // Threads over the heads of a row: more than ten heads each (what a row's heads share
+  // costs as much as two of them), more threads where the rows are too few to fill the
+  // SMs.
   const long long full = (long long)device_sms() * kNormBlocks * kNormThreads;
   int TY = 1;
   while (2 * TY <= H && 2 * TY * P <= kNormThreads &&
-         (H > 8 * TY || (long long)C.num_rows * P * TY < full))
+         (H > 24 * TY || (long long)C.num_rows * P * TY < full))
     TY *= 2;
   const int RB = kNormThreads / (P * TY);
   const size_t smem = 4 * (((size_t)RB * R.rd + 3) / 4 * 4 + 2 * (size_t)C.D);

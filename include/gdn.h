@@ -671,7 +671,8 @@ gdn_status gdn_norm_rope(const gdn_attn_dims* dims, const gdn_head_norm* norm,
  * device errors as gdn_kv_append (rows may belong to several requests; no page
  * that is written may be shared), and a block whose page index is out of range is
  * not written. D in {64, 128, 256}, page_size a power of two in [16, 256],
- * rotary_dim a multiple of 16, io dtype bf16 or fp16. */
+ * rotary_dim a multiple of 16, io dtype bf16 or fp16, rows 16-byte aligned (addresses,
+ * and strides multiples of 8), else GDN_ERR_UNSUPPORTED. */
 gdn_status gdn_kv8_append(const gdn_attn_dims* dims, const gdn_kv_batch* batch,
                           const gdn_head_norm* norm, const gdn_rope_params* rope, const void* q,
                           int64_t q_stride, const void* k, int64_t k_stride, const void* v,

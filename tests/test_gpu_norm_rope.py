@@ -108,6 +108,7 @@ def test_zero_infinite_and_nan_rows():
     gdn.gdn_norm_rope(dims, gdn.make_head_norm(eps=1e-6), None, q, out)
     assert (out[0] == 0).all() and (out[3] == 1).all()
     assert out[1, 0, 3].isnan() and (out[1, 0, :3] == 0).all() and (out[1, 1] == 1).all()
+    assert (out[1, 0, 4:] == 0).all()
     assert out[2, 1].isnan().all() and (out[2, 0] == 1).all()
 
 
