@@ -48,7 +48,8 @@ struct Cfg8 {
   static_assert(TM_O + D <= TM_COLS, "tensor memory columns");
   static constexpr uint32_t RING = NQ * QPART;
   static constexpr uint32_t EXPS = RING + NS * UNIT;
-  static constexpr uint32_t BARS = EXPS + kExpSlots * 8;
+  static constexpr uint32_t FACTORS = EXPS + kExpSlots * 8;  // of an item's rows and the next one's
+  static constexpr uint32_t BARS = FACTORS + 2 * kAttnM * 4;
   static constexpr uint32_t BYTES = BARS + 8 * (2 * NS + 1 + 3 * NSB + kExpSlots) + 32;
   static_assert(BYTES <= (CTAS == 2 ? 115712 : 232448), "shared memory");
   static_assert(NS / 2 + NSB + 2 <= kExpSlots, "exponents are read before they are replaced");
@@ -70,6 +71,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ 
   const uint32_t s_full = q_full + 8, p_ready = s_full + 8 * NSB, o_full = p_ready + 8 * NSB;
   const uint32_t e_full = o_full + 8 * NSB;
   uint8_t* exps = smem + C::EXPS;
+  float* factors = reinterpret_cast<float*>(smem + C::FACTORS);
   // [0] tensor memory, [1] a role gave up, [2..4] see `strange`
   volatile uint32_t* words = reinterpret_cast<uint32_t*>(
       smem + C::BARS + 8 * (2 * NS + 1 + 3 * NSB + kExpSlots));
@@ -304,15 +306,18 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ 
       return (x & 1) * C::QPART + g / (C::PITCH / 16) * C::QCHUNK +
              swizzled<C::PITCH>(r, g % (C::PITCH / 16));
     };
+    // A tile's rows are dealt to all threads: 4, 2 or 1 (1 << spread) of them have a row.
+    auto spread_of = [](const Walk& V) { return V.it.m_cnt <= 32 ? 2 : V.it.m_cnt <= 64 ? 1 : 0; };
     // start copying an item's Q to shared memory, each warp the rows that its own
     // threads cut into parts
     auto fetch_q = [&](const Walk& V) {
-      const int n = min(32, V.it.m_cnt - 32 * warp);
+      const int rows = 32 >> spread_of(V), r_from = rows * warp;
+      const int n = min(rows, V.it.m_cnt - r_from);
       if (n <= 0) return;
       // 16-byte pieces of a row, rows at once
       constexpr int CH = D / 8, RPI = CH < 32 ? 32 / CH : 1;
       int i, hq;
-      const long long row = pair_of(V.it, V.head, tid, i, hq);
+      const long long row = pair_of(V.it, V.head, r_from + lane, i, hq);
       const unsigned long long src = (unsigned long long)(q + row * qs + (long long)hq * D);
       const int ch = lane % CH;
 #pragma unroll 4
@@ -321,40 +326,47 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ 
         const unsigned long long from = __shfl_sync(~0u, src, r & 31) + ch * 16;
         if (r < n)
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                           sb + q_at(32 * warp + r, ch)),
+                           sb + q_at(r_from + r, ch)),
                        "l"(from)
                        : "memory");
       }
     };
-    // ... and wait for it, and cut this thread's row into its parts. Returns the
-    // factor of the row's scores: c2 times the power of two that it was divided by.
-    auto publish_q = [&](const Walk& V) {
+    // ... and wait for it, and cut the rows into their parts. The factor of a row's
+    // scores, c2 times the power of two that it was divided by, goes to a table.
+    auto publish_q = [&](const Walk& V, uint32_t item) {
       asm volatile("cp.async.wait_all;" ::: "memory");
       __syncwarp();
-      float factor = 0.0f;
-      if (V.it.m_cnt > warp * 32) {
-        const int r = min(tid, V.it.m_cnt - 1);
+      const int spread = spread_of(V), step = 1 << spread, r = tid >> spread;
+      if (V.it.m_cnt > (warp * 32 >> spread)) {
+        const bool on = r < V.it.m_cnt;
+        const int from = tid & (step - 1);  // groups of 16 elements: from, from + step, ..
         uint32_t top = 0;
-#pragma unroll 4
-        for (int x = 0; x < D / 8; ++x) {
-          const uint4 v = *reinterpret_cast<const uint4*>(smem + q_at(r, x));
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if (on) {
+#pragma unroll 2
+          for (int g = from; g < D / 16; g += step) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            top = max(top, max(w[e] & 0x7FFF, w[e] >> 16 & 0x7FFF));
+            for (int x = 0; x < 2; ++x) {
+              const uint4 v = *reinterpret_cast<const uint4*>(smem + q_at(r, 2 * g + x));
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) top = __vmaxu2(top, w[e] & 0x7FFF7FFFu);
+            }
           }
+          top = max(top & 0xFFFF, top >> 16);
         }
+        if (spread > 0) top = max(top, __shfl_xor_sync(~0u, top, 1));
+        if (spread > 1) top = max(top, __shfl_xor_sync(~0u, top, 2));
         const uint16_t top16 = (uint16_t)top;
         const float amax = elem_to_f(*reinterpret_cast<const T*>(&top16));
         const bool bad = !(amax < INFINITY);
         const int ex = max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -100);
         const float down = bad ? __int_as_float(0x7FFFFFFF) : pow2(-ex);
-        factor = c2 * pow2(bad ? 0 : ex);
-        if (tid < V.it.m_cnt) {
-#pragma unroll 2
-          for (int g = 0; g < D / 16; ++g) {
-            uint4* at0 = reinterpret_cast<uint4*>(smem + q_at(tid, 2 * g));
-            uint4* at1 = reinterpret_cast<uint4*>(smem + q_at(tid, 2 * g + 1));
+        if (on) {
+          if (from == 0) factors[(item & 1) * kAttnM + r] = c2 * pow2(bad ? 0 : ex);
+#pragma unroll 1
+          for (int g = from; g < D / 16; g += step) {
+            uint4* at0 = reinterpret_cast<uint4*>(smem + q_at(r, 2 * g));
+            uint4* at1 = reinterpret_cast<uint4*>(smem + q_at(r, 2 * g + 1));
             Vec<T, 8> a, c;
             a.u = *at0, c.u = *at1;
             float x[16];
@@ -376,7 +388,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ 
               const uint4 part = make_uint4(w[0], w[1], w[2], w[3]);
               if (n == 0) *at0 = part;
               else if (n == 1) *at1 = part;
-              else *reinterpret_cast<uint4*>(smem + q_at(tid, 2 * g) + 2 * C::QPART) = part;
+              else *reinterpret_cast<uint4*>(smem + q_at(r, 2 * g) + 2 * C::QPART) = part;
             }
           }
         }
@@ -384,7 +396,6 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ 
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
-      return factor;
     };
 
     // the next piece; one without tiles adds nothing to its rows
@@ -396,10 +407,9 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ 
       });
     };
     bool ok = true, more = advance(W);
-    float factor = 0.0f;
     if (more) {
       fetch_q(W);
-      factor = publish_q(W);
+      publish_q(W, 0);
     }
     for (; more; ++items) {
       Walk N = W;  // the next piece, looked up when this one's first scores are there
@@ -415,6 +425,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ 
 
       float m = -INFINITY, l = 0.0f;
       const int tiles = W.t1 - W.t0;
+      if (!(ok = wait(q_full, items & 1))) break;  // (the factors, which other warps wrote)
+      const float factor = factors[(items & 1) * kAttnM + min(tid, it.m_cnt - 1)];
       int b1 = 0;  // the previous tile's buffer, and its phase
       uint32_t pb1 = 0;
       for (int t = W.t0; t < W.t1; ++t, ++tile) {
@@ -549,8 +561,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ 
         if (++b == NSB) b = 0, pb ^= 1;
       }
       if (!ok) break;
-      float next_factor = 0.0f;
-      if (more) next_factor = publish_q(N);
+      if (more) publish_q(N, items + 1);
       units += 2 * tiles;
       if (!(ok = wait(o_full + 8 * b1, pb1))) break;
       tc_fence_after();
@@ -612,7 +623,6 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ 
       }
       tc_fence_before();
       W = N;
-      factor = next_factor;
     }
   }
   __syncthreads();

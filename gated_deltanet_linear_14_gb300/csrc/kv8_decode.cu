@@ -1,5 +1,5 @@
-// Attention over a cache of 8-bit codes for steps of few rows a request (decode,
-// verify): up to 32 (row, query head) pairs per key/value head, nothing shared
+// Attention over a cache of 8-bit codes for steps of few rows a request (decode, short
+// verifies): up to 16 (row, query head) pairs per key/value head, nothing shared
 // (sm_103a).
 //
 // kv8_attn.cu's arithmetic with the roles of the operands exchanged: 128 keys are
@@ -28,8 +28,9 @@ namespace {
 
 constexpr int kTileKeys = 128;                    // two of the plan's tiles
 constexpr int kFewBoxes = kTileKeys / 16;         // pages of a tile, at most
+constexpr int N = 16;                             // pairs, the columns
 
-template <class T, int D, int N>
+template <class T, int D>
 struct CfgFew {
   static constexpr int NC = D < 128 ? 1 : D / 128;      // chunks of a row, blocks of O^T
   static constexpr int PITCH = D < 128 ? D : 128;       // bytes of a row in a chunk, swizzled
@@ -38,10 +39,11 @@ struct CfgFew {
   static constexpr uint32_t UNIT = kTileKeys * D, QPART = N * D, PPART = kTileKeys * N;
   static constexpr int NQ = Parts<T>::Q, NP = Parts<T>::P;
   static constexpr int CTAS = D == 256 ? 1 : 2;
-  static constexpr uint32_t TM_O = 2 * N, TM_COLS = 2 * N + NC * N <= 64 ? 64 : 128;
+  static constexpr uint32_t TM_O = 2 * N, TM_COLS = 64;
+  static_assert(TM_O + NC * N <= TM_COLS, "tensor memory columns");
   // shared memory: two Qs (an item's and the next one's), the ring, two Ps
   static constexpr uint32_t LIMIT = CTAS == 2 ? 115712 : 232448;
-  static constexpr uint32_t COLS = 2 * N * 16, STATS = (2 + 4 + 4 + 2) * N * 4;
+  static constexpr uint32_t COLS = 2 * N * 16, STATS = (4 + 4 + 4 + 2) * N * 4;
   static constexpr uint32_t FIXED =
       2 * NQ * QPART + 2 * NP * PPART + kExpSlots * 16 + COLS + STATS + 8 * (2 * 8 + 9 + kExpSlots) + 64;
   static constexpr int FIT = (LIMIT - FIXED) / UNIT, NS = FIT < 8 ? FIT : 8;
@@ -58,56 +60,58 @@ struct CfgFew {
 };
 
 // What the threads read of a pair.
-template <int N>
 struct Columns {
   float factor[N];      // of its scores
   int lim[N];           // it sees keys below this
   long long row[N];     // row * Hq + head
 };
 
-// N consecutive fp32 columns of this thread's TMEM lane.
-template <int N>
+// Eight consecutive fp32 columns of this thread's TMEM lane. (What few tiles or no tile
+// needs loops over them at an address of its own: unrolled over a tile's registers its
+// code made short items wait for instructions, 120 against 53 us on 64 requests of 8
+// rows behind 1000 keys.)
+__device__ __forceinline__ void tm_read8(uint32_t taddr, float* v) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]),
+        "=&r"(r[6]), "=&r"(r[7])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tm_write8(uint32_t taddr, const float* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+               "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+               "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+               "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+               : "memory");
+}
+// ... and all N.
 __device__ __forceinline__ void tm_read(uint32_t taddr, float* v) {
-  if constexpr (N == 32) {
-    tmem_ld32(taddr, v);
-  } else {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-        "%14,%15}, [%16];\ntcgen05.wait::ld.sync.aligned;"
-        : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]),
-          "=&r"(r[6]), "=&r"(r[7]), "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]),
-          "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15])
-        : "r"(taddr)
-        : "memory");
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];\ntcgen05.wait::ld.sync.aligned;"
+      : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]),
+        "=&r"(r[6]), "=&r"(r[7]), "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]),
+        "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15])
+      : "r"(taddr)
+      : "memory");
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-  }
-}
-template <int N>
-__device__ __forceinline__ void tm_write(uint32_t taddr, const float* v) {
-  uint32_t r[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) r[i] = __float_as_uint(v[i]);
-  if constexpr (N == 32) tm_store32(taddr, r);
-  else tm_store16(taddr, r);
-}
-
-// Where the N bytes of a key lie in a part of P^T, in pieces of 16: rows of 16 bytes
-// side by side, or of 32 in the 32-byte swizzle.
-template <int N>
-__device__ __forceinline__ uint32_t p_at(int key, int piece) {
-  return N == 16 ? key * 16 : key * 32 + ((piece ^ (key >> 2 & 1)) << 4);
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 }  // namespace
 
-template <class T, int D, int N>
-__global__ void __launch_bounds__(kAttnThreads, CfgFew<T, D, N>::CTAS)
+template <class T, int D>
+__global__ void __launch_bounds__(kAttnThreads, CfgFew<T, D>::CTAS)
 kv8_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                AttnDims A, KvBatch B, AttnPlan P, const T* q, long long qs, Kv8Cache K, T* o,
                float* lse, float* po, float2* pml, int32_t* status) {
-  using C = CfgFew<T, D, N>;
+  using C = CfgFew<T, D>;
   constexpr int NS = C::NS, NQ = C::NQ, NP = C::NP;
   constexpr uint32_t UNIT = C::UNIT;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -116,10 +120,11 @@ kv8_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
   const uint32_t s_full = q_full + 16, p_ready = s_full + 16, o_full = p_ready + 16;
   const uint32_t vote = o_full + 16, e_full = vote + 8;
   uint8_t* exps = smem + C::EXPS;
-  Columns<N>* cols = reinterpret_cast<Columns<N>*>(smem + C::COL);
-  float* neg_m = reinterpret_cast<float*>(smem + C::STAT);  // [N]: 2^neg_m p is at most 2^15
-  float* f_tab = neg_m + N;                                 // [N]: what a raise scales by
-  int* warp_max = reinterpret_cast<int*>(f_tab + N);        // [4][N]
+  Columns* cols = reinterpret_cast<Columns*>(smem + C::COL);
+  // [2][N]: 2^(exponent + neg_tab) is at most 2^15, at present and before (or after) a raise
+  float* neg_tab = reinterpret_cast<float*>(smem + C::STAT);
+  float* f_tab = neg_tab + 2 * N;                           // [2][N]: what the raise scales by
+  int* warp_max = reinterpret_cast<int*>(f_tab + 2 * N);    // [4][N]
   float* warp_sum = reinterpret_cast<float*>(warp_max + 4 * N);  // [4][N]
   float* inv_tab = warp_sum + 4 * N;                        // [N]
   // [0] tensor memory, [1] a role gave up, [2..4] see `strange`, [5..7] votes
@@ -267,7 +272,7 @@ kv8_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
     const uint64_t dk = desc8<C::SW>(ring, 16, 8 * C::PITCH);
     // (64 elements are repeated to fill the 128 rows of the product)
     const uint64_t dv = desc8<C::SW>(ring, 0, 8 * C::PITCH);
-    const uint64_t dp = N == 16 ? desc8<0>(sb + C::PBUF, 128, 128) : desc8<6>(sb + C::PBUF, 16, 256);
+    const uint64_t dp = desc8<0>(sb + C::PBUF, 128, 128);  // (rows of 16 bytes, no swizzle)
     auto advance = [&]() {
       if (++slot == NS) slot = 0, phase ^= 1;
     };
@@ -345,6 +350,7 @@ kv8_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
     const float c2 = A.scale * 1.44269504088896341f;
     int b = 0;                     // score buffer of this tile, and its phase
     uint32_t pb = 0, vph = 0;      // vph: phase of the warps' meetings
+    int cur = 0;                   // the half of the tables that holds
     uint32_t units = 0, items = 0, tile = 0;  // ring units, items and tiles before this one
     // the four warps meet; what each wrote before is seen by all afterwards
     auto meet = [&]() {
@@ -437,7 +443,7 @@ kv8_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
       Walk X = W;  // the next piece, looked up when this one's first scores are there
       W.touch_next();
       const AttnItem& it = W.it;
-      const Columns<N>& col = cols[items & 1];
+      const Columns& col = cols[items & 1];
       const int kb = first_key(W), ke = end_key(W), tiles = tiles_of(W);
       const int first_seen = it.vis0 + it.m0 / A.G;  // the row that sees least: keys below this
       const bool mixed = it.m0 / A.G != (it.m0 + it.m_cnt - 1) / A.G;
@@ -464,88 +470,120 @@ kv8_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
           more = advance(X);
           if (more) fetch_q(X);
         }
-        float s[N];
-        tm_read<N>(tmem + N * b + lane_base, s);
-        // (a score that is past the range of fp32 is its end: 0 times it stays 0)
-#pragma unroll
-        for (int n = 0; n < N; ++n) s[n] *= kf;
-        auto hides = [&](int n) { return tid >= nv || (cut && key >= col.lim[n]); };
-        // the exponent of pair n's p at the present maximum
-        auto exponents = [&](float* t) {
-          float top = -INFINITY;
-#pragma unroll
-          for (int n = 0; n < N; n += 4) {
-            const float4 fc = *reinterpret_cast<const float4*>(col.factor + n);
-            const float4 nm = *reinterpret_cast<const float4*>(neg_m + n);
-            float2 a = __ffma2_rn(make_float2(s[n], s[n + 1]), make_float2(fc.x, fc.y),
-                                  __fadd2_rn(make_float2(ve, ve), make_float2(nm.x, nm.y)));
-            float2 c = __ffma2_rn(make_float2(s[n + 2], s[n + 3]), make_float2(fc.z, fc.w),
-                                  __fadd2_rn(make_float2(ve, ve), make_float2(nm.z, nm.w)));
-            t[n] = a.x, t[n + 1] = a.y, t[n + 2] = c.x, t[n + 3] = c.y;
-          }
-          if (masked) {
-#pragma unroll
-            for (int n = 0; n < N; ++n)
-              if (hides(n)) t[n] = -INFINITY;
-          }
-#pragma unroll
-          for (int n = 0; n < N; n += 2) top = max3(top, t[n], t[n + 1]);
-          return top;
-        };
+        const uint32_t ts = tmem + N * b + lane_base;
+        // Pair n's row (m0 + n) / G sees keys below vis0 + that: this key is hidden from the
+        // first `hidden` pairs.
+        const long long unseen = (long long)(key - it.vis0 + 1) * A.G - it.m0;
+        const int hidden = tid >= nv ? N : !cut ? 0 : (int)min(max(unseen, 0LL), (long long)N);
         float t[N];
-        bool raise = j == 0;
-        if (j > 0) {
-          const bool mine = __any_sync(~0u, exponents(t) > kP8Raise + kP8Up);
-          if (mine && lane == 0) words[5 + tile % 3] = 1;
-          // (the vote before the last, which everyone has read)
-          if (tid == 0) words[5 + (tile + 1) % 3] = 0;
-          if (!(ok = meet())) break;
-          raise = words[5 + tile % 3] != 0;
-        } else if (tid == 0) {
-          words[5 + (tile + 1) % 3] = 0;
-        }
-        if (raise) {
-          // the columns' maxima over the tile, as ordered whole numbers; NaN counts for none
-          int most = 0;
+        bool first = true;
+        uint32_t groups = ~0u;  // of eight pairs
+        // Once, or again with the new maxima where they are raised (always on an item's
+        // first tile).
+#pragma unroll 1
+        while (true) {
+          if (j > 0 || !first) {
+            // the exponents of the p's at the present maxima
+            tm_read(ts, t);
+            float top = -INFINITY;
+            const float2 ke2 = make_float2(kf, kf), ve2 = make_float2(ve, ve);
 #pragma unroll
-          for (int n = 0; n < N; ++n) {
-            float u = __fmaf_rn(s[n], col.factor[n], ve);
-            if ((masked && hides(n)) || !(u == u)) u = -INFINITY;
-            const int w = __float_as_int(u), top = __reduce_max_sync(~0u, w ^ (w >> 31 & 0x7FFFFFFF));
-            if (lane == n) most = top;
-          }
-          if (lane < N) warp_max[warp * N + lane] = most;
-          if (!(ok = meet())) break;
-          if (tid < N) {
-            int w = warp_max[tid];
+            for (int n = 0; n < N; n += 4) {
+              const float4 fc = *reinterpret_cast<const float4*>(col.factor + n);
+              const float4 nm = *reinterpret_cast<const float4*>(neg_tab + cur * N + n);
+              const float2 s0 = __fmul2_rn(make_float2(t[n], t[n + 1]), ke2);
+              const float2 s1 = __fmul2_rn(make_float2(t[n + 2], t[n + 3]), ke2);
+              const float2 a = __ffma2_rn(s0, make_float2(fc.x, fc.y),
+                                          __fadd2_rn(ve2, make_float2(nm.x, nm.y)));
+              const float2 c = __ffma2_rn(s1, make_float2(fc.z, fc.w),
+                                          __fadd2_rn(ve2, make_float2(nm.z, nm.w)));
+              t[n] = a.x, t[n + 1] = a.y, t[n + 2] = c.x, t[n + 3] = c.y;
+            }
+            if (masked) {
 #pragma unroll
-            for (int x = 1; x < kSoftmaxWarps; ++x) w = max(w, warp_max[x * N + tid]);
-            const float mx = __int_as_float(w ^ (w >> 31 & 0x7FFFFFFF));
-            // (each pair by itself: its rounding depends on no other)
-            const float m = j == 0 ? -INFINITY : kP8Up - neg_m[tid];
-            const bool up = mx - m > kP8Raise;
-            f_tab[tid] = up ? ex2(m - mx) : 1.0f;
-            if (up || j == 0) neg_m[tid] = kP8Up - mx;
+              for (int n = 0; n < N; ++n)
+                if (n < hidden) t[n] = -INFINITY;
+            }
+#pragma unroll
+            for (int n = 0; n < N; n += 2) top = max3(top, t[n], t[n + 1]);
+            if (!first || j == 0) break;
+            if (__any_sync(~0u, top > kP8Raise + kP8Up)) {
+              uint32_t over = 0;
+#pragma unroll
+              for (int n = 0; n < N; ++n) over |= t[n] > kP8Raise + kP8Up ? 1u << (n >> 3) : 0u;
+              over = __reduce_or_sync(~0u, over);
+              if (lane == 0) atomicOr(const_cast<uint32_t*>(words) + 5 + tile % 3, over);
+            }
+            // (the vote before the last, which everyone has read)
+            if (tid == 0) words[5 + (tile + 1) % 3] = 0;
+            if (!(ok = meet())) break;
+            groups = words[5 + tile % 3];
+            if (groups == 0) break;
+          } else if (tid == 0) {
+            words[5 + (tile + 1) % 3] = 0;
+          }
+          first = false;
+          // the pairs' maxima over the tile, of the groups of eight that have to be raised, as
+          // ordered whole numbers; NaN counts for none
+#pragma unroll 1
+          for (int n0 = 0; n0 < N; n0 += 8) {
+            if (!(groups >> (n0 >> 3) & 1)) continue;
+            float s[8];
+            tm_read8(ts + n0, s);
+            int most = 0;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              float x = __fmaf_rn(s[n] * kf, col.factor[n0 + n], ve);
+              if (n0 + n < hidden || !(x == x)) x = -INFINITY;
+              const int w = __float_as_int(x);
+              const int top = __reduce_max_sync(~0u, w ^ (w >> 31 & 0x7FFFFFFF));
+              if (lane == n) most = top;
+            }
+            if (lane < 8) warp_max[warp * N + n0 + lane] = most;
           }
           if (!(ok = meet())) break;
+          // every warp for itself, all the same, to the other half of the tables
+          if (lane < N) {
+            float neg = neg_tab[cur * N + lane], f = 1.0f;
+            if (groups >> (lane >> 3) & 1) {
+              int w = warp_max[lane];
+#pragma unroll
+              for (int x = 1; x < kSoftmaxWarps; ++x) w = max(w, warp_max[x * N + lane]);
+              const float mx = __int_as_float(w ^ (w >> 31 & 0x7FFFFFFF));
+              // (each pair by itself: its rounding depends on no other)
+              const float m = j == 0 ? -INFINITY : kP8Up - neg;
+              const bool up = mx - m > kP8Raise;
+              if (up) f = ex2(m - mx);
+              if (up || j == 0) neg = kP8Up - mx;
+            }
+            neg_tab[(cur ^ 1) * N + lane] = neg;
+            f_tab[(cur ^ 1) * N + lane] = f;
+          }
+          __syncwarp();
+          cur ^= 1;
           if (j > 0) {
+            const float* fs = f_tab + cur * N;
 #pragma unroll
-            for (int n = 0; n < N; ++n) l[n] *= f_tab[n];
+            for (int n = 0; n < N; n += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(fs + n);
+              l[n] *= f.x, l[n + 1] *= f.y, l[n + 2] *= f.z, l[n + 3] *= f.w;
+            }
             // O is complete up to the previous tile
             if (!(ok = wait(o_full + 8 * b1, pb1))) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < C::NC; ++c) {
-              float v[N];
-              tm_read<N>(tmem + C::TM_O + N * c + lane_base, v);
+            for (int c = 0; c < C::NC * N; c += 8) {
+              if (!(groups >> (c % N >> 3) & 1)) continue;
+              float v[8];
+              tm_read8(tmem + C::TM_O + c + lane_base, v);
 #pragma unroll
-              for (int n = 0; n < N; ++n) v[n] *= f_tab[n];
-              tm_write<N>(tmem + C::TM_O + N * c + lane_base, v);
+              for (int n = 0; n < 8; ++n) v[n] *= fs[c % N + n];
+              tm_write8(tmem + C::TM_O + c + lane_base, v);
             }
             tmem_st_wait();
           }
-          exponents(t);
         }
+        if (!ok) break;
         const float kl = pow2(-(int)ex[8]);
         uint32_t p[NP * (N / 4)];
 #pragma unroll
@@ -559,14 +597,9 @@ kv8_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
         }
         uint8_t* pdst = smem + C::PBUF + b * NP * C::PPART;
 #pragma unroll
-        for (int x = 0; x < NP; ++x) {
-#pragma unroll
-          for (int g = 0; g < N / 16; ++g) {
-            const uint32_t* w = p + x * (N / 4) + 4 * g;
-            *reinterpret_cast<uint4*>(pdst + x * C::PPART + p_at<N>(tid, g)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
+        for (int x = 0; x < NP; ++x)  // (a key's 16 bytes side by side)
+          *reinterpret_cast<uint4*>(pdst + x * C::PPART + tid * N) =
+              make_uint4(p[4 * x], p[4 * x + 1], p[4 * x + 2], p[4 * x + 3]);
         // Value rows past the last key hold whatever was there, and p = 0 does
         // not silence a NaN: they are zeroed. Where rows see different keys,
         // NaN codes are zeroed too and added at the end to the rows that see them.
@@ -619,7 +652,7 @@ kv8_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
             l[0] += __shfl_xor_sync(~0u, l[0], d);
           }
         }
-        warp_sum[warp * N + (N == 32 ? lane : lane >> 1)] = l[0];
+        warp_sum[warp * N + (lane >> 1)] = l[0];
       }
       if (!(ok = meet())) break;
       const bool direct = W.direct();
@@ -628,7 +661,7 @@ kv8_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
 #pragma unroll
         for (int x = 0; x < kSoftmaxWarps; ++x) sum += warp_sum[x * N + tid];
         inv_tab[tid] = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-        const float m = -neg_m[tid];
+        const float m = -neg_tab[cur * N + tid];
         if (tid < it.m_cnt) {
           if (!direct)
             pml[partial(P, it, W.head, A.Hq, A.G, W.span, W.unit, W.c, tid, D).row] =
@@ -642,12 +675,16 @@ kv8_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
       tc_fence_after();
       // whether a NaN code was taken out of a tile of this item
       const bool strange = words[2 + items % 3] != 0;
+      const AttnPart part = direct ? AttnPart{0, 0, 0}
+                                   : partial(P, it, W.head, A.Hq, A.G, W.span, W.unit, W.c, 0, D);
 #pragma unroll 1
-      for (int c = 0; c < C::NC; ++c) {
-        float v[N];
-        tm_read<N>(tmem + C::TM_O + N * c + lane_base, v);
-        const int d = 128 * c + tid;
-        if (strange && d < D) {
+      for (int c = 0; c < C::NC * N; c += 8) {
+        const int n0 = c % N, d = 128 * (c / N) + tid;
+        if (n0 >= it.m_cnt) continue;
+        float v[8];
+        tm_read8(tmem + C::TM_O + c + lane_base, v);
+        if (d >= D) continue;
+        if (strange) {
           // NaN codes that were taken out of the tiles in which rows see different keys
           int key = kb;
           while (key + kTileKeys <= first_seen) key += kTileKeys;
@@ -658,24 +695,17 @@ kv8_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
                 K.v[(((size_t)page * A.Hkv + W.head) * A.ps + (key & (A.ps - 1))) * D + d];
             if ((x & 0x7F) != 0x7F) continue;
 #pragma unroll
-            for (int n = 0; n < N; ++n)
-              if (key < col.lim[n]) v[n] = __int_as_float(0x7FFFFFFF);
+            for (int n = 0; n < 8; ++n)
+              if (key < col.lim[n0 + n]) v[n] = __int_as_float(0x7FFFFFFF);
           }
         }
-        if (d < D) {
-          if (direct) {
+        // (an item's pieces lie side by side: element 0 of pair n at 8 n)
+        float* dst = po + part.at + (long long)(d >> 3) * part.step + (d & 7) + 8 * n0;
 #pragma unroll
-            for (int n = 0; n < N; ++n)
-              if (n < it.m_cnt) elem_from_f(v[n] * inv_tab[n], o[col.row[n] * D + d]);
-          } else {
-            const AttnPart part =
-                partial(P, it, W.head, A.Hq, A.G, W.span, W.unit, W.c, 0, D);
-            // (an item's pieces lie side by side: element 0 of pair n at 8 n)
-            float* dst = po + part.at + (long long)(d >> 3) * part.step + (d & 7);
-#pragma unroll
-            for (int n = 0; n < N; ++n)
-              if (n < it.m_cnt) dst[8 * n] = v[n];
-          }
+        for (int n = 0; n < 8; ++n) {
+          if (n0 + n >= it.m_cnt) break;
+          if (direct) elem_from_f(v[n] * inv_tab[n0 + n], o[col.row[n0 + n] * D + d]);
+          else dst[8 * n] = v[n];
         }
       }
       tc_fence_before();
@@ -686,10 +716,9 @@ kv8_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
   if (warp == 5) tmem_dealloc(tmem, C::TM_COLS);
 }
 
-int kv8_few_pairs(const AttnDims& A, const KvBatch& B) {
+bool kv8_few_pairs(const AttnDims& A, const KvBatch& B) {
   const long long rows = B.max_rows < B.num_rows ? B.max_rows : B.num_rows;
-  const long long pairs = rows * A.G;
-  return B.num_groups > 0 || pairs > 32 ? 0 : pairs > 16 ? 32 : 16;
+  return B.num_groups == 0 && rows * A.G <= N;
 }
 
 cudaError_t launch_kv8_few(const void* tk, const void* tv, const AttnDims& A, const KvBatch& B,
@@ -698,23 +727,19 @@ cudaError_t launch_kv8_few(const void* tk, const void* tv, const AttnDims& A, co
                            cudaStream_t s) {
   const AttnLayout L = attn_layout(A, B);
   const AttnPlan P = attn_plan_view(A, B, L, plan);
-  auto go = [&](auto t, auto d, auto n) {
+  auto go = [&](auto t, auto d) {
     using T = decltype(t);
-    constexpr int D = decltype(d)::value, N = decltype(n)::value, bytes = CfgFew<T, D, N>::BYTES;
-    cudaError_t e = ensure_smem_limit<kv8_few_kernel<T, D, N>>(bytes);
+    constexpr int D = decltype(d)::value, bytes = CfgFew<T, D>::BYTES;
+    const cudaError_t e = ensure_smem_limit<kv8_few_kernel<T, D>>(bytes);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kv8_few_kernel<T, D, N>, dim3(L.ctas), dim3(kAttnThreads), bytes, s,
+    return launch_pdl(kv8_few_kernel<T, D>, dim3(L.ctas), dim3(kAttnThreads), bytes, s,
                       *(const CUtensorMap*)tk, *(const CUtensorMap*)tv, A, B, P, (const T*)q, qs,
                       K, (T*)o, lse, (float*)ws, (float2*)((char*)ws + L.ws_ml), status);
   };
-  auto by_pairs = [&](auto t, auto d) {
-    return kv8_few_pairs(A, B) == 16 ? go(t, d, std::integral_constant<int, 16>())
-                                     : go(t, d, std::integral_constant<int, 32>());
-  };
   auto by_dim = [&](auto t) {
-    if (A.D == 64) return by_pairs(t, std::integral_constant<int, 64>());
-    if (A.D == 128) return by_pairs(t, std::integral_constant<int, 128>());
-    return by_pairs(t, std::integral_constant<int, 256>());
+    if (A.D == 64) return go(t, std::integral_constant<int, 64>());
+    if (A.D == 128) return go(t, std::integral_constant<int, 128>());
+    return go(t, std::integral_constant<int, 256>());
   };
   const cudaError_t e = io == GDN_BF16 ? by_dim(bf16()) : by_dim(__half());
   if (e != cudaSuccess) return e;
