@@ -79,6 +79,46 @@ __device__ __forceinline__ void each_place(const KvBatch& B, bool packed, long l
 
 enum { ROLE_Q = 0, ROLE_K = 1, ROLE_V = 2 };
 
+// Element d of a key row of D elements, normed and turned (with element d2 of its pair, by
+// the angle pos * f; d2 < 0: not) in 64 bits and times 2^-e, rounded to fp32 so that a
+// rounding to fewer bits comes out as from the 64: towards zero, with the last bit set
+// where that was not exact. first: whether d is the pair's x. By a warp together, all
+// lanes with the same arguments.
+template <class T, int D>
+__device__ __forceinline__ float exact_key(const T* row, int d, int d2, bool first, int pos, float f,
+                                           const HeadNorm& N, int e) {
+  double x = (double)elem_to_f(row[d]), y = d2 >= 0 ? (double)elem_to_f(row[d2]) : 0.0;
+  if (N.on) {
+    // (squares of 16-bit values are exact in fp32)
+    float v[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) v[i] = elem_to_f(row[32 * i + (threadIdx.x & 31)]);
+    double ss = 0.0;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) ss += (double)(v[i] * v[i]);
+#pragma unroll 1
+    for (int i = 16; i; i >>= 1) ss += __shfl_xor_sync(~0u, ss, i);
+    const double mean = ss * (1.0 / D) + (double)N.eps;
+    // (an estimate and two steps of Newton; what leaves fp32's range is not here: those rows'
+    // fp32 values are as good as any)
+    double inv = (double)rsqrtf((float)mean);
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) inv *= 1.5 - 0.5 * mean * inv * inv;
+    auto weight = [&](int i) { return N.kw ? (double)N.offset + (double)N.kw[i] : 1.0; };
+    x *= inv * weight(d);
+    if (d2 >= 0) y *= inv * weight(d2);
+  }
+  if (d2 >= 0) {
+    double t = (double)pos * (double)f * 0.15915494309189533577, sn, cs;  // in turns
+    t -= rint(t);
+    sincospi(t + t, &sn, &cs);
+    x = first ? x * cs - y * sn : x * cs + y * sn;
+  }
+  x *= (double)pow2(-e);
+  const float r = __double2float_rz(x);
+  return (double)r == x ? r : __int_as_float(__float_as_int(r) | 1);
+}
+
 template <class T, int D, bool INTER>
 __global__ void __launch_bounds__(kKv8Threads, 4)
 kv8_append_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Rope R,
@@ -251,17 +291,60 @@ kv8_append_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Ro
         top = max(top_tab[warp & ~1], top_tab[warp | 1]);
         __syncthreads();
       }
-      if (!on) continue;
+      if (!on) continue;  // (a warp together)
       const int e8 = max(kv8_exponent(top), before);
       const float2 ss = make_float2(pow2(-e8), pow2(-e8));
+      // A key within 4 ulp of the middle between two codes is formed again in 64 bits: in fp32
+      // it may have come to the wrong side. (A hundred thousandth of them; those below 2^-6,
+      // whose codes are 2^-9 apart, are left.)
+      unsigned long long near = 0;
 #pragma unroll
       for (int n = 0; n < TURNS; ++n) {
-        if (!here(n)) continue;
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
           const float2 y = __fmul2_rn(make_float2(x[n][e], x[n][e + 1]), ss);
           x[n][e] = y.x, x[n][e + 1] = y.y;
         }
+        if (role == ROLE_K && (N.on || R.rd)) {
+          uint32_t bits = 0;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const uint32_t w = __float_as_uint(x[n][e]);
+            if (((w + 0x80004u) & 0xFFFFF) < 8u && fabsf(x[n][e]) >= 0x1p-6f) bits |= 1u << e;
+          }
+          if (here(n)) near |= (unsigned long long)bits << (16 * n);
+        }
+      }
+#pragma unroll 1
+      while (const uint32_t lanes = __ballot_sync(~0u, near != 0)) {
+        const int from = __ffs((int)lanes) - 1;
+        const int k = __shfl_sync(~0u, __ffsll((long long)near) - 1, from), e = k & 15;
+        const int fu = from % U, i = (k >> 4) * RPT + r0 - lane / U + from / U;
+        const bool turns = fu < R.rd / 16, first = INTER ? !(e & 1) : e < 8;
+        const int fa = INTER || !turns ? 16 * fu : 8 * fu, fb = INTER || !turns ? fa + 8 : half + 8 * fu;
+        const int d = e < 8 ? fa + e : fb + e - 8;
+        const int d2 = !turns ? -1 : INTER ? (first ? d + 1 : d - 1) : first ? fb + e : fa + e - 8;
+        int pos = 0;
+        float f = 0.0f;
+        if (turns) {
+          const int pair = 8 * fu + (INTER ? e >> 1 : e & 7);
+          int ax = R.axis ? R.axis[pair] : 0;
+          if (ax < 0 || ax >= R.axes) ax = 0;
+          pos = R.pos[(size_t)ax * R.num_rows + row0 + i];
+          f = R.inv_freq[pair];
+        }
+        const float v = exact_key<T, D>(base + i * stride + h * D, d, d2, first, pos, f, N, e8);
+        const int mine = lane == from ? k : -1;
+        if (lane == from) near &= near - 1;
+#pragma unroll
+        for (int n = 0; n < TURNS; ++n)
+#pragma unroll
+          for (int m = 0; m < 16; ++m)
+            if (mine == 16 * n + m) x[n][m] = v;
+      }
+#pragma unroll
+      for (int n = 0; n < TURNS; ++n) {
+        if (!here(n)) continue;
         uint8_t* p = codes + (n * RPT + r0) * D;
         *reinterpret_cast<uint2*>(p + ea) = make_uint2(e4m3x4(x[n]), e4m3x4(x[n] + 4));
         *reinterpret_cast<uint2*>(p + eb) = make_uint2(e4m3x4(x[n] + 8), e4m3x4(x[n] + 12));
