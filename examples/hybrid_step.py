@@ -4,10 +4,13 @@ them. Requests of one group continue the same prompt, whose pages they share.
 
 Per step the caller plans the attention once; per layer it makes one call for
 a GDN layer (gdn_decode) and two for an attention layer (gdn_kv_append, which
-rotates q and k on the way, and gdn_attn).
+rotates q and k on the way, and gdn_attn). With --bits 8 the attention layer norms
+its queries and keys and keeps them and its values in 8 bits (gdn_kv8_append and
+gdn_kv8_attn).
 
-    python examples/hybrid_step.py
+    python examples/hybrid_step.py [--bits 8]
 """
+import argparse
 import os
 import sys
 
@@ -15,7 +18,7 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import gated_deltanet_linear_14_gb300 as gdn  # noqa: E402
-from gated_deltanet_linear_14_gb300.pages import KvCache, PagePool  # noqa: E402
+from gated_deltanet_linear_14_gb300.pages import Kv8Cache, KvCache, PagePool  # noqa: E402
 
 HIDDEN, GDN_LAYERS = 1024, 3
 HK, HV, DG = 4, 8, 128             # GDN heads and head dimension
@@ -74,22 +77,49 @@ class AttentionLayer:
                      workspace, workspace.numel(), status)
         return x + self.out(o.flatten(1))
 
+    def plan_for(self, batch, status):
+        plan, workspace = (torch.empty(size(self.dims, batch), dtype=torch.uint8, device="cuda")
+                           for size in (gdn.gdn_attn_plan_bytes, gdn.gdn_attn_workspace_bytes))
+        gdn.gdn_attn_plan(self.dims, batch, plan, plan.numel(), status)
+        return plan, workspace
 
-def plan_for(dims, batch, status):
-    plan, workspace = (torch.empty(size(dims, batch), dtype=torch.uint8, device="cuda") for size in
-                       (gdn.gdn_attn_plan_bytes, gdn.gdn_attn_workspace_bytes))
-    gdn.gdn_attn_plan(dims, batch, plan, plan.numel(), status)
-    return plan, workspace
+
+class AttentionLayer8(AttentionLayer):
+    """Queries and keys normed head by head, keys and values kept in 8 bits."""
+
+    def __init__(self, pages, g):
+        super().__init__(pages, g)
+        self.cache = Kv8Cache(self.dims, pages)
+        self.q_norm, self.k_norm = (0.1 * torch.randn(D, device="cuda", generator=g)
+                                    for _ in range(2))
+        self.norm = gdn.make_head_norm(self.q_norm, self.k_norm, offset=1.0)
+
+    def step(self, x, batch, rope, plan, workspace, status):
+        q, k, v = self.rows(x)
+        q_rot = torch.empty(x.shape[0], HQ, D, device="cuda", dtype=torch.bfloat16)
+        o = torch.empty_like(q_rot)
+        gdn.gdn_kv8_append(self.dims, batch, self.norm, rope, q, k, v, q_rot, self.cache.codes,
+                           status)
+        gdn.gdn_kv8_attn(self.dims, batch, plan, q_rot, self.cache.codes, o, None, workspace,
+                         workspace.numel(), status)
+        return x + self.out(o.flatten(1))
+
+    def plan_for(self, batch, status):
+        plan, workspace = (torch.empty(size(self.dims, batch), dtype=torch.uint8, device="cuda")
+                           for size in (gdn.gdn_kv8_attn_plan_bytes,
+                                        gdn.gdn_kv8_attn_workspace_bytes))
+        gdn.gdn_kv8_attn_plan(self.dims, batch, plan, plan.numel(), status)
+        return plan, workspace
 
 
-def main(requests=16, prompt_pages=20, steps=4, seed=0):
+def main(requests=16, prompt_pages=20, steps=4, seed=0, bits=16):
     """The hidden states of the last step, and the attention layer with its page table and
     lengths (for checks)."""
     g = torch.Generator(device="cuda")
     g.manual_seed(seed)
     R, prompt = requests, prompt_pages * PAGE
     gdn_layers = [GdnLayer(R, g) for _ in range(GDN_LAYERS)]
-    attn = AttentionLayer(prompt_pages + R, g)
+    attn = (AttentionLayer8 if bits == 8 else AttentionLayer)(prompt_pages + R, g)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     inv_freq = 1.0 / 1e6 ** (torch.arange(ROT // 2, device="cuda").float() / (ROT // 2))
 
@@ -101,7 +131,7 @@ def main(requests=16, prompt_pages=20, steps=4, seed=0):
     maps = (i32([0]), i32([prompt]), i32([prompt]), table)
     rope = gdn.make_rope(ROT, inv_freq, torch.arange(prompt, device="cuda", dtype=torch.int32))
     first = gdn.make_kv_batch(1, prompt, prompt, attn.cache.num_pages, *maps)
-    attn.step(x, first, rope, *plan_for(attn.dims, first, status), status)
+    attn.step(x, first, rope, *attn.plan_for(first, status), status)
 
     # then R requests go on from it, one token a step
     ones, rows, group = i32([1] * R), i32(range(R)), (i32([0]), i32([R]), i32([prompt_pages]))
@@ -114,7 +144,7 @@ def main(requests=16, prompt_pages=20, steps=4, seed=0):
                                      *group)
         positions = kv_len - 1
         rope = gdn.make_rope(ROT, inv_freq, positions)
-        plan, workspace = plan_for(attn.dims, kv_batch, status)  # for all attention layers
+        plan, workspace = attn.plan_for(kv_batch, status)  # for all attention layers
         for layer in gdn_layers:
             x = layer.step(x, gdn_batch, status)
         before = x
@@ -124,5 +154,7 @@ def main(requests=16, prompt_pages=20, steps=4, seed=0):
 
 
 if __name__ == "__main__":
-    out = main()[1]
+    parser = argparse.ArgumentParser()
+    parser.add_argument("--bits", type=int, choices=(8, 16), default=16, help="of the key/value cache")
+    out = main(bits=parser.parse_args().bits)[1]
     print(f"hybrid step ok: {out.shape[0]} requests, |x| = {out.float().norm().item():.3f}")
