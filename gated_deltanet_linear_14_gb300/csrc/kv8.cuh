@@ -55,6 +55,12 @@ cudaError_t launch_kv8_append(const RopeCall& C, const Rope& P, const HeadNorm& 
 cudaError_t launch_kv8_read(const RopeCall& C, const AttnDims& A, const KvBatch& B,
                             const Kv8Cache& K, int32_t* status, cudaStream_t s);
 
+// The step's pages to 16 bits, a copy for each request: k_out, v_out [R * max_pages] pages,
+// table [R][max_pages] their indexes.
+cudaError_t launch_kv8_widen(const AttnDims& A, const KvBatch& B, int io, const Kv8Cache& K,
+                             void* k_out, void* v_out, int32_t* table, int32_t* status,
+                             cudaStream_t s);
+
 // Whether kv8_decode.cu takes the step: at most 16 (row, query head) pairs per key/value
 // head and request, and nothing declared shared. (64 requests, 32/8 heads x 128, us there
 // against kv8_attn.cu: 1 row each behind 100, 1000 and 4000 keys 18.5, 42.5 and 90.9

@@ -43,6 +43,37 @@ gdn_status check_kv8_dims(const gdn_attn_dims* d) {
   return check_cache_dims(&x);
 }
 
+// Long prompts: the step's pages are brought to 16 bits first, and gdn_attn's kernel takes
+// them, whose products and probabilities need no parts. That pays from about 1000 (row, query
+// head) pairs per key/value head and request on (bringing a key of 128 elements there and
+// back costs 0.15 ns, a tile of 128 pairs saves 0.016 ns of a key; 4 x 1500..2048 rows over
+// some 9000 keys, us with against without: 32/8 heads x 128 870 and 1030, in fp16 888 and
+// 1271, x 64 668 and 994, 16/2 heads x 256 894 and 918). The copies take what the requests' tables hold, twice the cache's bytes: up to
+// kMostCopies.
+constexpr long long kWidePairs = 1024, kMostCopies = 1LL << 30;
+
+struct Wide {
+  bool on;
+  size_t table, k, v, bytes;  // offsets behind the workspace's other parts, their end
+};
+
+Wide wide_layout(const AttnDims& A, const KvBatch& B, size_t at) {
+  Wide w{};
+  const long long pages = (long long)B.R * B.max_pages;
+  const long long page = 2LL * A.Hkv * A.ps * A.D;  // bytes, of keys or values
+  w.bytes = at;
+  if (B.R == 0 || pages == 0 || (long long)B.num_rows * A.G < kWidePairs * B.R ||
+      pages > kMostCopies / (2 * page))
+    return w;
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  w.on = true;
+  w.table = up(at);
+  w.k = up(w.table + 4 * (size_t)pages);
+  w.v = up(w.k + (size_t)(pages * page));
+  w.bytes = w.v + (size_t)(pages * page);
+  return w;
+}
+
 gdn_status launched(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH; }
 
 }  // namespace
@@ -150,7 +181,9 @@ size_t gdn_kv8_attn_plan_bytes(const gdn_attn_dims* dims, const gdn_kv_batch* ba
 
 size_t gdn_kv8_attn_workspace_bytes(const gdn_attn_dims* dims, const gdn_kv_batch* batch) {
   if (check_attn(dims) != GDN_OK || check_kv_batch(batch, true) != GDN_OK) return 0;
-  return attn_layout(attn_dims(dims), kv_batch(batch)).ws_bytes;
+  const AttnDims A = attn_dims(dims);
+  const KvBatch B = kv_batch(batch);
+  return wide_layout(A, B, attn_layout(A, B).ws_bytes).bytes;
 }
 
 gdn_status gdn_kv8_attn_plan(const gdn_attn_dims* dims, const gdn_kv_batch* batch, void* plan,
@@ -178,14 +211,30 @@ gdn_status gdn_kv8_attn(const gdn_attn_dims* dims, const gdn_kv_batch* batch, co
   if (workspace_bytes < gdn_kv8_attn_workspace_bytes(dims, batch)) return GDN_ERR_WORKSPACE;
   if (batch->num_pages == 0) return GDN_ERR_INVALID_ARG;
   const AttnDims A = attn_dims(dims);
-  const int box = A.ps < kAttnKeys ? A.ps : kAttnKeys;
+  KvBatch B = kv_batch(batch);
+  const int box = A.ps < kAttnKeys ? A.ps : kAttnKeys, tokens = A.Hkv * A.ps;
+  const Kv8Cache K = cache_args(cache);
   CUtensorMap tk, tv;
-  if ((e = encode_kv8_tmap(&tk, cache->k, A.D, A.Hkv * A.ps, batch->num_pages, box)) != GDN_OK ||
-      (e = encode_kv8_tmap(&tv, cache->v, A.D, A.Hkv * A.ps, batch->num_pages, box)) != GDN_OK)
+  const Wide w = wide_layout(A, B, attn_layout(A, B).ws_bytes);
+  if (w.on) {
+    char* ws = (char*)workspace;
+    int32_t* table = (int32_t*)(ws + w.table);
+    const int pages = B.R * B.max_pages;
+    if ((e = encode_cache_tmap(&tk, ws + w.k, A.D, tokens, pages, box)) != GDN_OK ||
+        (e = encode_cache_tmap(&tv, ws + w.v, A.D, tokens, pages, box)) != GDN_OK)
+      return e;
+    if (launch_kv8_widen(A, B, dims->io_dtype, K, ws + w.k, ws + w.v, table, status,
+                         (cudaStream_t)stream) != cudaSuccess)
+      return GDN_ERR_LAUNCH;
+    B.table = table, B.num_pages = pages;
+    return launched(launch_attn(&tk, &tv, A, B, dims->io_dtype, plan, q, q_stride, ws + w.v, o, lse,
+                                workspace, status, (cudaStream_t)stream));
+  }
+  if ((e = encode_kv8_tmap(&tk, cache->k, A.D, tokens, batch->num_pages, box)) != GDN_OK ||
+      (e = encode_kv8_tmap(&tv, cache->v, A.D, tokens, batch->num_pages, box)) != GDN_OK)
     return e;
-  return launched(launch_kv8_attn(&tk, &tv, A, kv_batch(batch), dims->io_dtype, plan, q, q_stride,
-                                  cache_args(cache), o, lse, workspace, status,
-                                  (cudaStream_t)stream));
+  return launched(launch_kv8_attn(&tk, &tv, A, B, dims->io_dtype, plan, q, q_stride, K, o, lse,
+                                  workspace, status, (cudaStream_t)stream));
 }
 
 }  // extern "C"

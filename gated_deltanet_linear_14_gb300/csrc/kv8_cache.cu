@@ -373,6 +373,18 @@ kv8_append_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Ro
 
 constexpr int kReadRows = 16;  // of a place
 
+// What two codes stand for, within T's range.
+template <class T>
+__device__ __forceinline__ float2 values_of(uint16_t codes, float scale) {
+  float2 v = from_e4m3x2(codes);
+  v.x *= scale, v.y *= scale;
+  if constexpr (std::is_same<T, __half>::value) {
+    v.x = v.x > 65504.0f ? 65504.0f : v.x < -65504.0f ? -65504.0f : v.x;
+    v.y = v.y > 65504.0f ? 65504.0f : v.y < -65504.0f ? -65504.0f : v.y;
+  }
+  return v;
+}
+
 template <class T, int D>
 __global__ void __launch_bounds__(kKv8Threads, 8)
 kv8_read_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ AttnDims A,
@@ -420,12 +432,7 @@ kv8_read_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Attn
       T y[16];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        float2 v = from_e4m3x2((uint16_t)(w[k >> 1] >> (16 * (k & 1))));
-        v.x *= scale, v.y *= scale;
-        if constexpr (sizeof(T) == 2 && !std::is_same<T, bf16>::value) {
-          v.x = v.x > 65504.0f ? 65504.0f : v.x < -65504.0f ? -65504.0f : v.x;
-          v.y = v.y > 65504.0f ? 65504.0f : v.y < -65504.0f ? -65504.0f : v.y;
-        }
+        const float2 v = values_of<T>((uint16_t)(w[k >> 1] >> (16 * (k & 1))), scale);
         elem_from_f(v.x, y[2 * k]);
         elem_from_f(v.y, y[2 * k + 1]);
       }
@@ -447,16 +454,69 @@ kv8_read_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Attn
   });
 }
 
+// ------------------------------------------------------------------- widen
+
+// The pages of the step's requests, each request's own copy, to 16 bits: page i of
+// request r becomes page r * max_pages + i of the copies, which `table` then says.
+template <class T, int D>
+__global__ void __launch_bounds__(kKv8Threads, 8)
+kv8_widen_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ KvBatch B,
+                 const __grid_constant__ Kv8Cache K, T* k_out, T* v_out, int32_t* table, int packed,
+                 int32_t* status) {
+  constexpr int U = D / 16;  // lanes a token and head
+  extern __shared__ float4 kv8_smem[];
+  long long* sum = reinterpret_cast<long long*>(kv8_smem);
+  pdl_begin();
+  const int tid = threadIdx.x;
+  auto count = [&](int r) -> long long {
+    const int start = B.row_start[r], len = B.row_len[r], kv = B.kv_len[r];
+    if (!kv_request_ok(B, A.ps, start, len, kv) || len == 0) return 0;  // (the plan reports it)
+    return (kv + (long long)A.ps - 1) >> A.ps_log2;
+  };
+  each_place(B, packed, sum, count, [&](int r, long long i) {
+    const long long at = (long long)r * B.max_pages + i;
+    const int page = B.table[at], tokens = min(A.ps, B.kv_len[r] - ((int)i << A.ps_log2));
+    if (tid == 0 && blockIdx.z == 0) table[at] = (int32_t)at;
+    if (page < 0 || page >= B.num_pages) {
+      if (tid == 0 && blockIdx.z == 0) report(status, GDN_DEV_BAD_PAGE);
+      return;
+    }
+    const int total = 2 * A.Hkv * A.ps * U;
+#pragma unroll 4
+    for (int x = blockIdx.z * kKv8Threads + tid; x < total; x += gridDim.z * kKv8Threads) {
+      const int u = x % U, slot = x / U & (A.ps - 1), hh = x / U >> A.ps_log2;
+      if (slot >= tokens) continue;
+      const bool is_k = hh < A.Hkv;
+      const int h = is_k ? hh : hh - A.Hkv;
+      const size_t from = (size_t)page * A.Hkv + h, to = (size_t)at * A.Hkv + h;
+      const uint4 c = *reinterpret_cast<const uint4*>((is_k ? K.k : K.v) +
+                                                      (from * A.ps + slot) * D + 16 * u);
+      const float scale =
+          pow2(kv8_clamp((is_k ? K.k_exp : K.v_exp)[from * (A.ps >> 4) + (slot >> 4)]));
+      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+      uint32_t y[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 v = values_of<T>((uint16_t)(w[k >> 1] >> (16 * (k & 1))), scale);
+        y[k] = pack2<T>(v.x, v.y);
+      }
+      uint4* dst = reinterpret_cast<uint4*>((is_k ? k_out : v_out) + (to * A.ps + slot) * D + 16 * u);
+      dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
+      dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+    }
+  });
+}
+
 namespace {
 
 // The grid for `each` places of the longest request and about `all` in sum, with
-// `parts` blocks to share one place's work where the places are few.
+// `parts` blocks to share one place's work where the places are fewer than per_sm an SM.
 struct Grid {
   dim3 dim;
   int packed;
   size_t sum_bytes;
 };
-Grid grid_for(const KvBatch& B, long long each, long long all, int parts) {
+Grid grid_for(const KvBatch& B, long long each, long long all, int parts, int per_sm = 8) {
   Grid g{};
   // a row of the grid per request, unless most of its blocks would be empty
   g.packed = each * B.R > 2 * all && B.R <= kPackedMost;
@@ -464,7 +524,7 @@ Grid grid_for(const KvBatch& B, long long each, long long all, int parts) {
   const long long x = g.packed ? most : std::min(each, (long long)1 << 20);
   const long long blocks = g.packed ? x : x * B.R;
   int z = 1;
-  while (2 * z <= parts && 2 * z * blocks <= 8LL * device_sms()) z *= 2;
+  while (2 * z <= parts && 2 * z * blocks <= (long long)per_sm * device_sms()) z *= 2;
   g.dim = dim3((unsigned)x, g.packed ? 1 : B.R, z);
   g.sum_bytes = g.packed ? 8 * ((size_t)B.R + 1) : 0;
   return g;
@@ -527,6 +587,25 @@ cudaError_t launch_kv8_read(const RopeCall& C, const AttnDims& A, const KvBatch&
   };
   if (C.io == GDN_F32) return by_dim(float());
   return C.io == GDN_BF16 ? by_dim(bf16()) : by_dim(__half());
+}
+
+cudaError_t launch_kv8_widen(const AttnDims& A, const KvBatch& B, int io, const Kv8Cache& K,
+                             void* k_out, void* v_out, int32_t* table, int32_t* status,
+                             cudaStream_t s) {
+  const int units = 2 * A.Hkv * A.ps * (A.D / 16);
+  const Grid g = grid_for(B, B.max_pages, (long long)B.R * B.max_pages,
+                          (units + kKv8Threads - 1) / kKv8Threads / 8, 64);
+  auto by_dim = [&](auto t) {
+    using T = decltype(t);
+    auto run = [&](auto kernel) {
+      return launch_pdl(kernel, g.dim, dim3(kKv8Threads), g.sum_bytes, s, A, B, K, (T*)k_out,
+                        (T*)v_out, table, g.packed, status);
+    };
+    if (A.D == 64) return run(kv8_widen_kernel<T, 64>);
+    if (A.D == 128) return run(kv8_widen_kernel<T, 128>);
+    return run(kv8_widen_kernel<T, 256>);
+  };
+  return io == GDN_BF16 ? by_dim(bf16()) : by_dim(__half());
 }
 
 }  // namespace gdn

@@ -693,13 +693,18 @@ gdn_status gdn_kv8_read(const gdn_attn_dims* dims, const gdn_kv_batch* batch,
 
 /* The plan, the workspace and the attention over an 8-bit cache: as gdn_attn_plan
  * and gdn_attn (types, limits, groups, errors, what a row sees) with k and v as the
- * codes stand for. The plan is this call's own. q is bf16 or fp16, as is o.
+ * codes stand for. The plan is this call's own. q is bf16 or fp16, as is o. Scores,
+ * softmax statistics and sums are fp32. A NaN code reaches only the rows that see it; an
+ * infinite or NaN query row is NaN throughout.
  * Both products run on the 8-bit tensor cores, exact in the codes: q is cut into
- * parts that together hold it (2 parts in bf16, 3 in fp16: within 2^-18 of the
- * row's largest element), and so are the probabilities (within 2^-7 of each in
- * bf16, 2^-10 in fp16, down to 2^-24 of the largest and beyond). Scores, softmax
- * statistics and sums are fp32. A NaN code reaches only the rows that see it; an
- * infinite or NaN query row is NaN throughout. */
+ * parts that together hold it (2 parts in bf16, 3 in fp16: within 2^-17 of the row's
+ * largest element), and so are the probabilities (within 2^-7 + 2^-10 of each in bf16,
+ * 2^-10 in fp16, and 2^-28 of the largest). Steps of long prompts, at least 1024
+ * (row, query head) pairs per key/value head and request (num_rows * Hq / Hkv >= 1024 *
+ * num_requests) whose copies take no more than 1 GiB (num_requests * max_pages
+ * pages of 16-bit keys and values, in the workspace), bring their pages to 16 bits first:
+ * there probabilities are rounded to the io dtype, and in fp16 keys and values are what
+ * gdn_kv8_read gives. */
 size_t gdn_kv8_attn_plan_bytes(const gdn_attn_dims* dims, const gdn_kv_batch* batch);
 size_t gdn_kv8_attn_workspace_bytes(const gdn_attn_dims* dims, const gdn_kv_batch* batch);
 gdn_status gdn_kv8_attn_plan(const gdn_attn_dims* dims, const gdn_kv_batch* batch, void* plan,

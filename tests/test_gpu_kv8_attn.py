@@ -97,7 +97,10 @@ def queries(P, t, dtype, seed=0, spread=0.0):
     (5, 5, 256, 16, [70], [257]), (128, 1, 64, 16, [2, 1], [33, 31]), (12, 3, 128, 32, [129], [129]),
     (32, 8, 128, 256, [1, 1, 1], [20000, 777, 12345]), (8, 2, 64, 128, [8, 5, 8], [9000, 130, 8]),
     (16, 2, 256, 128, [2, 4], [7000, 3001]), (16, 4, 128, 16, [8, 1, 3], [5000, 4097, 3]),
-    (3, 3, 256, 32, [32, 11], [4000, 32]), (16, 1, 64, 64, [1, 1], [40000, 64])])
+    (3, 3, 256, 32, [32, 11], [4000, 32]),
+    # (long prompts, which go through 16 bits)
+    (8, 1, 128, 64, [150], [700]), (16, 1, 64, 16, [64, 80], [500, 80]),
+    (8, 1, 256, 256, [200, 130], [200, 1000]), (16, 2, 128, 32, [1, 300, 0, 260], [900, 300, 5, 777]), (16, 1, 64, 64, [1, 1], [40000, 64])])
 def test_against_64_bits(dtype, hq, hkv, d, ps, lens, kv):
     P = Paged(len(lens), max(kv), hq, hkv, d, ps, dtype, seed=d + ps)
     fill(P, seed=1)
@@ -190,11 +193,12 @@ def test_small_probabilities_that_make_up_a_part_together(dtype):
         check(P, q, o, lse, [0], [1], [n])
 
 
-@pytest.mark.parametrize("rows", [1, 8, 16, 40])
+@pytest.mark.parametrize("rows", [1, 8, 16, 40, 190])
 def test_nan_codes_reach_only_the_rows_that_see_them(rows):
     """NaN in slots past the end, in a value and in a key inside the rows' own tile."""
     kv, d = 200, 128
-    P = Paged(1, 256, 4, 2, d, 64, seed=6)
+    P = Paged(1, 256, 4 if rows < 100 else 16, 2, d, 64, seed=6)
+    half = P.dims.num_q_heads // 2   # heads of the first key head
     fill(P)
     clean = P.cache.k.clone(), P.cache.v.clone()
     at = lambda j: (int(P.table[0, j // 64]), j % 64)  # noqa: E731
@@ -210,13 +214,13 @@ def test_nan_codes_reach_only_the_rows_that_see_them(rows):
     o2, lse2 = attend(P, batch, q)
     bad = torch.zeros_like(o, dtype=torch.bool)
     sees = torch.arange(rows, device="cuda") + kv - rows >= 190
-    bad[sees, 2:, 77] = True
+    bad[sees, half:, 77] = True
     assert torch.equal(o2.isnan(), bad) and torch.equal(o2[~bad], o[~bad]) and torch.equal(lse, lse2)
     P.cache.v.copy_(clean[1])
     P.cache.k.view(torch.uint8)[page, 0, slot, 5] = 0xFF
     o3, lse3 = attend(P, batch, q)
-    assert o3[sees][:, :2].isnan().all() and lse3[sees][:, :2].isnan().all()
-    assert torch.equal(o3[~sees], o[~sees]) and torch.equal(o3[:, 2:], o[:, 2:])
+    assert o3[sees][:, :half].isnan().all() and lse3[sees][:, :half].isnan().all()
+    assert torch.equal(o3[~sees], o[~sees]) and torch.equal(o3[:, half:], o[:, half:])
 
 
 def test_strange_queries():
@@ -264,6 +268,35 @@ def test_bad_requests_and_pages():
     assert P.status.item() == gdn.CODES["GDN_DEV_BAD_ROWS"]
     check(P, q, o, lse, [0, 0, 2, 0], [1] * 4, [200, 0, 150, 0], only=(0, 2))
     assert (o[1] == 7).all() and (o[3] == 7).all()
+
+
+def test_a_long_prompt_with_a_bad_page_beside_a_good_one():
+    P = Paged(2, 400, 16, 2, 64, 32, seed=9)
+    fill(P)
+    P.table[0, 3] = -5
+    q = queries(P, 500, BF)
+    o, lse = attend(P, P.batch([0, 200], [200, 300], [400, 333]), q)
+    assert P.status.item() == gdn.CODES["GDN_DEV_BAD_PAGE"]
+    check(P, q, o, lse, [0, 200], [200, 300], [400, 333], only=(1,))
+
+
+def test_fp16_prompts_take_keys_and_values_as_read_back():
+    """Codes beyond 65504 count as it, as gdn_kv8_read gives them."""
+    P = Paged(1, 200, 8, 1, 64, 64, HF, seed=9)
+    fill(P)
+    P.cache.v_exp.fill_(12)
+    q = queries(P, 160, HF)
+    o, _ = attend(P, P.batch([0], [160], [200]), q)
+    back = torch.empty(200, 1, 64, device="cuda", dtype=HF)
+    gdn.gdn_kv8_read(P.dims, P.batch([0], [200], [200]), P.cache.codes, None, back, P.status)
+    gdn.raise_on_status(P.status)
+    assert back.abs().max() == 65504 and torch.isfinite(o).all()
+    k = P.tokens(0, 200, P.cache.k, P.cache.k_exp)[0][:, 0]
+    s = q[:, 3].double() @ k.t() / 8
+    s = torch.where(torch.arange(200, device="cuda") <= torch.arange(160, device="cuda")[:, None] + 40, s, -math.inf)
+    p = torch.softmax(s, -1)
+    want, A = p @ back[:, 0].double(), p @ back[:, 0].double().abs()
+    assert ((o[:, 3].double() - want).abs() <= 2.0 ** -8 * A + 2.0 ** -10 * want.abs()).all()
 
 
 def test_a_plan_for_other_counts_is_refused():
