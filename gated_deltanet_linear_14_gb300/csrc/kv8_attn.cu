@@ -48,7 +48,7 @@ struct Cfg8 {
   static_assert(TM_O + D <= TM_COLS, "tensor memory columns");
   static constexpr uint32_t RING = NQ * QPART;
   static constexpr uint32_t EXPS = RING + NS * UNIT;
-  static constexpr uint32_t FACTORS = EXPS + kExpSlots * 8;  // of an item's rows and the next one's
+  static constexpr uint32_t FACTORS = EXPS + kExpSlots * 48;  // of an item's rows and the next one's
   static constexpr uint32_t BARS = FACTORS + 2 * kAttnM * 4;
   static constexpr uint32_t BYTES = BARS + 8 * (2 * NS + 1 + 3 * NSB + kExpSlots) + 32;
   static_assert(BYTES <= (CTAS == 2 ? 115712 : 232448), "shared memory");
@@ -70,7 +70,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ 
   const uint32_t full = sb + C::BARS, empty = full + 8 * NS, q_full = empty + 8 * NS;
   const uint32_t s_full = q_full + 8, p_ready = s_full + 8 * NSB, o_full = p_ready + 8 * NSB;
   const uint32_t e_full = o_full + 8 * NSB;
-  uint8_t* exps = smem + C::EXPS;
+  // of a tile's four blocks: 2^a, b, 2^-b
+  float4* exps = reinterpret_cast<float4*>(smem + C::EXPS);
   float* factors = reinterpret_cast<float*>(smem + C::FACTORS);
   // [0] tensor memory, [1] a role gave up, [2..4] see `strange`
   volatile uint32_t* words = reinterpret_cast<uint32_t*>(
@@ -143,7 +144,10 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ 
       };
       auto put_exp = [&](int e) {
         const int s = tile++ % kExpSlots;
-        if (lane < 8) exps[8 * s + lane] = (uint8_t)kv8_clamp(e);
+        float* to = reinterpret_cast<float*>(exps + 3 * s) + lane;
+        e = kv8_clamp(e);
+        if (lane < 8) to[0] = lane < 4 ? pow2(e) : (float)e;
+        if (lane >= 4 && lane < 8) to[4] = pow2(-e);
         __syncwarp();
         if (lane == 0) mbar_arrive(e_full + 8 * s);
       };
@@ -434,7 +438,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ 
         const int base = it.k0 + t * kAttnKeys, nv = min(kAttnKeys, it.kend - base);
         const bool cut = mixed && base + kAttnKeys > first_seen;  // rows see different keys
         if (!(ok = wait(e_full + 8 * (tile % kExpSlots), tile / kExpSlots & 1))) break;
-        const uint2 ex = *reinterpret_cast<const uint2*>(exps + 8 * (tile % kExpSlots));
+        const float4* ex = exps + 3 * (tile % kExpSlots);
         if (!(ok = wait(s_full + 8 * b, pb))) break;
         tc_fence_after();
         // every warp is past the item before the previous one: its flag is the
@@ -450,20 +454,22 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ 
         if (rows_here) {
           const bool masked = cut || nv < kAttnKeys;
           const int lim = min(seen, it.kend) - base;
+          // of block k: the factor of its scores (kept finite and above 0, so that a
+          // masked score stays -inf), and the values' exponent
+          float ck[4], vk[4];
+          {
+            const float4 c = ex[0], v = ex[1];
+            ck[0] = c.x, ck[1] = c.y, ck[2] = c.z, ck[3] = c.w;
+            vk[0] = v.x, vk[1] = v.y, vk[2] = v.z, vk[3] = v.w;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) ck[k] = fminf(fmaxf(factor * ck[k], 0x1p-126f), 0x1p127f);
+          }
           Cols64 x;
           tm_read64(ts, x);
           if (masked) {
 #pragma unroll
             for (int e = 0; e < 64; ++e)
               if (e >= lim) x.r[e] = 0xFF800000u;  // -inf
-          }
-          // of block k: the factor of its scores (kept finite and above 0, so that a
-          // masked score stays -inf), and the values' exponent
-          float ck[4], vk[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            ck[k] = fminf(fmaxf(factor * pow2((int8_t)(ex.x >> 8 * k)), 0x1p-126f), 0x1p127f);
-            vk[k] = (float)(int8_t)(ex.y >> 8 * k);
           }
           float mx = -INFINITY;
 #pragma unroll
@@ -497,6 +503,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ 
             }
           }
           const float mc = m == -INFINITY ? 0.0f : m - kP8Up;
+          const float4 kl4 = ex[2];
+          const float kl[4] = {kl4.x, kl4.y, kl4.z, kl4.w};
           uint32_t p[16 * NP];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -514,7 +522,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ 
               sum = __fadd2_rn(sum, __fadd2_rn(s, s2));
               cut_p<NP>(pack2<__half>(s.x, s.y), pack2<__half>(s2.x, s2.y), p + 4 * k + e, 16);
             }
-            l += (sum.x + sum.y) * pow2(-(int)(int8_t)(ex.y >> 8 * k));
+            l += (sum.x + sum.y) * kl[k];
           }
           tm_store32(ts, p);
           if constexpr (NP == 3) tm_store16(ts + 32, p + 32);

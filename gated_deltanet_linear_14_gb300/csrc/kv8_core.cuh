@@ -16,9 +16,10 @@ template <> struct Parts<__half> {
   static constexpr int Q = 3, P = 3;
 };
 
-// As attn.cu's Prob<__half>: p <= 2^15, the largest power of two below e5m2's and
-// fp16's limits, and raised by steps of 2^4 at least.
-constexpr float kP8Raise = 4.0f, kP8Up = 11.0f;
+// All p carry a factor 2^kP8Up, and the running maximum is raised when a score exceeds it
+// by more than kP8Raise (in powers of two): p <= 2^15, the largest power of two below
+// e5m2's and fp16's limits. 16 equal scores at the maximum sum up to half of that.
+constexpr float kP8Raise = 5.0f, kP8Up = 10.0f;
 constexpr int kExpSlots = 16;  // tiles whose exponents are kept: more than the ring holds
 
 // Byte offset of the 16-byte chunk `chunk` of row `row` in a swizzled tile.

@@ -9,7 +9,7 @@
 // tile is dealt to all threads, one key each, N values a thread. V^^T is V's tile
 // read along its rows, P^T is written to shared memory, a key's N values side by
 // side. A pair's running maximum lies across the threads: they vote whether some
-// score exceeds it by more than 2^4, which few tiles do, and only then form the new
+// score exceeds it by more than 2^5, which few tiles do, and only then form the new
 // maxima and rescale; sums stay in registers, a key's share each, to the end.
 //
 // A tile's keys and values are read from shared memory twice or three times

@@ -699,7 +699,7 @@ gdn_status gdn_kv8_read(const gdn_attn_dims* dims, const gdn_kv_batch* batch,
  * Both products run on the 8-bit tensor cores, exact in the codes: q is cut into
  * parts that together hold it (2 parts in bf16, 3 in fp16: within 2^-17 of the row's
  * largest element), and so are the probabilities (within 2^-7 + 2^-10 of each in bf16,
- * 2^-10 in fp16, and 2^-28 of the largest). Steps of long prompts, at least 1024
+ * 2^-10 in fp16, and 2^-27 of the largest). Steps of long prompts, at least 1024
  * (row, query head) pairs per key/value head and request (num_rows * Hq / Hkv >= 1024 *
  * num_requests) whose copies take no more than 1 GiB (num_requests * max_pages
  * pages of 16-bit keys and values, in the workspace), bring their pages to 16 bits first:

@@ -5,7 +5,7 @@ How far an output may be off, with A = sum p |v| / sum p:
     fp32 sums of D products: ds = scale (2^-17 max|q| sum|k| + 2^-19 sum|q k|), at most for any key
     seen: p is off by 2 ds relative to the others, o by 4 ds A;
   p in parts: fp16's half step 2^-11 and the parts' rest, 2^-7 of p in bf16, 2^-11 in fp16, and
-    2^-17 where p = 1 has 2^11 (2^-28) for small ones: R A + n 2^-28 max|v|;
+    2^-17 where the largest p has 2^10 (2^-27 of it) for small ones: R A + n 2^-27 max|v|;
   ex2 and the fp32 sums: 2^-18 A;
   the output's rounding: eps / 2 |o|.
 lse: ds, 2^-20 of the largest score's and its own size, 2^-18."""
@@ -72,7 +72,7 @@ def check(P, q, o, lse, start, lens, kv, only=None, scale=None):
             ds = torch.where(seen, ds, 0.0).amax(-1)
             peak = p.amax(-1)
             room = ((4 * ds + REST[q.dtype] + 2.0 ** -18)[:, None] * A + want.abs() * half * 1.01
-                    + (n * 2.0 ** -28 * peak)[:, None] * vh.abs().amax(0)
+                    + (n * 2.0 ** -27 * peak)[:, None] * vh.abs().amax(0)
                     + torch.finfo(q.dtype).tiny)
             off = (o[a:a + m, h].double() - want).abs()
             assert (off <= room).all(), (r, h, (off / room).max().item())
