@@ -385,6 +385,30 @@ __device__ __forceinline__ float2 values_of(uint16_t codes, float scale) {
   return v;
 }
 
+// 16 codes times scale as elements to dst (16-byte aligned if wide).
+template <class T>
+__device__ __forceinline__ void put16(const uint4& c, float scale, T* dst, bool wide) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  float x[16];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float2 v = values_of<T>((uint16_t)(w[k >> 1] >> (16 * (k & 1))), scale);
+    x[2 * k] = v.x, x[2 * k + 1] = v.y;
+  }
+  if (wide) {
+    constexpr int PER = 16 / sizeof(T);
+#pragma unroll
+    for (int k = 0; k < 16; k += PER) {
+      Vec<T, PER> out;
+      to_vec(x + k, out);
+      out.store(dst + k);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) elem_from_f(x[k], dst[k]);
+  }
+}
+
 template <class T, int D>
 __global__ void __launch_bounds__(kKv8Threads, 8)
 kv8_read_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ AttnDims A,
@@ -427,29 +451,10 @@ kv8_read_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Attn
                                                       (head * A.ps + slot) * D + 16 * u);
       const float scale =
           pow2(kv8_clamp((is_k ? K.k_exp : K.v_exp)[head * (A.ps >> 4) + (slot >> 4)]));
-      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-      Vec<T, 16 / sizeof(T)> out[sizeof(T)];
-      T y[16];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float2 v = values_of<T>((uint16_t)(w[k >> 1] >> (16 * (k & 1))), scale);
-        elem_from_f(v.x, y[2 * k]);
-        elem_from_f(v.y, y[2 * k + 1]);
-      }
-      T* dst = (T*)(is_k ? C.k_out : C.v_out) +
-               ((long long)start + i0 + i) * (is_k ? C.kos : C.vs) + h * D + 16 * u;
-      if (C.vec == 8) {
-        constexpr int PER = 16 / sizeof(T);
-#pragma unroll
-        for (int k = 0; k < (int)sizeof(T); ++k) {
-#pragma unroll
-          for (int e = 0; e < PER; ++e) out[k].e[e] = y[PER * k + e];
-          out[k].store(dst + PER * k);
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) dst[e] = y[e];
-      }
+      put16<T>(c, scale,
+               (T*)(is_k ? C.k_out : C.v_out) +
+                   ((long long)start + i0 + i) * (is_k ? C.kos : C.vs) + h * D + 16 * u,
+               C.vec == 8);
     }
   });
 }
@@ -481,29 +486,20 @@ kv8_widen_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ KvB
       if (tid == 0 && blockIdx.z == 0) report(status, GDN_DEV_BAD_PAGE);
       return;
     }
-    const int total = 2 * A.Hkv * A.ps * U;
+    // (a page's tokens of all heads lie side by side, in the cache and in the copy)
+    const int total = A.Hkv * A.ps * U;
+    const size_t from = (size_t)page * A.Hkv * A.ps * D, to = (size_t)at * A.Hkv * A.ps * D;
+    const size_t exp = (size_t)page * A.Hkv * (A.ps >> 4);
+    auto all = [&](const uint8_t* codes, const int8_t* exps, T* out) {
 #pragma unroll 4
-    for (int x = blockIdx.z * kKv8Threads + tid; x < total; x += gridDim.z * kKv8Threads) {
-      const int u = x % U, slot = x / U & (A.ps - 1), hh = x / U >> A.ps_log2;
-      if (slot >= tokens) continue;
-      const bool is_k = hh < A.Hkv;
-      const int h = is_k ? hh : hh - A.Hkv;
-      const size_t from = (size_t)page * A.Hkv + h, to = (size_t)at * A.Hkv + h;
-      const uint4 c = *reinterpret_cast<const uint4*>((is_k ? K.k : K.v) +
-                                                      (from * A.ps + slot) * D + 16 * u);
-      const float scale =
-          pow2(kv8_clamp((is_k ? K.k_exp : K.v_exp)[from * (A.ps >> 4) + (slot >> 4)]));
-      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-      uint32_t y[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float2 v = values_of<T>((uint16_t)(w[k >> 1] >> (16 * (k & 1))), scale);
-        y[k] = pack2<T>(v.x, v.y);
+      for (int x = blockIdx.z * kKv8Threads + tid; x < total; x += gridDim.z * kKv8Threads) {
+        if ((x / U & (A.ps - 1)) >= tokens) continue;
+        put16<T>(*reinterpret_cast<const uint4*>(codes + from + 16 * (size_t)x),
+                 pow2(kv8_clamp(exps[exp + x / (16 * U)])), out + to + 16 * (size_t)x, true);
       }
-      uint4* dst = reinterpret_cast<uint4*>((is_k ? k_out : v_out) + (to * A.ps + slot) * D + 16 * u);
-      dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
-      dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
-    }
+    };
+    all(K.k, K.k_exp, k_out);
+    all(K.v, K.v_exp, v_out);
   });
 }
 
@@ -592,9 +588,9 @@ cudaError_t launch_kv8_read(const RopeCall& C, const AttnDims& A, const KvBatch&
 cudaError_t launch_kv8_widen(const AttnDims& A, const KvBatch& B, int io, const Kv8Cache& K,
                              void* k_out, void* v_out, int32_t* table, int32_t* status,
                              cudaStream_t s) {
-  const int units = 2 * A.Hkv * A.ps * (A.D / 16);
+  const int units = A.Hkv * A.ps * (A.D / 16);
   const Grid g = grid_for(B, B.max_pages, (long long)B.R * B.max_pages,
-                          (units + kKv8Threads - 1) / kKv8Threads / 8, 64);
+                          units / kKv8Threads / 4, 64);
   auto by_dim = [&](auto t) {
     using T = decltype(t);
     auto run = [&](auto kernel) {
