@@ -162,13 +162,23 @@ kv8_append_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Ro
     if (!good && tid == 0 && z == 0) report(status, GDN_DEV_BAD_PAGE);
     // (called when a thread's first rows are on their way)
     auto angles = [&] {
-      for (int x = tid; x < kKv8Block * half; x += kKv8Threads) {
-        const int i = x / half, j = x - i * half;
-        if (i < lo || i >= hi) continue;
-        int ax = R.axis ? R.axis[j] : 0;
-        if (ax < 0 || ax >= R.axes) ax = 0;
-        const float2 cs = cos_sin(R.pos[(size_t)ax * R.num_rows + row0 + i], R.inv_freq[j]);
-        c_tab[x] = cs.x, s_tab[x] = cs.y;
+      auto angle = [&](int i, int j, int ax, float f) {
+        const float2 cs = cos_sin(R.pos[(size_t)ax * R.num_rows + row0 + i], f);
+        c_tab[i * half + j] = cs.x, s_tab[i * half + j] = cs.y;
+      };
+      auto axis_of = [&](int j) {
+        const int ax = R.axis ? R.axis[j] : 0;
+        return ax < 0 || ax >= R.axes ? 0 : ax;
+      };
+      if (half > 0 && kKv8Threads % half == 0) {  // a thread has the same pair of several rows
+        const int j = tid % half, ax = axis_of(j);
+        const float f = R.inv_freq[j];
+        for (int i = lo + tid / half; i < hi; i += kKv8Threads / half) angle(i, j, ax, f);
+      } else {
+        for (int x = lo * half + tid; x < hi * half; x += kKv8Threads) {
+          const int i = x / half, j = x - i * half;
+          angle(i, j, axis_of(j), R.inv_freq[j]);
+        }
       }
       __syncthreads();
     };
@@ -295,8 +305,10 @@ kv8_append_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Ro
       const int e8 = max(kv8_exponent(top), before);
       const float2 ss = make_float2(pow2(-e8), pow2(-e8));
       // A key within 4 ulp of the middle between two codes is formed again in 64 bits: in fp32
-      // it may have come to the wrong side. (A hundred thousandth of them; those below 2^-6,
-      // whose codes are 2^-9 apart, are left.)
+      // it may have come to the wrong side. (A hundred thousandth of them. Left are those below
+      // 2^-6, whose codes are 2^-9 apart, what a turn makes much smaller than its pair,
+      // which fp32 misses by more, and without a norm those on the middle itself, as
+      // 16-bit values often are that do not turn.)
       unsigned long long near = 0;
 #pragma unroll
       for (int n = 0; n < TURNS; ++n) {
@@ -306,13 +318,16 @@ kv8_append_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Ro
           x[n][e] = y.x, x[n][e + 1] = y.y;
         }
         if (role == ROLE_K && (N.on || R.rd)) {
-          uint32_t bits = 0;
+          auto beside = [&](int e) { return (__float_as_uint(x[n][e]) + 0x80004u) & 0xFFFFFu; };
+          uint32_t least = ~0u;  // (most lanes have none)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const uint32_t w = __float_as_uint(x[n][e]);
-            if (((w + 0x80004u) & 0xFFFFF) < 8u && fabsf(x[n][e]) >= 0x1p-6f) bits |= 1u << e;
+          for (int e = 0; e < 16; ++e) least = min(least, beside(e));
+          if (least < 8 && here(n) && (N.on || rot)) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (beside(e) < 8 && (N.on || beside(e) != 4) && fabsf(x[n][e]) >= 0x1p-6f)
+                near |= 1ull << (16 * n + e);
           }
-          if (here(n)) near |= (unsigned long long)bits << (16 * n);
         }
       }
 #pragma unroll 1

@@ -314,3 +314,34 @@ def test_captured_and_replayed_on_two_streams():
         assert ((back - v).abs().double() <= v.abs().amax().double() * 2.0 ** -4).all()
         x, _ = P.tokens(3, 33, P.cache.v, P.cache.v_exp)
         assert torch.equal(back[60:80].double(), x[13:])
+
+
+@pytest.mark.parametrize("norm_on", [True, False])
+def test_keys_next_to_the_middle_of_two_codes_come_to_the_right_one(norm_on):
+    """Codes of keys as a rounding of the 64-bit values gives them: of 2 million keys dozens lie within
+    4 ulp of the middle between two codes (8 of the 2^20 ulp from one middle to the next), where
+    fp32 may err. Not counted: keys smaller than the other of their pair (a turn errs by ulp of
+    |x| + |y|, c = (|x| + |y|) / |x| times as many of x's own: at c > 2 more than the 4) and keys below
+    2^-5 of their block's scale, which are left to the fp32 value; all are held to half a step
+    and 2^-18 of the pair by test_append_and_read."""
+    T, d, hkv = 4096, 128, 4
+    P = Paged(1, T, 4, hkv, d, 64, seed=21)
+    _, k, v = rows_for(P, T, seed=4, spread=0.3)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    kw = 1 + 0.3 * torch.randn(d, generator=g, device="cuda")
+    inv = (1e4 ** -(torch.arange(d // 2, device="cuda").double() / (d // 2))).float()
+    pos = torch.arange(7, T + 7, device="cuda", dtype=torch.int32)
+    norm = gdn.make_head_norm(None, kw, eps=1e-6) if norm_on else None
+    gdn.gdn_kv8_append(P.dims, P.batch([0], [T], [T]), norm, gdn.make_rope(d, inv, pos), None, k, v,
+                       None, P.cache.codes, P.status)
+    gdn.raise_on_status(P.status)
+    y = normed(k, kw, 1e-6, 0.0) if norm_on else k.double()
+    turned = rotated(y, d, inv, pos)
+    want = Blocks(hkv, d)
+    want.append(turned, 0)
+    x, e = P.tokens(0, T, P.cache.k, P.cache.k_exp)
+    larger = turned.abs() >= turned.roll(d // 2, -1).abs()
+    same = (e == want.e).repeat_interleave(BLOCK, 0)[..., None]
+    unit = torch.exp2(e.double()).repeat_interleave(BLOCK, 0)[..., None]
+    counted = same & larger & (want.x.abs() >= 2.0 ** -5 * unit)
+    assert counted.sum() > 10 ** 6 and not ((x != want.x) & counted).any()
