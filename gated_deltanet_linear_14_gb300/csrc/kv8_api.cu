@@ -46,10 +46,10 @@ gdn_status check_kv8_dims(const gdn_attn_dims* d) {
 // Long prompts: the step's pages are brought to 16 bits first, and gdn_attn's kernel takes
 // them, whose products and probabilities need no parts. That pays from about 1000 (row, query
 // head) pairs per key/value head and request on (bringing a key of 128 elements there and
-// back costs 0.15 ns, a tile of 128 pairs saves 0.016 ns of a key; 4 x 1500..2048 rows over
-// some 9000 keys, us with against without: 32/8 heads x 128 870 and 1030, in fp16 888 and
-// 1271, x 64 668 and 994, 16/2 heads x 256 894 and 918). The copies take what the requests' tables hold, twice the cache's bytes: up to
-// kMostCopies.
+// back costs 0.15 ns, a tile of 128 pairs saves 0.016 ns of a key; 4 x 1500..2048 rows behind
+// 8192 shared keys, us with against without: 32/8 heads x 128 787 and 1030, in fp16 810 and
+// 1271, x 64 653 and 994, 16/2 heads x 256 876 and 918; 16 x 64..512 rows, 64.7 and 74.0). The
+// copies may take what the requests' tables hold, twice the cache's bytes: up to kMostCopies.
 constexpr long long kWidePairs = 1024, kMostCopies = 1LL << 30;
 
 struct Wide {

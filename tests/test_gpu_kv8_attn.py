@@ -280,6 +280,25 @@ def test_a_long_prompt_with_a_bad_page_beside_a_good_one():
     check(P, q, o, lse, [0, 200], [200, 300], [400, 333], only=(1,))
 
 
+def test_long_prompts_behind_shared_pages():
+    """Pages are brought to 16 bits once for a group, but for those that its first request has not
+    (a shorter one, one without rows) or not the same, whatever is declared."""
+    R, ps, lens = 7, 32, [200, 150, 190, 0, 170, 160, 150]
+    kv = [1000, 900, 1100, 640, 700, 300, 1200]
+    P = Paged(R, max(kv), 16, 2, 64, ps, seed=10)
+    P.table[1:3, :20] = P.table[0, :20].clone()
+    P.table[4, :20] = P.table[3, :20].clone()     # first: no rows
+    P.table[6, :20] = P.table[5, :20].clone()     # first: 300 keys, 9 whole pages
+    P.table[6, 4] = P.table[6, 25]                # not the same after all
+    fill(P)
+    start = [sum(lens[:r]) for r in range(R)]
+    q = queries(P, sum(lens), BF)
+    groups = i32([0, 3, 5]), i32([3, 2, 2]), i32([20, 20, 20])
+    o, lse = attend(P, P.batch(start, lens, kv, groups=groups), q)
+    gdn.raise_on_status(P.status)
+    check(P, q, o, lse, start, lens, kv)
+
+
 def test_fp16_prompts_take_keys_and_values_as_read_back():
     """Codes beyond 65504 count as it, as gdn_kv8_read gives them."""
     P = Paged(1, 200, 8, 1, 64, 64, HF, seed=9)
