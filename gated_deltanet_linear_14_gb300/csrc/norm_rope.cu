@@ -3,7 +3,10 @@
 // (angles.cuh).
 //
 // One read and one write of every element, about ten flops each: bound by
-// memory. The lanes of a head hold it in registers between the sum of its squares
+// memory, beside the issue of some 160 instructions for a lane's 16 elements. Measured
+// (GB300): 22 k rows of 40 heads x 128, bf16: 83 us, 5.5 TB/s, 0.82 of the copy rate (107 us
+// with five heads a thread, weights and angles formed anew for each; 103 us where a
+// branch kept the heads in flight from overlapping). The lanes of a head hold it in registers between the sum of its squares
 // (shuffles) and the rest, so that it is read once; cosines, sines and weights
 // lie in shared memory, formed once per block for all heads of its rows while the
 // first heads are in flight, and go to registers for a thread's heads of a row.
