@@ -379,3 +379,56 @@ def test_a_step_captured_append_plan_attention():
         graph.replay()
         gdn.raise_on_status(P.status)
         check(P, q_out, o, None, list(range(R)), [1] * R, kv_len.tolist())
+
+
+@pytest.mark.parametrize("lens,kv", [([1] * 6, [700] * 6), ([9] * 6, [700, 9, 64, 128, 300, 30]),
+                                     ([300] * 2, [700, 333])])
+def test_two_calls_at_once(lens, kv):
+    """The same step on two streams with caches and workspaces of their own, as one after the other."""
+    start = [sum(lens[:r]) for r in range(len(lens))]
+    made = []
+    for seed in range(2):
+        P = Paged(len(lens), max(kv), 16, 4, 128, 32, seed=seed)
+        fill(P, seed=seed)
+        batch, q = P.batch(start, lens, kv), queries(P, sum(lens), BF, seed=seed)
+        plan, ws = planned(P, batch)
+        made.append((P, batch, q, plan, ws, [torch.empty_like(q) for _ in range(2)], torch.cuda.Stream()))
+
+    def run(m, out, stream):
+        P, batch, q, plan, ws = m[:5]
+        for _ in range(5):
+            gdn.gdn_kv8_attn(P.dims, batch, plan, q, P.cache.codes, m[5][out], None, ws, ws.numel(),
+                             P.status, stream=stream)
+
+    for m in made:
+        run(m, 0, None)
+    torch.cuda.synchronize()
+    for m in made:
+        run(m, 1, m[6])
+    torch.cuda.synchronize()
+    for m in made:
+        gdn.raise_on_status(m[0].status)
+        assert torch.equal(*m[5])
+
+
+def test_requests_without_rows_or_keys():
+    lens, kv = [0, 1, 0, 2], [0, 1, 40, 2]
+    P = Paged(4, 48, 4, 2, 64, 16, seed=12)
+    fill(P)
+    q = queries(P, 5, BF)
+    o, lse = attend(P, P.batch([0, 0, 1, 1], lens, kv, rows=5), q)
+    gdn.raise_on_status(P.status)
+    check(P, q, o, lse, [0, 0, 1, 1], lens, kv)
+    assert (o[3:] == 7).all() and (lse[3:] == 7).all()
+
+
+def test_one_very_long_history():
+    """300 000 keys of one row and of a few, cut among all CTAs and joined."""
+    n = 300001
+    P = Paged(1, n, 8, 2, 64, 256, seed=13)
+    fill(P, spread=0.2)
+    for m in (1, 12):
+        q = queries(P, m, BF)
+        o, lse = attend(P, P.batch([0], [m], [n]), q)
+        gdn.raise_on_status(P.status)
+        check(P, q, o, lse, [0], [m], [n])

@@ -345,3 +345,30 @@ def test_keys_next_to_the_middle_of_two_codes_come_to_the_right_one(norm_on):
     unit = torch.exp2(e.double()).repeat_interleave(BLOCK, 0)[..., None]
     counted = same & larger & (want.x.abs() >= 2.0 ** -5 * unit)
     assert counted.sum() > 10 ** 6 and not ((x != want.x) & counted).any()
+
+
+def test_query_rows_of_no_request_keep_what_they_hold():
+    P = Paged(2, 40, 4, 2, 128, 16)
+    q, k, v = rows_for(P, 12)
+    out = torch.full((12, 4, 128), 7.0, device="cuda", dtype=BF)
+    batch = P.batch([2, 9], [5, 0], [20, 0], rows=12)
+    gdn.gdn_kv8_append(P.dims, batch, gdn.make_head_norm(eps=1e-6), None, q, k, v, out,
+                       P.cache.codes, P.status)
+    gdn.raise_on_status(P.status)
+    assert (out[:2] == 7).all() and (out[7:] == 7).all()
+    want = normed(q[2:7], None, 1e-6, 0.0)
+    assert ((out[2:7].double() - want).abs() <= want.abs() * 2.0 ** -8 * 1.01 + 1e-7).all()
+
+
+def test_queries_in_place():
+    P = Paged(1, 70, 4, 1, 256, 64)
+    q, k, v = rows_for(P, 70)
+    q2, other = q.contiguous(), torch.empty(70, 4, 256, device="cuda", dtype=BF)
+    norm = gdn.make_head_norm(torch.rand(256, device="cuda"), None, eps=1e-6)
+    inv = torch.logspace(0, -4, 64, device="cuda")
+    rope = gdn.make_rope(128, inv, torch.arange(70, device="cuda", dtype=torch.int32), interleaved=True)
+    batch = P.batch([0], [70], [70])
+    gdn.gdn_kv8_append(P.dims, batch, norm, rope, q, k, v, other, P.cache.codes, P.status)
+    gdn.gdn_kv8_append(P.dims, batch, norm, rope, q2, k, v, q2, P.cache.codes, P.status)
+    gdn.raise_on_status(P.status)
+    assert torch.equal(q2, other)
