@@ -99,8 +99,8 @@ gdn_status gdn_attn_plan(const gdn_attn_dims* dims, const gdn_kv_batch* batch, v
   if ((e = check_kv_batch(batch, true)) != GDN_OK) return e;
   if (!plan || !status || ((uintptr_t)plan & 15) != 0) return GDN_ERR_INVALID_ARG;
   if (plan_bytes < gdn_attn_plan_bytes(dims, batch)) return GDN_ERR_WORKSPACE;
-  return launch_attn_plan(attn_dims(dims), kv_batch(batch), plan, status, (cudaStream_t)stream) ==
-                 cudaSuccess
+  return launch_attn_plan(attn_dims(dims), kv_batch(batch), false, plan, status,
+                          (cudaStream_t)stream) == cudaSuccess
              ? GDN_OK
              : GDN_ERR_LAUNCH;
 }

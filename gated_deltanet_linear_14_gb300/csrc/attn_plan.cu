@@ -82,7 +82,7 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads)
-attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, AttnStamp stamp, char* plan,
+attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, AttnStamp stamp, bool codes8, char* plan,
                  int32_t* status) {
   __shared__ unsigned long long scan64[32];
   __shared__ int scan32[32];
@@ -91,6 +91,7 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, AttnStamp stamp, char* pla
   __shared__ unsigned long long used_s[kPlanThreads], share_s;
   __shared__ int cut_s[kRounds], cuts_s[kRounds];
   __shared__ unsigned long long saved_s;
+  __shared__ int alone_s;  // tiles of a piece that has its CTA alone
   __shared__ int longest_s, group_tiles_s;  // of the requests' items, of the groups'
   pdl_begin();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, NG = B.num_groups;
@@ -186,7 +187,7 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, AttnStamp stamp, char* pla
   const bool sharing = saved_s > (unsigned long long)kMinSaved * L.ctas;
   if (!sharing)  // not worth the join
     for (int g = tid; g < NG; g += kPlanThreads) g_shared[g] = g_rows[g] = 0;
-  const unsigned own_cost = item_cost(A, B, sharing);
+  const unsigned own_cost = item_cost(A, B, sharing, codes8);
   __syncthreads();
   int list_rows = 0;
   for (int b = 0; b < NG; b += kPlanThreads) {
@@ -327,6 +328,39 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, AttnStamp stamp, char* pla
     at += total;
   }
   __syncthreads();
+  // Few items over an 8-bit cache: pieces that have a CTA each (least_piece8), all of
+  // cost `alone`, so that each part of the line holds one of them.
+  unsigned alone = 0;
+  if (codes8 && own_first == 0 && n_items > 0 && (long long)n_items * A.Hkv <= L.ctas) {
+    auto pieces = [](int tiles, int t) { return (max(tiles, 1) + t - 1) / t; };
+    if (warp == 0) {
+      auto fits = [&](int t) {
+        int n = 0;
+        for (int i = lane; i < n_items; i += 32) n += min(pieces(items[i].tiles, t), L.ctas);
+        return (long long)__reduce_add_sync(~0u, n) * A.Hkv <= L.ctas;
+      };
+      int lo = least_piece8(longest_s), hi = max(longest_s, lo);  // (hi fits)
+      if (fits(lo)) hi = lo;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (fits(mid)) hi = mid;
+        else lo = mid + 1;
+      }
+      if (lane == 0) alone_s = hi;
+    }
+    __syncthreads();
+    const int t = alone_s;
+    const unsigned part = t * kTileCost + own_cost;
+    const unsigned least = kTileCost * least_piece8(longest_s) + own_cost;
+    if (part <= max((at + L.ctas - 1) / L.ctas, (unsigned long long)least) + own_cost) {
+      alone = part;
+      const bool mine = tid < n_items;  // (n_items <= ctas <= kPlanThreads)
+      const unsigned cost = mine ? pieces(items[tid].tiles, t) * part : 0;
+      const unsigned long long off = block_scan((unsigned long long)cost * A.Hkv, at, scan64);
+      if (mine) items[tid].cost = cost, items[tid].off = off;
+      __syncthreads();
+    }
+  }
   // Of the ways to cut the groups' items, the one that ends first: its longest
   // CTA, or everybody's part where the requests' items fill that up.
   int len = 0, rounds = 0;
@@ -383,7 +417,7 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, AttnStamp stamp, char* pla
   __syncthreads();
   // What is left to each CTA beside its units, so that all end together; less
   // than the shortest piece and an item's own cost is not worth beginning.
-  const unsigned least = kTileCost * least_piece(longest_s) + own_cost;
+  const unsigned least = alone ? alone : kTileCost * least_piece(longest_s) + own_cost;
   unsigned long long used = 0;
   if (tid < L.ctas)
     for (int k = tid; k < n_units; k += L.ctas)
@@ -485,11 +519,11 @@ attn_plan_kernel(AttnDims A, KvBatch B, AttnLayout L, AttnStamp stamp, char* pla
   }
 }
 
-cudaError_t launch_attn_plan(const AttnDims& A, const KvBatch& B, void* plan, int32_t* status,
-                             cudaStream_t s) {
+cudaError_t launch_attn_plan(const AttnDims& A, const KvBatch& B, bool codes8, void* plan,
+                             int32_t* status, cudaStream_t s) {
   const AttnLayout L = attn_layout(A, B);
   return launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, A, B, L,
-                    plan_stamp(A, B, L.ctas), (char*)plan, status);
+                    plan_stamp(A, B, L.ctas), codes8, (char*)plan, status);
 }
 
 // ---------------------------------------------------------------- the join

@@ -32,8 +32,14 @@ constexpr unsigned kTileCost = 4;
 // 1.3 us a tile (D = 128). Where it is bound by the SMs: 2.1 us against 0.75
 // (D = 64), 3.1 against 0.7 (D = 128), 4.0 against 1.1 (D = 256). (Of 8, 12, 14
 // and 20 for the latter, 20 measured best on all three.)
-__host__ __device__ inline unsigned item_cost(const AttnDims& A, const KvBatch& B, bool sharing) {
-  return !sharing && (long long)B.max_rows * A.G <= 64 ? 3 : 20;
+//
+// Over an 8-bit cache (`codes8`) a tile takes half the memory's time, and an item's
+// start and end are not covered: 20 there too (1 row of 64 requests behind up to 2000
+// keys, us with 3, 12, 20 and 32: 56, 46, 43 and 42.5; 512 requests behind up to 1500:
+// 260, 245, 233 and 227; 64 behind up to 300: 23.9, 22.0, 22.5 and 23.0).
+__host__ __device__ inline unsigned item_cost(const AttnDims& A, const KvBatch& B, bool sharing,
+                                              bool codes8) {
+  return !codes8 && !sharing && (long long)B.max_rows * A.G <= 64 ? 3 : 20;
 }
 // Tiles below which an item of T is not cut: a piece more costs the join about
 // a twelfth of a tile's time, so cutting further than this pays with the join
@@ -42,6 +48,19 @@ __host__ __device__ inline int least_piece(int T) {
   int n = 1;
   while (n < 64 && 12 * n * n < T) ++n;
   return n;
+}
+// Over an 8-bit cache: where the requests' items, one to a CTA and head, leave CTAs
+// over, and no group shares, every item is cut into equal pieces that have a CTA each,
+// the pieces as short as there are CTAs for, of at least this many tiles. A CTA whose
+// part of the line crossed from one item into the next took both one after the other,
+// and their starts and ends are most of so short a step (1 row, 32/8 heads x 128, us
+// cut so against along the line: 1 request behind 64, 512 and 8000 keys 6.8, 9.0 and
+// 12.1 against 12.1, 10.5 and 15.3; 8 behind up to 500 10.0 against 14.0. With pieces
+// of one tile 64 keys took 8.9, of at least three 512 keys 10.7). The line stays where
+// the longest piece would take longer than everybody's part and an item's cost.
+__host__ __device__ inline int least_piece8(int T) {
+  const int n = least_piece(T);
+  return n > 2 ? n : 2;
 }
 // A request joins its group's shared pass with up to this many (row, head)
 // pairs; above, its own tiles are full enough to read the shared keys alone
@@ -222,8 +241,8 @@ __device__ __forceinline__ void piece_tiles(const AttnItem& it, unsigned long lo
 
 int attn_ctas_per_sm(int D);
 AttnLayout attn_layout(const AttnDims& A, const KvBatch& B);
-cudaError_t launch_attn_plan(const AttnDims& A, const KvBatch& B, void* plan, int32_t* status,
-                             cudaStream_t s);
+cudaError_t launch_attn_plan(const AttnDims& A, const KvBatch& B, bool codes8, void* plan,
+                             int32_t* status, cudaStream_t s);
 cudaError_t launch_attn_join(const AttnDims& A, const KvBatch& B, int io, const void* plan,
                              const void* ws, void* o, float* lse, cudaStream_t s);
 // tk, tv: CUtensorMaps of the caches (16-bit elements, [pages][Hkv * page_size][D],

@@ -192,7 +192,7 @@ gdn_status gdn_kv8_attn_plan(const gdn_attn_dims* dims, const gdn_kv_batch* batc
   if (e != GDN_OK || (e = check_kv_batch(batch, true)) != GDN_OK) return e;
   if (!plan || !status || ((uintptr_t)plan & 15) != 0) return GDN_ERR_INVALID_ARG;
   if (plan_bytes < gdn_kv8_attn_plan_bytes(dims, batch)) return GDN_ERR_WORKSPACE;
-  return launched(launch_attn_plan(attn_dims(dims), kv_batch(batch), plan, status,
+  return launched(launch_attn_plan(attn_dims(dims), kv_batch(batch), true, plan, status,
                                    (cudaStream_t)stream));
 }
 

@@ -432,3 +432,35 @@ def test_one_very_long_history():
         o, lse = attend(P, P.batch([0], [m], [n]), q)
         gdn.raise_on_status(P.status)
         check(P, q, o, lse, [0], [m], [n])
+
+
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("beside", [-1, 0, 1])
+@pytest.mark.parametrize("rows", [1, 9])
+def test_as_many_items_as_blocks(d, beside, rows):
+    # (a block of threads an item, one item fewer and one more; two blocks to a
+    # multiprocessor at D = 64, one at 256)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    n = sms * (1 if d == 256 else 2) + beside
+    lens = [rows] * n
+    kv = [rows + (r * 37) % 200 for r in range(n)]
+    kv[n // 2] = 3000
+    P = Paged(n, max(kv), 3, 1, d, 32, BF)
+    fill(P, seed=7)
+    start = [rows * r for r in range(n)]
+    q = queries(P, rows * n, BF, seed=1)
+    o, lse = attend(P, P.batch(start, lens, kv), q)
+    gdn.raise_on_status(P.status)
+    check(P, q, o, lse, start, lens, kv)
+
+
+@pytest.mark.parametrize("n", [1, 63, 64, 65, 128, 129, 192, 193, 511, 1537, 6000, 48000])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_one_request_over_all_blocks(n, rows):
+    rows = min(n, rows)
+    P = Paged(1, n, 8, 2, 128, 64, BF)
+    fill(P, seed=n)
+    q = queries(P, rows, BF, seed=2)
+    o, lse = attend(P, P.batch([0], [rows], [n]), q)
+    gdn.raise_on_status(P.status)
+    check(P, q, o, lse, [0], [rows], [n])
