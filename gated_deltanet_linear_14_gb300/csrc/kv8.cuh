@@ -63,9 +63,9 @@ cudaError_t launch_kv8_widen(const AttnDims& A, const KvBatch& B, int io, const 
 
 // Whether kv8_decode.cu takes the step: at most 16 (row, query head) pairs per key/value
 // head and request, and nothing declared shared. (64 requests, 32/8 heads x 128, us there
-// against kv8_attn.cu: 1 row each behind 100, 1000 and 4000 keys 18.5, 42.5 and 90.9
-// against 23.5, 53.0 and 111.6; 4 rows each 20.1, 46.5 and 94.5 against 23.6, 55.7 and
-// 114.4. With 32 columns the softmax's registers and code made it the slower one.)
+// against kv8_attn.cu: 1 row each behind 100, 1000 and 4000 keys 18.1, 42.2 and 91.0
+// against 21.5, 48.4 and 104.8; 4 rows each 19.9, 45.4 and 93.5 against 22.3, 52.2 and
+// 105.9; one row behind 512 9.0 against 10.1. With 32 columns the softmax's registers and code made it the slower one.)
 bool kv8_few_pairs(const AttnDims& A, const KvBatch& B);
 // tk, tv: CUtensorMaps of the codes ([pages][Hkv * page_size][D], boxes of min(D, 128)
 // codes x min(page_size, 64) tokens, swizzled over a box's row). The plan is

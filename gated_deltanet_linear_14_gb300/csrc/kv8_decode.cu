@@ -15,9 +15,9 @@
 // A tile's keys and values are read from shared memory twice, in fp16 three times
 // (once for each part of q and p); per 128 keys and D = 128 some 96 KB go through
 // it, against 1400 cycles that their 32 KB take from memory: bound by HBM. Measured (GB300,
-// join included): 64 requests of 1 row and up to 32767 keys, 32/8 heads x 128: 332 us for 2.08
-// GB, 6.3 TB/s, 0.94 of the copy rate; 96 of 16/2 heads x 256 and up to 12000 keys: 118 us, 0.89;
-// one row of 513 keys: 12.5 us, latency.
+// join included): 64 requests of 1 row and up to 32767 keys, 32/8 heads x 128: 329 us for 2.08
+// GB, 6.3 TB/s, 0.95 of the copy rate; 96 of 16/2 heads x 256 and up to 12000 keys: 117 us, 0.90;
+// one row of 513 keys: 9.1 us, latency.
 #include <cuda.h>
 
 #include <type_traits>
