@@ -94,21 +94,25 @@ __device__ __forceinline__ float exact_key(const T* row, int d, int d2, bool fir
                                            const HeadNorm& N, int e) {
   double x = (double)elem_to_f(row[d]), y = d2 >= 0 ? (double)elem_to_f(row[d2]) : 0.0;
   if (N.on) {
-    // (squares of 16-bit values are exact in fp32)
-    float v[D / 32];
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) v[i] = elem_to_f(row[32 * i + (threadIdx.x & 31)]);
+    // (in 64 bits, which hold the squares of all that fp32 does)
     double ss = 0.0;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) ss += (double)(v[i] * v[i]);
+    for (int i = 0; i < D / 32; ++i) {
+      const double v = (double)elem_to_f(row[32 * i + (threadIdx.x & 31)]);
+      ss = __fma_rn(v, v, ss);
+    }
 #pragma unroll 1
     for (int i = 16; i; i >>= 1) ss += __shfl_xor_sync(~0u, ss, i);
-    const double mean = ss * (1.0 / D) + (double)N.eps;
-    // (an estimate and two steps of Newton; what leaves fp32's range is not here: those rows'
-    // fp32 values are as good as any)
-    double inv = (double)rsqrtf((float)mean);
+    // mean = m 4^h with m in [1, 4), within fp32's range: an estimate and two steps of Newton
+    // for its root, and 2^-h (no such h where the mean is 0, but then the fp32 value is NaN
+    // and not formed again)
+    double m = ss * (1.0 / D) + (double)N.eps;
+    const int h2 = ((__double2hiint(m) >> 20 & 0x7FF) - 1023) & ~1;
+    m *= __hiloint2double((1023 - h2) << 20, 0);
+    double inv = (double)rsqrtf((float)m);
 #pragma unroll 1
-    for (int i = 0; i < 2; ++i) inv *= 1.5 - 0.5 * mean * inv * inv;
+    for (int i = 0; i < 2; ++i) inv *= 1.5 - 0.5 * m * inv * inv;
+    inv *= __hiloint2double((1023 - h2 / 2) << 20, 0);
     auto weight = [&](int i) { return N.kw ? (double)N.offset + (double)N.kw[i] : 1.0; };
     x *= inv * weight(d);
     if (d2 >= 0) y *= inv * weight(d2);

@@ -372,3 +372,52 @@ def test_queries_in_place():
     gdn.gdn_kv8_append(P.dims, batch, norm, rope, q2, k, v, q2, P.cache.codes, P.status)
     gdn.raise_on_status(P.status)
     assert torch.equal(q2, other)
+
+
+def _codes_of_normed_keys(P, k, kw, eps, inv, pos):
+    """The keys as stored, and those and the exponents that 64 bits give."""
+    T, hkv, d = k.shape
+    norm = gdn.make_head_norm(None, kw, eps=eps)
+    gdn.gdn_kv8_append(P.dims, P.batch([0], [T], [T]), norm, gdn.make_rope(d, inv, pos), None, k, k,
+                       None, P.cache.codes, P.status)
+    gdn.raise_on_status(P.status)
+    turned = rotated(normed(k, kw, eps, 0.0), d, inv, pos)
+    want = Blocks(hkv, d)
+    want.append(turned, 0)
+    return *P.tokens(0, T, P.cache.k, P.cache.k_exp), turned, want
+
+
+@pytest.mark.parametrize("size,eps", [(1e25, 1e-6), (3e37, 1e-6), (1e-25, 0.0),
+                                      (1e-32, 2.0 ** -100), (1e-22, 2.0 ** -126)])
+def test_keys_whose_squares_leave_the_range(size, eps):
+    """bf16 has fp32's range, the squares of its ends do not fit it. Of a million keys some ten lie
+    next to a middle and are formed again; the others as in test_append_and_read."""
+    T, d, hkv = 2048, 128, 4
+    P = Paged(1, T, 4, hkv, d, 64, seed=22)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    k = (torch.randn(T, hkv, d, generator=g, device="cuda") * size).to(BF)
+    kw = 1 + 0.3 * torch.randn(d, generator=g, device="cuda")
+    inv = (1e4 ** -(torch.arange(d // 2, device="cuda").double() / (d // 2))).float()
+    pos = torch.arange(7, T + 7, device="cuda", dtype=torch.int32)
+    x, e, turned, want = _codes_of_normed_keys(P, k, kw, eps, inv, pos)
+    assert torch.isfinite(turned).all() and torch.isfinite(x).all()
+    unit = torch.exp2(e.double()).repeat_interleave(BLOCK, 0)[..., None]
+    room = grid_step(turned / unit) / 2 * unit + partners(turned, d, False) * 2.0 ** -18
+    assert ((x - turned).abs() <= room * (1 + 1e-9)).all()
+    # (the same keys as in the test of those next to a middle)
+    larger = turned.abs() >= turned.roll(d // 2, -1).abs()
+    same = (e == want.e).repeat_interleave(BLOCK, 0)[..., None]
+    counted = same & larger & (want.x.abs() >= 2.0 ** -5 * unit)
+    assert counted.sum() > 5 * 10 ** 5 and not ((x != want.x) & counted).any()
+
+
+@pytest.mark.parametrize("size", [2.0 ** 65, -2.0 ** 126, 2.0 ** -80, 1.0])
+def test_large_and_small_keys_on_the_middle_of_two_codes(size):
+    """Rows of one value come to the weight itself, 17/16: midway between two codes, to the even
+    one."""
+    P = Paged(1, 16, 2, 1, 64, 16)
+    k = torch.full((16, 1, 64), size, device="cuda", dtype=BF)
+    kw = torch.full((64,), 1.0625, device="cuda")
+    zero = torch.zeros(16, device="cuda", dtype=torch.int32)
+    x, e, _, _ = _codes_of_normed_keys(P, k, kw, 0.0, torch.ones(32, device="cuda"), zero)
+    assert (e == -8).all() and (x == (1.0 if size > 0 else -1.0)).all()
