@@ -316,8 +316,8 @@ kv8_append_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Ro
       // A key within 4 ulp of the middle between two codes is formed again in 64 bits: in fp32
       // it may have come to the wrong side. (A hundred thousandth of them. Left are those below
       // 2^-6, whose codes are 2^-9 apart, what a turn makes much smaller than its pair,
-      // which fp32 misses by more, and without a norm those on the middle itself, as
-      // 16-bit values often are that do not turn.)
+      // which fp32 misses by more, and without a norm and a turn, or at a turn of sine 0, those
+      // on the middle itself, as 16-bit values often are: they are exact.)
       unsigned long long near = 0;
 #pragma unroll
       for (int n = 0; n < TURNS; ++n) {
@@ -332,9 +332,11 @@ kv8_append_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Ro
 #pragma unroll
           for (int e = 0; e < 16; ++e) least = min(least, beside(e));
           if (least < 8 && here(n) && (N.on || rot)) {
+            const float* sn = s_tab + (n * RPT + r0) * half + 8 * u;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              if (beside(e) < 8 && (N.on || beside(e) != 4) && fabsf(x[n][e]) >= 0x1p-6f)
+              if (beside(e) < 8 && fabsf(x[n][e]) >= 0x1p-6f &&
+                  (N.on || beside(e) != 4 || sn[INTER ? e >> 1 : e & 7] != 0.0f))
                 near |= 1ull << (16 * n + e);
           }
         }

@@ -421,3 +421,22 @@ def test_large_and_small_keys_on_the_middle_of_two_codes(size):
     zero = torch.zeros(16, device="cuda", dtype=torch.int32)
     x, e, _, _ = _codes_of_normed_keys(P, k, kw, 0.0, torch.ones(32, device="cuda"), zero)
     assert (e == -8).all() and (x == (1.0 if size > 0 else -1.0)).all()
+
+
+def test_keys_on_a_middle_that_turn_a_little():
+    """A turn that fp32 rounds away, off the middle between two codes: to its side. Those that do
+    not turn go to the even code."""
+    P = Paged(1, 16, 2, 1, 64, 16)
+    k = torch.zeros(16, 1, 64, device="cuda", dtype=BF)
+    # pairs (j, 32 + j): x on a middle, y = 1 or -1; x - y 2^-30 is what is rounded
+    k[:, 0, 0:4] = torch.tensor([1.0625, 1.0625, 1.1875, 1.1875], device="cuda")
+    k[:, 0, 32:36] = torch.tensor([1.0, -1.0, 1.0, -1.0], device="cuda")
+    inv = torch.full((32,), 2.0 ** -30, device="cuda")
+    pos = torch.zeros(16, device="cuda", dtype=torch.int32)
+    pos[8:] = 1
+    gdn.gdn_kv8_append(P.dims, P.batch([0], [16], [16]), None, gdn.make_rope(64, inv, pos), None, k, k,
+                       None, P.cache.codes, P.status)
+    gdn.raise_on_status(P.status)
+    x, _ = P.tokens(0, 16, P.cache.k, P.cache.k_exp)
+    assert x[0, 0, :4].tolist() == [1.0, 1.0, 1.25, 1.25] and (x[:8] == x[0]).all()
+    assert x[8, 0, :4].tolist() == [1.0, 1.125, 1.125, 1.25] and (x[8:] == x[8]).all()
