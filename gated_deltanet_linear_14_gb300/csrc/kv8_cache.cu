@@ -118,8 +118,12 @@ __device__ __forceinline__ float exact_key(const T* row, int d, int d2, bool fir
     if (d2 >= 0) y *= inv * weight(d2);
   }
   if (d2 >= 0) {
-    double t = (double)pos * (double)f * 0.15915494309189533577, sn, cs;  // in turns
-    t -= rint(t);
+    // In turns. f / (2 pi) as a sum of two values: the position's 31 bits times the upper's 53
+    // leave their rounding error for the lower part, and whole turns drop out in between.
+    constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
+    const double fd = (double)f, p = (double)pos, fh = fd * kHi;
+    const double fl = __fma_rn(fd, kLo, __fma_rn(fd, kHi, -fh)), th = p * fh;
+    double t = th - rint(th) + __fma_rn(p, fl, __fma_rn(p, fh, -th)), sn, cs;
     sincospi(t + t, &sn, &cs);
     x = first ? x * cs - y * sn : x * cs + y * sn;
   }

@@ -4,6 +4,8 @@ A stored value is its value rounded once to the grid of its block: half a grid s
 what fp32 does to a key (2^-18 of its pair, see test_gpu_norm_rope.py). Values (v) see no arithmetic and
 are exact. A block's exponent is the least that holds its largest value; a key's block may come out
 one higher or lower only where its largest value is within 2^-18 of the limit."""
+import math
+
 import pytest
 import torch
 
@@ -440,3 +442,45 @@ def test_keys_on_a_middle_that_turn_a_little():
     x, _ = P.tokens(0, 16, P.cache.k, P.cache.k_exp)
     assert x[0, 0, :4].tolist() == [1.0, 1.0, 1.25, 1.25] and (x[:8] == x[0]).all()
     assert x[8, 0, :4].tolist() == [1.0, 1.125, 1.125, 1.25] and (x[8:] == x[8]).all()
+
+
+def test_keys_at_far_positions_next_to_the_middle_of_two_codes():
+    """Positions next to 2^31: the turn is formed with all of the position's bits, so the codes are
+    those of whole-number arithmetic."""
+    T, d, hkv = 16384, 128, 4
+    P = Paged(1, T, 4, hkv, d, 64, seed=23)
+    g = torch.Generator(device="cuda").manual_seed(8)
+    k = torch.randn(T, hkv, d, generator=g, device="cuda").to(BF)
+    inv = torch.exp2(-torch.rand(d // 2, generator=g, device="cuda"))
+    pos = (2 ** 31 - 1 - torch.randint(0, 10 ** 6, (T,), generator=g, device="cuda")).int()
+    gdn.gdn_kv8_append(P.dims, P.batch([0], [T], [T]), None, gdn.make_rope(d, inv, pos), None, k, k,
+                       None, P.cache.codes, P.status)
+    gdn.raise_on_status(P.status)
+    # whole turns out of the product in whole numbers: f = n 2^-24, and 2^120 / (2 pi) (pi by
+    # Machin's formula)
+    def arctan_of(x, one):
+        s = term = one // x
+        n, sign = 3, -1
+        while term:
+            term //= x * x
+            s, n, sign = s + sign * (term // n), n + 2, -sign
+        return s
+
+    one = 1 << 160
+    pi = 4 * (4 * arctan_of(5, one) - arctan_of(239, one))
+    turn = (1 << 120) * one // (2 * pi)
+    ns = [int(f * 2 ** 24) for f in inv.double().tolist()]
+    assert all(n / 2 ** 24 == f for n, f in zip(ns, inv.double().tolist()))
+    frac = [[(p * n * turn & (1 << 144) - 1) / (1 << 144) for n in ns] for p in pos.tolist()]
+    angle = torch.tensor(frac, dtype=torch.float64, device="cuda")[:, None] * (2 * math.pi)
+    c, s = torch.cos(angle), torch.sin(angle)
+    a, b = k[..., :d // 2].double(), k[..., d // 2:].double()
+    turned = torch.cat((a * c - b * s, b * c + a * s), -1)
+    want = Blocks(hkv, d)
+    want.append(turned, 0)
+    x, e = P.tokens(0, T, P.cache.k, P.cache.k_exp)
+    unit = torch.exp2(e.double()).repeat_interleave(BLOCK, 0)[..., None]
+    larger = turned.abs() >= turned.roll(d // 2, -1).abs()
+    same = (e == want.e).repeat_interleave(BLOCK, 0)[..., None]
+    counted = same & larger & (want.x.abs() >= 2.0 ** -5 * unit)
+    assert counted.sum() > 10 ** 6 and not ((x != want.x) & counted).any()
