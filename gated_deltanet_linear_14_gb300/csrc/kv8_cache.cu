@@ -230,7 +230,7 @@ kv8_append_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Ro
               inv = inv_rms([&](float scale) {
                 const float s = unit_squares(a[n], b[n], scale);
                 return lanes_sum(on ? s : 0.0f, U);
-              }, D, N.eps);
+              }, [&](float s) { scale_unit(a[n], b[n], s); }, D, N.eps);
             if (!on) continue;
             turn.apply(a[n], b[n], inv);
             a[n].store(dst + h * D + ea), b[n].store(dst + h * D + eb);
@@ -274,7 +274,7 @@ kv8_append_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Ro
           if (N.on)
             inv = inv_rms([&](float scale) {
               return lanes_sum(unit_squares(a[n], b[n], scale), U);
-            }, D, N.eps);
+            }, [&](float s) { scale_unit(a[n], b[n], s); }, D, N.eps);
           if (!here(n)) inv = 0.0f;
           UnitTurn<8, INTER> turn;
           const int at = min(n * RPT + r0, kKv8Block - 1) * half + 8 * u;

@@ -1,6 +1,8 @@
 // What the norms of query and key heads share (norm_rope.cu, kv8_cache.cu).
 #pragma once
 
+#include <type_traits>
+
 #include "attn.cuh"
 
 namespace gdn {
@@ -28,16 +30,20 @@ __device__ __forceinline__ float lanes_sum(float v, int P) {
 
 // 1 / sqrt(mean x^2 + eps), from squares(scale) = sum (scale x)^2 over the row's
 // lanes. By all lanes of a warp: where a row's squares leave fp32's range (or lose
-// bits that eps does not cover), they are formed again of scaled values.
-template <class F>
-__device__ __forceinline__ float inv_rms(F squares, int D, float eps) {
+// bits that eps does not cover), they are formed again of scaled values. The result
+// for a small row may have no place in that range either: scale_up multiplies its x
+// by 2^90, exactly, and the result is theirs. (The others' by 1, which is faster than a
+// branch: 86.8 us against 88.0 for 22 k rows of 40 heads x 128, bf16.)
+template <class F, class G>
+__device__ __forceinline__ float inv_rms(F squares, G scale_up, int D, float eps) {
   const float ss = squares(1.0f), n = 1.0f / (float)D;
   const bool big = !(ss <= 3.0e38f), small = ss < 1.0e-26f && eps < 1.0e-20f;
   float inv = rsqrtf(ss * n + eps);  // (within 2^-22)
   if (__any_sync(~0u, big || small)) {
-    const float scale = big ? 0x1p-70f : 0x1p70f;
-    const float again = scale * rsqrtf(squares(scale) * n + eps * scale * scale);
-    if (big || small) inv = again;
+    const float scale = big ? 0x1p-70f : 0x1p90f;
+    scale_up(small ? scale : 1.0f);
+    const float again = rsqrtf(squares(small ? 1.0f : scale) * n + eps * scale * scale);
+    if (big || small) inv = small ? again : scale * again;
   }
   return inv;
 }
@@ -69,6 +75,26 @@ __device__ __forceinline__ float unit_squares(const Vec<T, VEC>& a, const Vec<T,
     s = __ffma2_rn(x, x, s);
   }
   return s.x + s.y;
+}
+
+// A unit of a small row times s, a power of two. (Such fp16 rows are zero.)
+template <class T, int VEC>
+__device__ __forceinline__ void scale_unit(Vec<T, VEC>& a, Vec<T, VEC>& b, float s) {
+  if constexpr (std::is_same<T, bf16>::value && VEC % 2 == 0) {
+    const __nv_bfloat162 ss = __float2bfloat162_rn(s);
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) {
+      __nv_bfloat162 &x = reinterpret_cast<__nv_bfloat162&>(a.e[e]),
+                     &y = reinterpret_cast<__nv_bfloat162&>(b.e[e]);
+      x = __hmul2(x, ss), y = __hmul2(y, ss);
+    }
+  } else if constexpr (!std::is_same<T, __half>::value) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      elem_from_f(elem_to_f(a.e[e]) * s, a.e[e]);
+      elem_from_f(elem_to_f(b.e[e]) * s, b.e[e]);
+    }
+  }
 }
 
 // VEC values rounded to T, two at a time where T has 16 bits.

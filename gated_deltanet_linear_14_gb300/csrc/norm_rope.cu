@@ -87,7 +87,8 @@ norm_rope_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Rop
           const float s = unit_squares(a[n], b[n], scale);  // (no branch: heads overlap)
           return lanes_sum(on ? s : 0.0f, P);
         };
-        const float inv = inv_rms(squares, D, N.eps);
+        const float inv =
+            inv_rms(squares, [&](float s) { scale_unit(a[n], b[n], s); }, D, N.eps);
         if (!on) continue;
         if (h >= C.Hq && !for_k) turn_for(h, lane_u);
         turn.apply(a[n], b[n], inv);
@@ -100,22 +101,24 @@ norm_rope_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Rop
       for (int n = 0; n < kNormHeads; ++n) {
         const int h = h0 + n * TY + ty;
         const bool on = here && h < H;
+        float up = 1.0f;  // of the elements, which are loaded again each time
         auto squares = [&](float scale) {
           float s = 0.0f;
           for (int u = lane_u; on && u < U; u += P) {
             Vec<T, VEC> va, vb;
             va.load(src_of(h) + first(u));
             vb.load(src_of(h) + second(u));
-            s += unit_squares(va, vb, scale);
+            s += unit_squares(va, vb, scale * up);
           }
           return lanes_sum(s, P);
         };
-        const float inv = inv_rms(squares, D, N.eps);
+        const float inv = inv_rms(squares, [&](float s) { up = s; }, D, N.eps);
         for (int u = lane_u; on && u < U; u += P) {
           Vec<T, VEC> va, vb;
           va.load(src_of(h) + first(u));
           vb.load(src_of(h) + second(u));
           turn_for(h, u);
+          if (up != 1.0f) scale_unit(va, vb, up);
           turn.apply(va, vb, inv);
           va.store(dst_of(h) + first(u));
           vb.store(dst_of(h) + second(u));

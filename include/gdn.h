@@ -646,8 +646,8 @@ typedef struct {
 /* Norm query and key rows head by head, then rotate them as gdn_rope does
  * (rope NULL: they are normed only), in one pass: fp32 throughout, rounded once.
  * Arguments, types, alignments, in-place outputs and limits as gdn_rope; the mean
- * of squares is formed in fp32 (of rows scaled down where the squares leave its
- * range). A row that holds an infinite or NaN value gives NaN there and what the
+ * of squares is formed in fp32 (of rows scaled by a power of two where the squares
+ * leave its range). A row that holds an infinite or NaN value gives NaN there and what the
  * formula gives elsewhere (0 beside an infinite one, NaN beside a NaN). One launch
  * on `stream`. */
 gdn_status gdn_norm_rope(const gdn_attn_dims* dims, const gdn_head_norm* norm,

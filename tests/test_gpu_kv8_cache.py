@@ -484,3 +484,28 @@ def test_keys_at_far_positions_next_to_the_middle_of_two_codes():
     same = (e == want.e).repeat_interleave(BLOCK, 0)[..., None]
     counted = same & larger & (want.x.abs() >= 2.0 ** -5 * unit)
     assert counted.sum() > 10 ** 6 and not ((x != want.x) & counted).any()
+
+
+@pytest.mark.parametrize("d", [64, 256])
+def test_keys_below_the_normal_range_without_eps(d):
+    """Their size has no fp32 reciprocal."""
+    T = 50
+    P = Paged(1, T, 2, 2, d, 64)
+    q, k, v = (x.clone() for x in rows_for(P, T, spread=0.0))
+    q, k = (q.float() * 1e-39).to(BF), (k.float() * 1e-40).to(BF)
+    k[:, 1] = v[:, 1]
+    inv = (1e4 ** -(torch.arange(d // 2, device="cuda").double() / (d // 2))).float()
+    pos = torch.arange(T, device="cuda", dtype=torch.int32)
+    out = torch.empty_like(q)
+    gdn.gdn_kv8_append(P.dims, P.batch([0], [T], [T]), gdn.make_head_norm(eps=0.0),
+                       gdn.make_rope(d, inv, pos), q, k, v, out, P.cache.codes, P.status)
+    gdn.raise_on_status(P.status)
+    turned = rotated(normed(k, None, 0.0, 0.0), d, inv, pos)
+    x, e = P.tokens(0, T, P.cache.k, P.cache.k_exp)
+    unit = torch.exp2(e.double()).repeat_interleave(BLOCK, 0)[:T, :, None]
+    room = grid_step(turned / unit) / 2 * unit + partners(turned, d, False) * 2.0 ** -18
+    assert ((x - turned).abs() <= room * (1 + 1e-9)).all()
+    yq = normed(q, None, 0.0, 0.0)
+    want = rotated(yq, d, inv, pos)
+    assert ((out.double() - want).abs() <= want.abs() * 2.0 ** -8 * (1 + 2.0 ** -10)
+            + partners(yq, d, False) * 2.0 ** -18).all()

@@ -124,3 +124,17 @@ def test_captured_and_replayed_with_other_rows():
     qkv.copy_(qkv.flip(0))
     graph.replay()
     check(out, q, qw, 1e-6, 1.0, 64, inv, pos)
+
+
+@pytest.mark.parametrize("dtype,d,size", [(BF, 128, 1e-39), (BF, 1024, 1e-40), (F32, 128, 1e-39),
+                                          (F32, 64, 1e-43), (F32, 1024, 1e-41), (HF, 128, 1e-7)])
+def test_rows_below_the_normal_range_without_eps(dtype, d, size):
+    """Their size has no fp32 reciprocal."""
+    qkv, qw, kw, inv, pos, _ = made(8, 4, 1, d, d, F32)
+    dims = gdn.make_attn_dims(4, 1, d, 16, io=CODE[dtype])
+    q = (qkv[:, :4] * size).to(dtype)
+    q[:, 1] = (qkv[:, 1]).to(dtype)   # (a row of ordinary size beside them)
+    out = torch.empty(8, 4, d, device="cuda", dtype=dtype)
+    gdn.gdn_norm_rope(dims, gdn.make_head_norm(qw, eps=0.0), gdn.make_rope(d, inv, pos[0]), q, out)
+    assert torch.isfinite(out).all()
+    check(out, q, qw, 0.0, 0.0, d, inv, pos)
