@@ -3,6 +3,8 @@
 // and nothing written.
 #include <cuda.h>
 
+#include <algorithm>
+
 #include "attn_checks.h"
 #include "attn_plan.cuh"
 #include "gdn.h"
@@ -61,8 +63,10 @@ Wide wide_layout(const AttnDims& A, const KvBatch& B, size_t at) {
   Wide w{};
   const long long pages = (long long)B.R * B.max_pages;
   const long long page = 2LL * A.Hkv * A.ps * A.D;  // bytes, of keys or values
+  // (the rows that requests can have: row buffers may be larger)
+  const long long rows = std::min<long long>(B.num_rows, (long long)B.R * B.max_rows);
   w.bytes = at;
-  if (B.R == 0 || pages == 0 || (long long)B.num_rows * A.G < kWidePairs * B.R ||
+  if (B.R == 0 || pages == 0 || rows * A.G < kWidePairs * B.R ||
       pages > kMostCopies / (2 * page))
     return w;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };

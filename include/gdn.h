@@ -701,11 +701,11 @@ gdn_status gdn_kv8_read(const gdn_attn_dims* dims, const gdn_kv_batch* batch,
  * parts that together hold it (2 parts in bf16, 3 in fp16: within 2^-17 of the row's
  * largest element), and so are the probabilities (within 2^-7 + 2^-10 of each in bf16,
  * 2^-10 in fp16, and 2^-27 of the largest). Steps of long prompts, at least 1024
- * (row, query head) pairs per key/value head and request (num_rows * Hq / Hkv >= 1024 *
- * num_requests) whose copies take no more than 1 GiB (num_requests * max_pages
- * pages of 16-bit keys and values, in the workspace), bring their pages to 16 bits first:
- * there probabilities are rounded to the io dtype, and in fp16 keys and values are what
- * gdn_kv8_read gives. */
+ * (row, query head) pairs per key/value head and request (min(num_rows, num_requests *
+ * max_rows) * Hq / Hkv >= 1024 * num_requests) whose copies take no more than 1 GiB
+ * (num_requests * max_pages pages of 16-bit keys and values, in the workspace), bring
+ * their pages to 16 bits first: there probabilities are rounded to the io dtype, and in
+ * fp16 keys and values are what gdn_kv8_read gives. */
 size_t gdn_kv8_attn_plan_bytes(const gdn_attn_dims* dims, const gdn_kv_batch* batch);
 size_t gdn_kv8_attn_workspace_bytes(const gdn_attn_dims* dims, const gdn_kv_batch* batch);
 gdn_status gdn_kv8_attn_plan(const gdn_attn_dims* dims, const gdn_kv_batch* batch, void* plan,

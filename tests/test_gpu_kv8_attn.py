@@ -464,3 +464,18 @@ def test_one_request_over_all_blocks(n, rows):
     o, lse = attend(P, P.batch([0], [rows], [n]), q)
     gdn.raise_on_status(P.status)
     check(P, q, o, lse, [0], [rows], [n])
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_few_rows_in_a_large_buffer(dtype):
+    """What a request can have counts, not the buffer: nothing is brought to 16 bits."""
+    P = Paged(2, 700, 16, 2, 128, 32, dtype, seed=3)
+    fill(P)
+    batch = P.batch([0, 1], [1, 3], [700, 200], rows=2048, max_rows=3)
+    assert (gdn.gdn_kv8_attn_workspace_bytes(P.dims, batch)
+            == gdn.gdn_attn_workspace_bytes(P.dims, batch))
+    q = queries(P, 2048, dtype)
+    o, lse = attend(P, batch, q)
+    gdn.raise_on_status(P.status)
+    check(P, q, o, lse, [0, 1], [1, 3], [700, 200])
+    assert (o[4:] == 7).all() and (lse[4:] == 7).all()

@@ -192,6 +192,21 @@ def test_attn_buffers_refused(lib):
     assert call_attn(lib, b=batch(num_requests=0)) == OK
 
 
+def test_copies_are_for_steps_of_many_rows_a_request(lib):
+    """By the rows that the requests can have, not by the size of the row buffers."""
+    def sizes(n, rows, most):
+        d, b = dims(), batch(num_requests=n, num_rows=rows, max_rows=most, max_pages=100)
+        return [size(R(d), R(b))
+                for size in (lib.gdn_attn_workspace_bytes, lib.gdn_kv8_attn_workspace_bytes)]
+
+    for n, rows, most in ((1, 4096, 1), (4, 4096, 8), (1, 1 << 20, 255), (8, 1 << 20, 255)):
+        plain, codes8 = sizes(n, rows, most)
+        assert plain == codes8 > 0, (n, rows, most)
+    for n, rows, most in ((1, 256, 256), (8, 2048, 2048), (8, 1 << 20, 256)):
+        plain, codes8 = sizes(n, rows, most)
+        assert codes8 > plain + 2 * n * 100 * 2 * 8 * 64 * 128 - 1, (n, rows, most)
+
+
 def test_structs_match_the_header(tmp_path):
     cc = shutil.which("gcc") or shutil.which("cc")
     if cc is None:
