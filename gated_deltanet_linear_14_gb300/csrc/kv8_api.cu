@@ -52,6 +52,8 @@ gdn_status check_kv8_dims(const gdn_attn_dims* d) {
 // 8192 shared keys, us with against without: 32/8 heads x 128 787 and 1030, in fp16 810 and
 // 1271, x 64 653 and 994, 16/2 heads x 256 876 and 918; 16 x 64..512 rows, 64.7 and 74.0). The
 // copies may take what the requests' tables hold, twice the cache's bytes: up to kMostCopies.
+// A workspace without room for them (made for more requests of fewer rows, say) is no error:
+// the step goes over the codes.
 constexpr long long kWidePairs = 1024, kMostCopies = 1LL << 30;
 
 struct Wide {
@@ -212,15 +214,16 @@ gdn_status gdn_kv8_attn(const gdn_attn_dims* dims, const gdn_kv_batch* batch, co
   if ((((uintptr_t)plan | (uintptr_t)workspace) & 15) != 0) return GDN_ERR_INVALID_ARG;
   if (!stride_ok(q_stride, dims->num_q_heads, dims->head_dim)) return GDN_ERR_INVALID_ARG;
   if ((((uintptr_t)q | (uintptr_t)o) & 15) != 0 || q_stride % 8 != 0) return GDN_ERR_UNSUPPORTED;
-  if (workspace_bytes < gdn_kv8_attn_workspace_bytes(dims, batch)) return GDN_ERR_WORKSPACE;
-  if (batch->num_pages == 0) return GDN_ERR_INVALID_ARG;
   const AttnDims A = attn_dims(dims);
   KvBatch B = kv_batch(batch);
+  const size_t least = attn_layout(A, B).ws_bytes;
+  if (workspace_bytes < least) return GDN_ERR_WORKSPACE;
+  if (batch->num_pages == 0) return GDN_ERR_INVALID_ARG;
   const int box = A.ps < kAttnKeys ? A.ps : kAttnKeys, tokens = A.Hkv * A.ps;
   const Kv8Cache K = cache_args(cache);
   CUtensorMap tk, tv;
-  const Wide w = wide_layout(A, B, attn_layout(A, B).ws_bytes);
-  if (w.on) {
+  const Wide w = wide_layout(A, B, least);
+  if (w.on && workspace_bytes >= w.bytes) {
     char* ws = (char*)workspace;
     int32_t* table = (int32_t*)(ws + w.table);
     const int pages = B.R * B.max_pages;

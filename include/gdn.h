@@ -705,7 +705,10 @@ gdn_status gdn_kv8_read(const gdn_attn_dims* dims, const gdn_kv_batch* batch,
  * max_rows) * Hq / Hkv >= 1024 * num_requests) whose copies take no more than 1 GiB
  * (num_requests * max_pages pages of 16-bit keys and values, in the workspace), bring
  * their pages to 16 bits first: there probabilities are rounded to the io dtype, and in
- * fp16 keys and values are what gdn_kv8_read gives. */
+ * fp16 keys and values are what gdn_kv8_read gives. gdn_kv8_attn_workspace_bytes counts
+ * the copies, so it may be larger for fewer requests with as many rows; a workspace of
+ * gdn_attn_workspace_bytes or more is taken, and one without room for the copies has the
+ * step go over the codes. */
 size_t gdn_kv8_attn_plan_bytes(const gdn_attn_dims* dims, const gdn_kv_batch* batch);
 size_t gdn_kv8_attn_workspace_bytes(const gdn_attn_dims* dims, const gdn_kv_batch* batch);
 gdn_status gdn_kv8_attn_plan(const gdn_attn_dims* dims, const gdn_kv_batch* batch, void* plan,

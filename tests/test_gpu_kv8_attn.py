@@ -479,3 +479,21 @@ def test_few_rows_in_a_large_buffer(dtype):
     gdn.raise_on_status(P.status)
     check(P, q, o, lse, [0, 1], [1, 3], [700, 200])
     assert (o[4:] == 7).all() and (lse[4:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_a_long_prompt_without_room_for_copies(dtype):
+    """Its step goes over the codes, and nothing is written past the workspace."""
+    lens, kv = [300, 200], [700, 200]
+    P = Paged(2, 700, 16, 2, 128, 32, dtype, seed=3)
+    fill(P)
+    batch, q = P.batch([0, 300], lens, kv), queries(P, 500, dtype)
+    plan, ws = planned(P, batch)
+    least = gdn.gdn_attn_workspace_bytes(P.dims, batch)
+    for size in (least, ws.numel() - 1):
+        store = torch.full((size + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+        o, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+        gdn.gdn_kv8_attn(P.dims, batch, plan, q, P.cache.codes, o, lse, store, size, P.status)
+        gdn.raise_on_status(P.status)
+        check(P, q, o, lse, [0, 300], lens, kv)
+        assert (store[least:] == 0x5A).all()

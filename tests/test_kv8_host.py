@@ -207,6 +207,15 @@ def test_copies_are_for_steps_of_many_rows_a_request(lib):
         assert codes8 > plain + 2 * n * 100 * 2 * 8 * 64 * 128 - 1, (n, rows, most)
 
 
+def test_a_workspace_without_room_for_copies_is_taken(lib):
+    d, b = dims(), batch(num_requests=1, num_rows=2048, max_rows=2048, max_pages=100)
+    least = lib.gdn_attn_workspace_bytes(R(d), R(b))
+    assert least < lib.gdn_kv8_attn_workspace_bytes(R(d), R(b))
+    assert call_attn(lib, b=b, n=least - 1) == WORKSPACE
+    if not torch.cuda.is_available():   # (host memory is passed on to the launch)
+        assert call_attn(lib, b=b, n=least) not in (WORKSPACE, INVALID, UNSUPPORTED)
+
+
 def test_structs_match_the_header(tmp_path):
     cc = shutil.which("gcc") or shutil.which("cc")
     if cc is None:
