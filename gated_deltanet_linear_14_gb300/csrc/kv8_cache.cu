@@ -499,11 +499,9 @@ kv8_read_kernel(const __grid_constant__ RopeCall C, const __grid_constant__ Attn
 template <class T, int D>
 __global__ void __launch_bounds__(kKv8Threads, 8)
 kv8_widen_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ KvBatch B,
-                 const __grid_constant__ Kv8Cache K, T* k_out, T* v_out, int32_t* table, int packed,
+                 const __grid_constant__ Kv8Cache K, T* k_out, T* v_out, int32_t* table,
                  int32_t* status) {
   constexpr int U = D / 16;  // lanes a token and head
-  extern __shared__ float4 kv8_smem[];
-  long long* sum = reinterpret_cast<long long*>(kv8_smem);
   __shared__ int first_s;
   pdl_begin();
   const int tid = threadIdx.x;
@@ -512,7 +510,7 @@ kv8_widen_kernel(const __grid_constant__ AttnDims A, const __grid_constant__ KvB
     if (!kv_request_ok(B, A.ps, start, len, kv) || len == 0) return 0;  // (the plan reports it)
     return (kv + (long long)A.ps - 1) >> A.ps_log2;
   };
-  each_place(B, packed, sum, count, [&](int r, long long i) {
+  each_place(B, false, nullptr, count, [&](int r, long long i) {
     const long long at = (long long)r * B.max_pages + i;
     const int page = B.table[at], tokens = min(A.ps, B.kv_len[r] - ((int)i << A.ps_log2));
     if (tid == 0) first_s = r;
@@ -635,13 +633,14 @@ cudaError_t launch_kv8_widen(const AttnDims& A, const KvBatch& B, int io, const 
                              void* k_out, void* v_out, int32_t* table, int32_t* status,
                              cudaStream_t s) {
   const int units = A.Hkv * A.ps * (A.D / 16);
+  // (a row of the grid per request: the copies bound the table's entries)
   const Grid g = grid_for(B, B.max_pages, (long long)B.R * B.max_pages,
                           units / kKv8Threads / 4, 64);
   auto by_dim = [&](auto t) {
     using T = decltype(t);
     auto run = [&](auto kernel) {
-      return launch_pdl(kernel, g.dim, dim3(kKv8Threads), g.sum_bytes, s, A, B, K, (T*)k_out,
-                        (T*)v_out, table, g.packed, status);
+      return launch_pdl(kernel, g.dim, dim3(kKv8Threads), 0, s, A, B, K, (T*)k_out, (T*)v_out,
+                        table, status);
     };
     if (A.D == 64) return run(kv8_widen_kernel<T, 64>);
     if (A.D == 128) return run(kv8_widen_kernel<T, 128>);
