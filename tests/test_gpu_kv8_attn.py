@@ -497,3 +497,153 @@ def test_a_long_prompt_without_room_for_copies(dtype):
         gdn.raise_on_status(P.status)
         check(P, q, o, lse, [0, 300], lens, kv)
         assert (store[least:] == 0x5A).all()
+
+
+# Steps for each of the kernels, 8 query and 2 key heads: few pairs as columns; 128 pairs as rows, of
+# which an item fills a quarter, half or all (so many threads cut a row of q); groups that share; long
+# prompts through 16 bits.
+KINDS = ["one", "few", "quarter", "half", "whole", "shared", "widened"]
+
+
+def step_of(kind, d=128, dtype=BF, seed=0, ps=32, scale=0.0):
+    """(cache, batch, starts, rows, lengths) of a step of this kind."""
+    rows = {"one": 1, "few": 3, "quarter": 7, "half": 16, "whole": 40, "shared": 2, "widened": 300}[kind]
+    R, shared = (20, 1024) if kind == "shared" else (2, 0)
+    lens = [rows] * R
+    kv = [shared + rows + 211 + (37 * r) % 100 for r in range(R)]
+    P = Paged(R, max(kv), 8, 2, d, ps, dtype, seed=seed)
+    P.dims = gdn.make_attn_dims(8, 2, d, ps, io=P.dims.io_dtype, scale=scale)
+    fill(P, seed=seed)
+    n = shared // ps
+    P.table[:, :n] = P.table[0, :n].clone()
+    start = [rows * r for r in range(R)]
+    groups = (i32([0]), i32([R]), i32([n])) if shared else ()
+    return P, P.batch(start, lens, kv, groups=groups), start, lens, kv
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 128), (HF, 128), (BF, 256), (HF, 256)])
+@pytest.mark.parametrize("apart", [0, 5, 10, 50])
+def test_exponents_apart_in_every_kernel(kind, dtype, d, apart):
+    """Blocks whose scales differ by up to 2^apart either way, values and (up to 2^12) keys. In fp16
+    the values stay below 448, for the outputs' sake, and a step that is brought to 16 bits holds
+    what fp16 does."""
+    if kind == "widened" and dtype is HF and apart > 0:
+        pytest.skip("values beyond fp16's normal range")
+    P, batch, start, lens, kv = step_of(kind, d, dtype, seed=apart)
+    g = torch.Generator(device="cuda").manual_seed(apart)
+    top = apart if dtype is BF else 0
+
+    def between(e, lo, hi):
+        return torch.randint(max(lo, -60), hi + 1, e.shape, generator=g, device="cuda").to(torch.int8)
+
+    if apart:
+        P.cache.v_exp.copy_(between(P.cache.v_exp, top - 2 * apart, top))
+        P.cache.k_exp.copy_(between(P.cache.k_exp, -min(apart, 12) - 6, -6))
+    q = queries(P, sum(lens), dtype, seed=apart, spread=0.3)
+    o, lse = attend(P, batch, q)
+    gdn.raise_on_status(P.status)
+    check(P, q, o, lse, start, lens, kv, only=(0, 1, len(lens) - 1))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("end,beyond,size", [((-60, 60), (-128, 127), 1.0),
+                                             ((60, -60), (61, -61), 2.0 ** -66)])
+def test_exponents_beyond_the_range_in_every_kernel(kind, end, beyond, size):
+    P, batch, start, lens, kv = step_of(kind)
+    q = (queries(P, sum(lens), BF).float() * size).to(BF)
+    got = []
+    for k_exp, v_exp in (end, beyond):
+        P.cache.k_exp.fill_(k_exp)
+        P.cache.v_exp.fill_(v_exp)
+        got.append(attend(P, batch, q))
+    gdn.raise_on_status(P.status)
+    (o, lse), (o2, lse2) = got
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all() and (o != 0).any()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_strange_queries_in_every_kernel(kind, dtype):
+    """Small, zero, large, infinite and NaN rows beside one another, and one with an outlier: each
+    by itself."""
+    P, batch, start, lens, kv = step_of(kind, dtype=dtype)
+    t = sum(lens)
+    q = queries(P, t, dtype)
+    bad = torch.zeros(t, 8, dtype=torch.bool, device="cuda")
+    for r in {0, t // 2, t - 1}:
+        q[r, 0] *= 1e-30 if dtype is BF else 1e-6
+        q[r, 1] = 0.0
+        q[r, 2] *= 20.0
+        q[r, 3, 3], q[r, 4, 4] = float("inf"), float("nan")
+        q[r, 5, 5] = 60.0
+        bad[r, 3] = bad[r, 4] = True
+    o, lse = attend(P, batch, q)
+    assert torch.equal(o.isnan().all(-1), bad) and torch.equal(o.isnan().any(-1), bad)
+    assert torch.equal(lse.isnan(), bad)
+    q2 = q.clone()
+    q2[bad] = 1.0
+    o2, lse2 = attend(P, batch, q2)
+    gdn.raise_on_status(P.status)
+    assert torch.equal(o2[~bad], o[~bad]) and torch.equal(lse2[~bad], lse[~bad])
+    check(P, q2, o2, lse2, start, lens, kv, only=(0, len(lens) // 2, len(lens) - 1))
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("rows", [1, 3, 7, 40, 300])
+def test_small_probabilities_in_every_kernel(dtype, rows):
+    """One key far above 20 000 equal ones, as in the test of a single row."""
+    n = 20001
+    P = Paged(1, n, 8, 2, 64, 256, dtype)
+    P.cache.k.copy_(torch.zeros(P.cache.k.shape, device="cuda"))
+    P.cache.v.copy_(torch.ones(P.cache.v.shape, device="cuda"))
+    for e in (P.cache.k_exp, P.cache.v_exp):
+        e.fill_(0)
+    page = int(P.table[0, 0])
+    P.cache.k.view(torch.uint8)[page, :, 0] = 0x38   # 1
+    P.cache.v.view(torch.uint8)[page, :, 0] = 0x00
+    for s in (8.0, 14.0):
+        q = torch.full((rows, 8, 64), s / 8, device="cuda", dtype=dtype)
+        o, lse = attend(P, P.batch([0], [rows], [n]), q)
+        check(P, q, o, lse, [0], [rows], [n])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_the_callers_scale_in_every_kernel(kind):
+    P, batch, start, lens, kv = step_of(kind, d=64, scale=0.5)
+    q = queries(P, sum(lens), BF)
+    o, lse = attend(P, batch, q)
+    check(P, q, o, lse, start, lens, kv, only=(0, len(lens) - 1), scale=0.5)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_bad_page_in_every_kernel(kind):
+    P, batch, start, lens, kv = step_of(kind)
+    P.table[1, kv[1] // 32 - 2] = 10 ** 6   # (of its own pages)
+    q = queries(P, sum(lens), BF)
+    o, lse = attend(P, batch, q)
+    assert P.status.item() == gdn.CODES["GDN_DEV_BAD_PAGE"]
+    check(P, q, o, lse, start, lens, kv, only=[r for r in (0, 2, 19) if r < len(lens)])
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_nan_codes_behind_shared_pages(dtype):
+    """In a shared value: that element of all rows. In a key of a request's own: its rows."""
+    P, batch, start, lens, kv = step_of("shared", dtype=dtype)
+    q = queries(P, sum(lens), dtype)
+    o, lse = attend(P, batch, q)
+    at = lambda r, j: (int(P.table[r, j // 32]), j % 32)  # noqa: E731
+    page, slot = at(0, 100)
+    P.cache.v.view(torch.uint8)[page, 1, slot, 77] = 0xFF
+    page, slot = at(3, 1100)
+    P.cache.k.view(torch.uint8)[page, 0, slot, 9] = 0x7F
+    o2, lse2 = attend(P, batch, q)
+    gdn.raise_on_status(P.status)
+    bad = torch.zeros_like(o, dtype=torch.bool)
+    bad[:, 4:, 77] = True
+    bad[6:8, :4] = True
+    assert torch.equal(o2.isnan(), bad) and torch.equal(o2[~bad], o[~bad])
+    sees = torch.zeros_like(lse, dtype=torch.bool)
+    sees[6:8, :4] = True
+    assert torch.equal(lse2.isnan(), sees) and torch.equal(lse2[~sees], lse[~sees])
