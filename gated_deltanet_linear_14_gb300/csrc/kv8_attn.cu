@@ -9,7 +9,8 @@
 //   l = l 2^{m - m'} + sum_j 2^{-b_j} p_j,   O = O 2^{m - m'} + P V^
 // so that o = O / l: the values' scales ride in the exponent of p at the cost of an
 // addition for each block. (m is the maximum of p times the values' scale; exponents
-// lie in [-60, 60], so that l stays in fp32's range.)
+// lie in [-60, 60], so that l stays in fp32's range. Below -36 a p may leave it, and
+// its key still weigh: far_sum.)
 //
 // The codes go to the tensor cores as they are, by TMA, and both products run at the
 // 8-bit rate; the 16-bit operands are cut into parts of 8 bits whose products add up
@@ -57,11 +58,55 @@ struct Cfg8 {
   static constexpr uint32_t RING = NQ * QPART;
   static constexpr uint32_t EXPS = RING + NS * UNIT;
   static constexpr uint32_t FACTORS = EXPS + kExpSlots * 48;  // of an item's rows and the next one's
+  // Blocks of values below kP8Far are summed by themselves (far_sum). fp16 has none that weigh:
+  // its values come to exponents from -32 to 8, and zeros to -60.
+  static constexpr bool FAR = std::is_same<T, bf16>::value;
+  static constexpr uint32_t FAR_BYTES = FAR ? kAttnM * 8 : 0;
   static constexpr uint32_t BARS = FACTORS + 2 * kAttnM * 4;
-  static constexpr uint32_t BYTES = BARS + 8 * (2 * NS + 1 + 3 * NSB + kExpSlots) + 32;
+  static constexpr uint32_t BYTES = BARS + 8 * (2 * NS + 1 + 3 * NSB + kExpSlots) + 32 + FAR_BYTES;
   static_assert(BYTES <= (CTAS == 2 ? 115712 : 232448), "shared memory");
   static_assert(NS / 2 + NSB + 2 <= kExpSlots, "exponents are read before they are replaced");
 };
+
+// What the keys of blocks below kP8Far add to l: of a tile's scores below column lim at ts, with
+// the scales ex of its blocks, a row's factor and its maximum m before the tile (first: it has
+// none). Added to sum_of, the maximum that its sum goes by and the sum. Apart from the tile's own
+// pass, whose maximum is formed here once more, and called where that masks: in its registers, or
+// at a branch of its own, verification rows took 4 to 10 % longer (so 2 to 3.5 % in bf16).
+__device__ __noinline__ void far_sum(uint32_t ts, const float* ex, float factor, float m, bool first,
+                                     int lim, float2* sum_of) {
+  auto block = [&](int k, float add, float& top, float& sum) {
+    const float c = fminf(fmaxf(factor * ex[k], 0x1p-126f), 0x1p127f);
+    float most = -INFINITY;
+#pragma unroll 1
+    for (int n = 16 * k; n < 16 * k + 16; n += 8) {
+      float s[8];
+      tm_read8(ts + n, s);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (n + e >= lim) s[e] = -INFINITY;
+        most = fmaxf(most, s[e]);
+        sum += ex2(__fmaf_rn(s[e], c, add) + kP8FarUp);
+      }
+    }
+    top = fmaxf(top, __fmaf_rn(most, c, ex[4 + k]));
+  };
+  float mx = -INFINITY, l = 0.0f, unused = 0.0f;
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) block(k, -INFINITY, mx, unused);
+  if (first || mx - m > kP8Raise) m = mx;
+  const float mc = m == -INFINITY ? 0.0f : m - kP8Up;
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    const float b = ex[4 + k];
+    if (b >= (float)kP8Far) continue;
+    float sum = 0.0f;
+    block(k, b - mc, unused, sum);
+    l += sum * pow2(-(int)b - (int)kP8FarUp);
+  }
+  const float2 old = *sum_of;
+  *sum_of = make_float2(m, old.y > 0.0f ? l + lower(old.y, old.x - m) : l);
+}
 
 }  // namespace
 
@@ -78,12 +123,13 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ 
   const uint32_t full = sb + C::BARS, empty = full + 8 * NS, q_full = empty + 8 * NS;
   const uint32_t s_full = q_full + 8, p_ready = s_full + 8 * NSB, o_full = p_ready + 8 * NSB;
   const uint32_t e_full = o_full + 8 * NSB;
-  // of a tile's four blocks: 2^a, b, 2^-b
+  // of a tile's four blocks: 2^a, b, 2^-b (0 where far_sum takes the block)
   float4* exps = reinterpret_cast<float4*>(smem + C::EXPS);
   float* factors = reinterpret_cast<float*>(smem + C::FACTORS);
   // [0] tensor memory, [1] a role gave up, [2..4] see `strange`
   volatile uint32_t* words = reinterpret_cast<uint32_t*>(
       smem + C::BARS + 8 * (2 * NS + 1 + 3 * NSB + kExpSlots));
+  float2* far_of = reinterpret_cast<float2*>(smem + C::BYTES - C::FAR_BYTES);  // [kAttnM]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
@@ -155,7 +201,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ 
         float* to = reinterpret_cast<float*>(exps + 3 * s) + lane;
         e = kv8_clamp(e);
         if (lane < 8) to[0] = lane < 4 ? pow2(e) : (float)e;
-        if (lane >= 4 && lane < 8) to[4] = pow2(-e);
+        const bool far = C::FAR && lane >= 4 && lane < 8 && e < kP8Far;
+        if (lane >= 4 && lane < 8) to[4] = far ? 0.0f : pow2(-e);
         __syncwarp();
         if (lane == 0) mbar_arrive(e_full + 8 * s);
       };
@@ -436,6 +483,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ 
       const bool mixed = !group && it.m0 / A.G != (it.m0 + it.m_cnt - 1) / A.G;
 
       float m = -INFINITY, l = 0.0f;
+      if constexpr (C::FAR) far_of[tid] = make_float2(0.0f, 0.0f);
       const int tiles = W.t1 - W.t0;
       if (!(ok = wait(q_full, items & 1))) break;  // (the factors, which other warps wrote)
       const float factor = factors[(items & 1) * kAttnM + min(tid, it.m_cnt - 1)];
@@ -460,7 +508,6 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ 
         // the item's scores are complete: Q makes way for the next item's
         if (more && t + 1 == W.t1) fetch_q(N);
         if (rows_here) {
-          const bool masked = cut || nv < kAttnKeys;
           const int lim = min(seen, it.kend) - base;
           // of block k: the factor of its scores (kept finite and above 0, so that a
           // masked score stays -inf), and the values' exponent
@@ -472,9 +519,17 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ 
 #pragma unroll
             for (int k = 0; k < 4; ++k) ck[k] = fminf(fmaxf(factor * ck[k], 0x1p-126f), 0x1p127f);
           }
+          const bool far =
+              C::FAR && fminf(fminf(vk[0], vk[1]), fminf(vk[2], vk[3])) < (float)kP8Far;
+          const bool masked = cut || nv < kAttnKeys || far;  // (one branch for both)
           Cols64 x;
           tm_read64(ts, x);
           if (masked) {
+            if (far) {
+              far_sum(ts, reinterpret_cast<const float*>(ex), factor, m, t == W.t0, lim,
+                      far_of + tid);
+              tm_read64(ts, x);
+            }
 #pragma unroll
             for (int e = 0; e < 64; ++e)
               if (e >= lim) x.r[e] = 0xFF800000u;  // -inf
@@ -495,8 +550,8 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ 
           if (t == W.t0) {
             m = mx;
           } else if (__any_sync(~0u, raise)) {
-            const float f = raise ? ex2(m - mx) : 1.0f;
-            l *= f;
+            const float down = raise ? m - mx : 0.0f, f = ex2(down);
+            l = lower(l, down);
             if (raise) m = mx;
             // O is complete up to the previous tile
             if (!(ok = wait(o_full + 8 * b1, pb1))) break;
@@ -583,6 +638,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ 
       tc_fence_after();
       // whether a NaN code was taken out of a tile of this item
       const bool strange = words[2 + items % 3] != 0;
+      if (C::FAR && far_of[tid].y > 0.0f) l += lower(far_of[tid].y, far_of[tid].x - m);
       if (rows_here) {
         const bool direct = W.direct();
         const bool mine = tid < it.m_cnt;

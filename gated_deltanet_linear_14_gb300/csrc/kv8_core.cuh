@@ -20,7 +20,21 @@ template <> struct Parts<__half> {
 // by more than kP8Raise (in powers of two): p <= 2^15, the largest power of two below
 // e5m2's and fp16's limits. 16 equal scores at the maximum sum up to half of that.
 constexpr float kP8Raise = 5.0f, kP8Up = 10.0f;
+// p's least value is 2^-126, what ex2 gives. A key of a block of values far smaller than the
+// row's largest may lie below and still weigh: for l, which counts weights, p of blocks below
+// 2^kP8Far is formed once more, times 2^kP8FarUp. (Lost are weights below 2^-40 of one that
+// is counted.)
+constexpr int kP8Far = -36;
+constexpr float kP8FarUp = 40.0f;
 constexpr int kExpSlots = 16;  // tiles whose exponents are kept: more than the ring holds
+
+// l times 2^down, in two steps where ex2 has no such number: l may be as large.
+__device__ __forceinline__ float lower(float l, float down) {
+  const bool twice = down < -120.0f;
+  const float step = ex2(twice ? 0.5f * down : down);
+  l *= step;
+  return twice ? l * step : l;
+}
 
 // Byte offset of the 16-byte chunk `chunk` of row `row` in a swizzled tile.
 template <int PITCH>
@@ -67,6 +81,20 @@ __device__ __forceinline__ void tm_store16(uint32_t taddr, const uint32_t* r) {
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
       "r"(r[15])
       : "memory");
+}
+
+// Eight consecutive fp32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tm_read8(uint32_t taddr, float* v) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]),
+        "=&r"(r[6]), "=&r"(r[7])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // Bits 7, 15, 23, 31 of the result: whether the byte is a NaN code.

@@ -69,22 +69,9 @@ struct Columns {
   long long row[N];     // row * Hq + head
 };
 
-// Eight consecutive fp32 columns of this thread's TMEM lane. (What few tiles or no tile
-// needs loops over them at an address of its own: unrolled over a tile's registers its
-// code made short items wait for instructions, 120 against 53 us on 64 requests of 8
-// rows behind 1000 keys.)
-__device__ __forceinline__ void tm_read8(uint32_t taddr, float* v) {
-  uint32_t r[8];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]),
-        "=&r"(r[6]), "=&r"(r[7])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
+// (What few tiles or no tile needs loops over eight columns at an address of its own:
+// unrolled over a tile's registers its code made short items wait for instructions, 120
+// against 53 us on 64 requests of 8 rows behind 1000 keys.)
 __device__ __forceinline__ void tm_write8(uint32_t taddr, const float* v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
                "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
@@ -126,8 +113,9 @@ kv8_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
   Columns* cols = reinterpret_cast<Columns*>(smem + C::COL);
   // [2][N]: 2^(exponent + neg_tab) is at most 2^15, at present and before (or after) a raise
   float* neg_tab = reinterpret_cast<float*>(smem + C::STAT);
-  float* f_tab = neg_tab + 2 * N;                           // [2][N]: what the raise scales by
-  int* warp_max = reinterpret_cast<int*>(f_tab + 2 * N);    // [4][N]
+  float* f_tab = neg_tab + 2 * N;                           // [2][N]: what the raise scales by,
+  float* f2_tab = f_tab + 2 * N;                            // [N]: and once more
+  int* warp_max = reinterpret_cast<int*>(f2_tab + N);       // [4][N]
   float* warp_sum = reinterpret_cast<float*>(warp_max + 4 * N);  // [4][N]
   float* inv_tab = warp_sum + 4 * N;                        // [N]
   // [0] tensor memory, [1] a role gave up, [2..4] see `strange`, [5..7] votes
@@ -547,7 +535,7 @@ kv8_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
           if (!(ok = meet())) break;
           // every warp for itself, all the same, to the other half of the tables
           if (lane < N) {
-            float neg = neg_tab[cur * N + lane], f = 1.0f;
+            float neg = neg_tab[cur * N + lane], f = 1.0f, f2 = 1.0f;
             if (groups >> (lane >> 3) & 1) {
               int w = warp_max[lane];
 #pragma unroll
@@ -556,11 +544,15 @@ kv8_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
               // (each pair by itself: its rounding depends on no other)
               const float m = j == 0 ? -INFINITY : kP8Up - neg;
               const bool up = mx - m > kP8Raise;
-              if (up) f = ex2(m - mx);
+              // (in two steps where ex2 has no such number: l may be as large)
+              const bool twice = m - mx < -120.0f && mx < INFINITY && m > -INFINITY;
+              if (up) f = ex2(twice ? 0.5f * (m - mx) : m - mx);
+              if (up && twice) f2 = f;
               if (up || j == 0) neg = kP8Up - mx;
             }
             neg_tab[(cur ^ 1) * N + lane] = neg;
             f_tab[(cur ^ 1) * N + lane] = f;
+            f2_tab[lane] = f2;
           }
           __syncwarp();
           cur ^= 1;
@@ -570,6 +562,8 @@ kv8_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
             for (int n = 0; n < N; n += 4) {
               const float4 f = *reinterpret_cast<const float4*>(fs + n);
               l[n] *= f.x, l[n + 1] *= f.y, l[n + 2] *= f.z, l[n + 3] *= f.w;
+              const float4 g = *reinterpret_cast<const float4*>(f2_tab + n);
+              l[n] *= g.x, l[n + 1] *= g.y, l[n + 2] *= g.z, l[n + 3] *= g.w;
             }
             // O is complete up to the previous tile
             if (!(ok = wait(o_full + 8 * b1, pb1))) break;
@@ -580,14 +574,20 @@ kv8_few_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
               float v[8];
               tm_read8(tmem + C::TM_O + c + lane_base, v);
 #pragma unroll
-              for (int n = 0; n < 8; ++n) v[n] *= fs[c % N + n];
+              for (int n = 0; n < 8; ++n) v[n] *= fs[c % N + n] * f2_tab[c % N + n];
               tm_write8(tmem + C::TM_O + c + lane_base, v);
             }
             tmem_st_wait();
           }
         }
         if (!ok) break;
-        const float kl = pow2(-(int)ex[8]);
+        const bool far = ex[8] < kP8Far;
+        const float kl = far ? 0.0f : pow2(-(int)ex[8]);
+        if (__builtin_expect(far, 0)) {
+          const float kf = pow2(-(int)ex[8] - (int)kP8FarUp);
+#pragma unroll
+          for (int n = 0; n < N; ++n) l[n] = __fmaf_rn(ex2(t[n] + kP8FarUp), kf, l[n]);
+        }
         uint32_t p[NP * (N / 4)];
 #pragma unroll
         for (int n = 0; n < N; n += 4) {

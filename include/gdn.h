@@ -700,15 +700,18 @@ gdn_status gdn_kv8_read(const gdn_attn_dims* dims, const gdn_kv_batch* batch,
  * Both products run on the 8-bit tensor cores, exact in the codes: q is cut into
  * parts that together hold it (2 parts in bf16, 3 in fp16: within 2^-17 of the row's
  * largest element), and so are the probabilities (within 2^-7 + 2^-10 of each in bf16,
- * 2^-10 in fp16, and 2^-27 of the largest). Steps of long prompts, at least 1024
- * (row, query head) pairs per key/value head and request (min(num_rows, num_requests *
- * max_rows) * Hq / Hkv >= 1024 * num_requests) whose copies take no more than 1 GiB
- * (num_requests * max_pages pages of 16-bit keys and values, in the workspace), bring
- * their pages to 16 bits first: there probabilities are rounded to the io dtype, and in
- * fp16 keys and values are what gdn_kv8_read gives. gdn_kv8_attn_workspace_bytes counts
- * the copies, so it may be larger for fewer requests with as many rows; a workspace of
- * gdn_attn_workspace_bytes or more is taken, and one without room for the copies has the
- * step go over the codes. */
+ * 2^-10 in fp16, and 2^-27 of the largest times its value's scale). Their sum misses none
+ * above 2^-28 of another (in fp16 where the values' exponents are up to 96 apart; those of
+ * fp16 values and of zeros are within 68).
+ * Steps of long prompts, at least 1024 (row, query head) pairs per key/value head and
+ * request (min(num_rows, num_requests * max_rows) * Hq / Hkv >= 1024 * num_requests)
+ * whose copies take no more than 1 GiB (num_requests * max_pages pages of 16-bit keys and
+ * values, in the workspace), bring their pages to 16 bits first: there probabilities are
+ * rounded to the io dtype, in fp16 keys and values are what gdn_kv8_read gives, and a row
+ * with an infinite element is what gdn_attn makes of it. gdn_kv8_attn_workspace_bytes
+ * counts the copies, so it may be larger for fewer requests with as many rows; a workspace
+ * of gdn_attn_workspace_bytes or more is taken, and one without room for the copies has
+ * the step go over the codes. */
 size_t gdn_kv8_attn_plan_bytes(const gdn_attn_dims* dims, const gdn_kv_batch* batch);
 size_t gdn_kv8_attn_workspace_bytes(const gdn_attn_dims* dims, const gdn_kv_batch* batch);
 gdn_status gdn_kv8_attn_plan(const gdn_attn_dims* dims, const gdn_kv_batch* batch, void* plan,

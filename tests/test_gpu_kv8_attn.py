@@ -647,3 +647,29 @@ def test_nan_codes_behind_shared_pages(dtype):
     sees = torch.zeros_like(lse, dtype=torch.bool)
     sees[6:8, :4] = True
     assert torch.equal(lse2.isnan(), sees) and torch.equal(lse2[~sees], lse[~sees])
+
+
+@pytest.mark.parametrize("rows", [1, 3, 40])
+@pytest.mark.parametrize("n,bits,late", [(301, 8, True), (20001, 17, False), (20001, 17, True)])
+def test_weights_of_keys_whose_values_are_far_smaller(rows, n, bits, late):
+    """One key of values 2^60 among keys of values 2^-60 that weigh 2^-bits of it each, and as
+    much together as it does or a part of that: the sum counts them."""
+    R = 200 if rows < 40 else 40
+    P = Paged(1, n, 8, 2, 64, 256)
+    P.table = P.table.repeat(R, 1)   # (all requests read the same: items of many tiles)
+    P.cache.k.copy_(torch.zeros(P.cache.k.shape, device="cuda"))
+    P.cache.v.copy_(torch.ones(P.cache.v.shape, device="cuda"))
+    P.cache.k_exp.zero_()
+    P.cache.v_exp.fill_(-60)
+    at = n - 50 if late else 5
+    page, slot = int(P.table[0, at // 256]), at % 256
+    P.cache.k.view(torch.uint8)[page, :, slot] = 0x38   # 1
+    block = slot // 16
+    P.cache.v_exp[page, :, block] = 60
+    P.cache.v.view(torch.uint8)[page, :, 16 * block:16 * block + 16] = 0
+    P.cache.v.view(torch.uint8)[page, :, slot] = 0x38
+    q = torch.full((R * rows, 8, 64), bits * math.log(2) / 8, device="cuda", dtype=BF)
+    start, lens, kv = [rows * r for r in range(R)], [rows] * R, [n] * R
+    o, lse = attend(P, P.batch(start, lens, kv), q)
+    gdn.raise_on_status(P.status)
+    check(P, q, o, lse, start, lens, kv, only=(0, R // 2, R - 1))
