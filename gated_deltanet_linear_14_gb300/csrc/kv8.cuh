@@ -65,7 +65,8 @@ cudaError_t launch_kv8_widen(const AttnDims& A, const KvBatch& B, int io, const 
 // head and request, and nothing declared shared. (64 requests, 32/8 heads x 128, us there
 // against kv8_attn.cu: 1 row each behind 100, 1000 and 4000 keys 18.1, 42.2 and 91.0
 // against 21.5, 48.4 and 104.8; 4 rows each 19.9, 45.4 and 93.5 against 22.3, 52.2 and
-// 105.9; one row behind 512 9.0 against 10.1. With 32 columns the softmax's registers and code made it the slower one.)
+// 105.9; one row behind 512 9.0 against 10.1. With 32 columns a tile of 64 requests of 5 rows
+// behind 100 keys took its first softmax warp 19000 cycles, 5400 with 16.)
 bool kv8_few_pairs(const AttnDims& A, const KvBatch& B);
 // tk, tv: CUtensorMaps of the codes ([pages][Hkv * page_size][D], boxes of min(D, 128)
 // codes x min(page_size, 64) tokens, swizzled over a box's row). The plan is

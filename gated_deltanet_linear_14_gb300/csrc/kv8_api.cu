@@ -49,8 +49,9 @@ gdn_status check_kv8_dims(const gdn_attn_dims* d) {
 // them, whose products and probabilities need no parts. That pays from about 1000 (row, query
 // head) pairs per key/value head and request on (bringing a key of 128 elements there and
 // back costs 0.15 ns, a tile of 128 pairs saves 0.016 ns of a key; 4 x 1500..2048 rows behind
-// 8192 shared keys, us with against without: 32/8 heads x 128 787 and 1030, in fp16 810 and
-// 1271, x 64 653 and 994, 16/2 heads x 256 876 and 918; 16 x 64..512 rows, 64.7 and 74.0). The
+// 8192 shared keys, three steps in turn, us with against without: 32/8 heads x 128 783 and
+// 986, in fp16 813 and 1224, x 64 696 and 959, 16/2 heads x 256 881 and 913; 16 x 64..512 rows,
+// 81.1 and 97.9; with inputs of its own for each pass the first takes 840 to 850). The
 // copies may take what the requests' tables hold, twice the cache's bytes: up to kMostCopies.
 // A workspace without room for them (made for more requests of fewer rows, say) is no error:
 // the step goes over the codes.

@@ -23,11 +23,14 @@
 // Roles and buffers as in attn.cu. The fetching warp also brings the scales of the tile's
 // four blocks, as the floats that the softmax uses, to a small ring.
 //
-// What bounds it (GB300, join included): the softmax's issue, some 550 instructions a tile and
-// warp (160 of them the parts of p in bf16, 260 in fp16) against 376 over 16 bits, and
-// 640 (bf16) or 960 cycles of products per 64 keys and CTA. 64 requests of 8 rows in four
-// groups: 81 us in bf16, 92.5 in fp16 (113 with the scales taken apart by every softmax
-// thread); 96 requests of 32/4 heads x 64 behind 49152 keys: 92 us. The values brought to fp16
+// What bounds it (GB300, join included): on long tiles the softmax's issue, some 550
+// instructions a tile and warp (160 of them the parts of p in bf16, 260 in fp16) against 376
+// over 16 bits, and 640 (bf16) or 960 cycles of products per 64 keys and CTA. On verification
+// rows no unit is full (tensor pipe 41 %, issue 41 %, DRAM 15 %): requests' own keys come in
+// tiles of which a quarter of the rows is used, so that one softmax warp of four works, and
+// the products wait for it. 64 requests of 8 rows in four groups: 84 us in bf16, 93 in fp16 (113
+// with the scales taken apart by every softmax thread); 96 requests of one row, 32/4 heads x
+// 64, behind 49152 shared keys and up to 500 of their own: 97 us in bf16, 108 in fp16. The values brought to fp16
 // in shared memory by two warps of their own, one product instead of two or three, was
 // slower: 1205 against 1030 us on long prompts, 119 against 113 on the groups in fp16.
 #include <cuda.h>

@@ -7,10 +7,11 @@
 // row's heads share (weights, cosines) in its registers. Of the keys and values a warp
 // has a head's block in registers. Bound by memory (the rows, the rotated queries and
 // the codes) and the issue: per place the loads' latency, then 3 (queries) to 15 (keys)
-// instructions an element. Measured (GB300): 32768 rows of 32/8 heads x 128, fp16: 193 us, 738
-// MB at 3.8 TB/s, of which the queries by themselves take 97 us (norm_rope.cu), keys and
-// values 68 (86 us with every thread going through all heads of a row, twice); 40 requests of 8
-// to 400 rows of 16/2 heads x 256: 19 us. Reading back is a copy, two bytes written for
+// instructions an element. Measured (GB300): 32768 rows of 32/8 heads x 128, fp16: 197 us, 738
+// MB at 3.7 TB/s (the queries by themselves take 99 us in norm_rope.cu, keys and values 73
+// here, 86 with every thread going through all heads of a row twice: together they are 25 us
+// slower than one after the other); 40 requests of 8 to 400 rows of 16/2 heads x 256: 21 us.
+// Reading back is a copy, two bytes written for
 // one read: 135 k tokens of 8 heads x 128, 142 us, 5.7 TB/s, 0.85 of the copy rate.
 #include <algorithm>
 

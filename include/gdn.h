@@ -658,8 +658,11 @@ gdn_status gdn_norm_rope(const gdn_attn_dims* dims, const gdn_head_norm* norm,
 
 /* Append a step's rows to an 8-bit cache: row t of request r becomes token
  * kv_len[r] - row_len[r] + t. k is normed (norm NULL: not) and rotated (rope NULL:
- * not) and v is taken as it is; both are quantised from fp32, with one rounding (keys
- * within 4 ulp of the middle between two codes are formed again in 64 bits).
+ * not) and v is taken as it is; both are quantised from fp32, with one rounding: a key is
+ * off by half a step of its codes and 2^-18 of |x| + |y| of its pair at most. Keys that
+ * fp32 puts within 4 ulp of the middle between two codes are formed again in 64 bits, which
+ * brings them to the right one; but for those below 2^-6 2^exp, and those that a turn makes
+ * much smaller than the other of their pair, which fp32 misses by more.
  * With q (else NULL, as q_out; needs norm or rope) the query rows are normed and
  * rotated to q_out in the io dtype in the same launch.
  *   exp   of a block: the least with max |x| <= 448 * 2^exp over the block's new
